@@ -605,3 +605,9 @@ def quantize_e4m3(x: torch.Tensor, ws: torch.Tensor):
     _check(_lib.ss_quantize_e4m3(_ptr(x), x.numel(), _ptr(q), _ptr(xq), _ptr(ws), ws.numel(),
                                  _stream(dev)), "ss_quantize_e4m3")
     return q, xq
+
+
+# The operators in front of the head (include/ss_block.h).
+from .block import (  # noqa: E402
+    ACTS, HEADER_BLOCK, MAX_F, DropoutSpec, dropout, dropout_backward, ffn_backward, ffn_forward,
+    ffn_workspace, ffn_workspace_size)

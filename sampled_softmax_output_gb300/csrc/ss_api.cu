@@ -35,7 +35,7 @@ struct Layout {
   int64_t ldT8, ldC8;  // row pitch (bytes) of the transposed e4m3 / e5m2 copies
 };
 
-constexpr size_t kHdrBytes = 1024;  // int32 status, int32 U, padding, FP8 amax words
+constexpr size_t kHdrBytes = kHeaderBytes;  // int32 status, int32 U, padding, FP8 amax words
 constexpr size_t kHdrAmax = 64;     // byte offset of float amax[2] (max |H|, max |W_c|)
 constexpr size_t kHdrBar = 72;      // uint32 bar[2] of k_h_prep_beside (arrivals, gave up)
 constexpr size_t kHdrQuant = 80;    // ss_quantize_e4m3's own float amax + int32 status
@@ -713,6 +713,21 @@ void trace_post(cudaStream_t s) {
   }
   ++t.count;
 }
+
+}  // namespace
+
+int current_num_sms() { return num_sms_current(); }
+ss_status record_failure(const char* what, cudaError_t e) { return fail(what, e); }
+bool make_bf16_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
+                   uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer) {
+  return make_map(m, base, inner, outer, row_bytes, box_inner, box_outer,
+                  CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                  box_inner == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+}
+StageTrace::StageTrace(cudaStream_t s, const char* name) : s_(s) { trace_pre(s, name); }
+StageTrace::~StageTrace() { trace_post(s_); }
+
+namespace {
 
 // ------------------------------------------------- allocation-free forward
 // Scratch of ss_forward_noalloc, in the library's own device data: callers

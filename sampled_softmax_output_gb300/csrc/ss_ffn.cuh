@@ -1,0 +1,107 @@
+// ss_ffn.cuh -- what the kernels of the gated feed-forward block share: the
+// activations with their slopes, the rounding of a row of outputs, and the
+// launchers of the two families of kernels.
+//
+// The block's seven products are all of the form Out[n, m] = sum_k B[n, k] A[m, k]
+// with operands that TMA brings to shared memory as they lie (K-major, or
+// MN-major through the MMA's operand descriptor), so nothing is transposed:
+//   gate/up  G, U [T, F]  X [T, D] (K-major)      Wg, Wu [F, D] (K-major)
+//   down     Z  [T, D]    A [T, F] (K-major)      Wd [D, F] (K-major)
+//   dA       dA [T, F]    dZ [T, D] (K-major)     Wd [D, F] (MN-major)
+//   dX       dX [T, D]    dG, dU [T, F] (K-major) Wg, Wu [F, D] (MN-major)
+//   dW       dWg [F, D]   dG [T, F] (MN-major)    X [T, D] (MN-major); dWu and
+//            dWd (dZ, A) likewise
+// Two families run them: ss_ffn_pair.cu on CTA pairs with 256 x 256 tiles, and
+// ss_ffn_split.cu with smaller tiles and K split over a thread-block cluster,
+// for problems whose tiles would leave most SMs idle.
+#pragma once
+
+#include <type_traits>
+
+#include "ss_dropout.cuh"
+#include "ss_internal.h"
+#include "ss_ptx.cuh"
+
+namespace ss {
+
+// ------------------------------------------------------------- activations
+
+// sigmoid(x) = 1 / (1 + 2^(-x log2 e)): exactly 0 and 1 at the ends
+__device__ __forceinline__ float sigmoid_fast(float x) {
+  return rcp_approx(1.f + ex2_approx(-1.4426950408889634f * x));
+}
+
+// a = act(g), and (SLOPE) d = act'(g)
+template <int ACT, bool SLOPE>
+__device__ __forceinline__ void act_eval(float g, float& a, float& d) {
+  if constexpr (ACT == SS_ACT_SILU) {
+    const float s = sigmoid_fast(g);
+    a = g * s;
+    if (SLOPE) d = fmaf(a, 1.f - s, s);
+  } else if constexpr (ACT == SS_ACT_GELU) {
+    const float cdf = fmaf(0.5f, erff(g * 0.70710678118654752f), 0.5f);
+    a = g * cdf;
+    // density of the normal distribution: 2^(-g^2 log2(e) / 2) / sqrt(2 pi)
+    if (SLOPE) d = fmaf(g * 0.39894228040143268f, ex2_approx(-0.72134752044448170f * g * g), cdf);
+  } else if constexpr (ACT == SS_ACT_GELU_TANH) {
+    // (1 + tanh v) / 2 = sigmoid(2 v), 2 v = c (g + 0.044715 g^3), c = 2 sqrt(2 / pi)
+    constexpr float c = 1.5957691216057308f;
+    const float g2 = g * g;
+    const float s = sigmoid_fast(c * g * fmaf(0.044715f, g2, 1.f));
+    a = g * s;
+    // where g^2 is past 10^4, s is 0 or 1 and the factor (1 - s) a is 0: the
+    // bound keeps 0 * infinity out
+    if (SLOPE) d = fmaf(a * (1.f - s), c * fmaf(0.134145f, fminf(g2, 1e4f), 1.f), s);
+  } else {
+    a = g < 0.f ? 0.f : g;  // a NaN stays
+    if (SLOPE) d = g > 0.f ? 1.f : 0.f;
+  }
+}
+
+// fn.template operator()<ACT>() for the activation `act`
+template <class F>
+__device__ __forceinline__ void dispatch_act(int act, F&& fn) {
+  switch (act) {  // uniform
+    case SS_ACT_SILU: fn(std::integral_constant<int, SS_ACT_SILU>{}); break;
+    case SS_ACT_GELU: fn(std::integral_constant<int, SS_ACT_GELU>{}); break;
+    case SS_ACT_GELU_TANH: fn(std::integral_constant<int, SS_ACT_GELU_TANH>{}); break;
+    default: fn(std::integral_constant<int, SS_ACT_RELU>{}); break;
+  }
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// ---------------------------------------------------------------- problems
+
+struct FfnForward {
+  const uint16_t *X, *Wg, *Wu, *Wd, *residual;
+  int T, D, F, act;
+  DropArgs drop;
+  uint16_t *Y, *G, *U, *A;  // G, U null: not kept
+  int* status;
+  int num_sms;
+};
+
+struct FfnBackward {
+  const uint16_t *dZ, *X, *Wg, *Wu, *Wd, *G, *U, *A;  // dZ: dY with dropped elements zeroed
+  int T, D, F, act;
+  float scale;  // 1 / (1 - p): dZ above times this is the gradient of Z
+  int dw_fp32, accumulate;
+  uint16_t *dX, *dG, *dU;
+  void *dWg, *dWu, *dWd;
+  int* status;
+  int num_sms;
+};
+
+// y = x with the dropped elements zeroed, not scaled (ss_dropout.cu)
+cudaError_t launch_drop_mask(const uint16_t* x, int64_t n, const DropArgs& drop, uint16_t* y,
+                             int num_sms, cudaStream_t stream);
+
+// CTA pairs, 256 x 256 tiles (ss_ffn_pair.cu)
+cudaError_t pair_gate_up(const FfnForward& p, cudaStream_t s);
+cudaError_t pair_down(const FfnForward& p, cudaStream_t s);
+cudaError_t pair_grad_act(const FfnBackward& p, cudaStream_t s);  // dG, dU
+cudaError_t pair_grads(const FfnBackward& p, cudaStream_t s);     // dX, dWg, dWu, dWd
+
+}  // namespace ss

@@ -1,0 +1,696 @@
+// ss_ffn_pair.cu -- the feed-forward block's products on CTA pairs: one 2-SM
+// tcgen05.mma.cta_group::2 per 256 x 256 x 16 step, the protocol of
+// ss_gemm2.cuh over a list of jobs.
+//
+// A job is one product with up to two segments of K (dX = dG Wg + dU Wu is one
+// accumulation over 2 F), its operands' tensor maps and majors, and its tiles.
+// A launch runs one or more jobs; pair p runs the units p, p + pairs, ... of
+// all jobs' tiles in a row.
+//
+// gate/up: the two CTAs of a pair hold the two halves of the MMA's N, and here
+// the leader's half is 128 rows of Wg and the peer's 128 rows of Wu. Columns
+// 0-127 of each accumulator row are then G and 128-255 U of the same features,
+// so the epilogue has both in one thread and the activation and product need
+// no exchange.
+//
+// Roles per CTA: warp 0 TMA producer, warp 1 MMA issuer (the leader's), warps
+// 2-9 epilogue: two column groups of four warps, one accumulator row per
+// thread, two TMEM accumulators so that the epilogue of a tile runs beside the
+// MMAs of the next.
+#include <type_traits>
+
+#include "ss_ffn.cuh"
+#include "ss_gemm.cuh"
+#include "ss_gemm2.cuh"
+
+namespace ss {
+
+namespace {
+
+enum Kind { kUp, kDown, kGradAct, kGrads };
+
+constexpr int kBN = 256;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kMaxJobs = 4;
+
+struct PairJob {
+  CUtensorMap a[2], b[2];  // per segment of K (gate/up: b per CTA of the pair)
+  int kb[2];               // k-blocks of each segment
+  int a_mn, b_mn;          // 1: MN-major operand
+  int m_tiles, n_tiles;
+  int units_end;  // units of this job and of those before it
+};
+
+// The output of a job of kGrads: rows x cols of bf16 or fp32, times scale.
+struct GradOut {
+  void* out;
+  int rows, cols;
+  float scale;
+  int fp32, accumulate;
+};
+
+// Staging of 32-column chunks: 128 rows x 64 bytes, 64-byte swizzle (16-byte
+// chunk c of row r at c ^ ((r >> 1) & 3)), so that eight rows' 16-byte accesses
+// to the same chunk hit all 32 banks.
+constexpr uint32_t kChunkBytes = 128 * 64;
+__device__ __forceinline__ uint32_t chunk_addr(uint32_t buf, int row, int c) {
+  return buf + static_cast<uint32_t>(row) * 64u +
+         static_cast<uint32_t>((c ^ ((row >> 1) & 3)) * 16);
+}
+
+template <int KIND>
+struct PairCfg;
+template <>
+struct PairCfg<kUp> {
+  static constexpr int kStages = 5, kBufs = 1, kTensors = 3;  // G, U, A chunks
+};
+template <>
+struct PairCfg<kDown> {
+  static constexpr int kStages = 6, kBufs = 0, kTensors = 0;
+};
+template <>
+struct PairCfg<kGradAct> {
+  static constexpr int kStages = 4, kBufs = 3, kTensors = 2;  // G, U in; dG, dU out, in place
+};
+template <>
+struct PairCfg<kGrads> {
+  static constexpr int kStages = 6, kBufs = 0, kTensors = 0;
+};
+
+template <int KIND>
+constexpr int epi_bytes() {
+  return 2 * PairCfg<KIND>::kBufs * PairCfg<KIND>::kTensors * static_cast<int>(kChunkBytes);
+}
+
+template <int KIND>
+struct PairArgs {
+  PairJob job[KIND == kGrads ? kMaxJobs : 1];
+  int n_jobs, group_m;
+  int T, D, F, act;
+  // kUp: G, U, A (stores); kGradAct: G, U (loads), dG, dU (stores)
+  CUtensorMap m[4];
+  int save;  // kUp: G and U are kept
+  // kDown
+  const uint16_t* residual;
+  uint16_t* Y;
+  DropArgs drop;
+  float scale;  // kGradAct
+  GradOut grad[KIND == kGrads ? kMaxJobs : 1];
+  int* status;
+};
+
+struct Unit {
+  int job, mt, nt;
+};
+template <int KIND>
+__device__ __forceinline__ Unit find_unit(const PairArgs<KIND>& p, int u) {
+  int j = 0, first = 0;
+  if constexpr (KIND == kGrads) {
+    while (j + 1 < p.n_jobs && u >= p.job[j].units_end) first = p.job[j++].units_end;
+  }
+  GemmShape shp{p.job[j].m_tiles, p.job[j].n_tiles, 0, 0, 0, nullptr, p.group_m};
+  Unit r{j, 0, 0};
+  unit_tile(shp, u - first, r.mt, r.nt);
+  return r;
+}
+
+template <int KIND>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    k_ffn_pair(const __grid_constant__ PairArgs<KIND> p) {
+  pdl_enter();
+  using C = PairCfg<KIND>;
+  constexpr int STAGES = C::kStages;
+  using L = Gemm2Smem<kBN, STAGES, epi_bytes<KIND>()>;
+  static_assert(sizeof(GemmCtrl) <= L::CTRL_BYTES, "control block");
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int s_go;
+  __shared__ uint64_t s_load[2][3];  // kGradAct: chunk loads per column group and buffer
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  GemmCtrl* ctrl = reinterpret_cast<GemmCtrl*>(smem + L::CTRL_OFFSET);
+  const uint32_t tiles = smem_u32(smem);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  int* status = p.status;
+  const int num_units = p.job[p.n_jobs - 1].units_end;
+
+  // Both CTAs take the same decision (see ss_gemm2.cuh).
+  if (threadIdx.x == 0) s_go = read_status(status) == 0;
+  cluster_sync_all();
+  if (threadIdx.x == 0)
+    s_go = s_go && ld_shared_cluster_u32(mapa_shared(smem_u32(&s_go), rank ^ 1u));
+  cluster_sync_all();
+  if (!s_go) return;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&ctrl->full[s], 1);
+      mbar_init(&ctrl->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&ctrl->tfull[b], 1);
+      mbar_init(&ctrl->tempty[b], 2 * kEpiWarps);
+    }
+    for (int i = 0; i < 6; ++i) mbar_init(&s_load[0][0] + i, 1);
+    mbar_init(&ctrl->drain, 1);
+    ctrl->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&ctrl->tmem_base, 2 * kBN);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = ctrl->tmem_base;
+  volatile int* abort_flag = &ctrl->abort_flag;
+
+  if (warp == 0) {
+    // ------------------------------------------------ producer (both CTAs)
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0, issued = 0, issued_ph = 0;
+      bool ok = true;
+      for (int u = pair; ok && u < num_units; u += npairs) {
+        const Unit un = find_unit(p, u);
+        const PairJob& job = p.job[un.job];
+        const int m0 = un.mt * 2 * BM + static_cast<int>(rank) * BM;
+        // this CTA's half of the tile's N; gate/up: the same 128 features of
+        // the CTA's own matrix
+        const int n0 = KIND == kUp ? un.nt * (kBN / 2)
+                                   : un.nt * kBN + static_cast<int>(rank) * (kBN / 2);
+#pragma unroll 1
+        for (int seg = 0; ok && seg < 2; ++seg) {
+          const CUtensorMap* ma = &job.a[seg];
+          const CUtensorMap* mb = &job.b[KIND == kUp ? static_cast<int>(rank) : seg];
+          for (int kb = 0; kb < job.kb[seg]; ++kb) {
+            if (!mbar_wait(&ctrl->empty[s], ph ^ 1u, abort_flag, status)) {
+              ok = false;
+              break;
+            }
+            const uint32_t fb_local = smem_u32(&ctrl->full[s]);
+            if (rank == 0) mbar_arrive_expect_tx(&ctrl->full[s], 2 * L::STAGE_BYTES);
+            const uint32_t fb = rank == 0 ? fb_local : mapa_shared(fb_local, 0);
+            const uint32_t a_dst = tiles + s * L::STAGE_BYTES;
+            const uint32_t b_dst = a_dst + L::A_BYTES;
+            if (job.a_mn) {
+              tma_load_2d_pair(a_dst, ma, fb, m0, kb * BK);
+              tma_load_2d_pair(a_dst + 8192, ma, fb, m0 + 64, kb * BK);
+            } else {
+              tma_load_2d_pair(a_dst, ma, fb, kb * BK, m0);
+            }
+            if (job.b_mn) {
+              tma_load_2d_pair(b_dst, mb, fb, n0, kb * BK);
+              tma_load_2d_pair(b_dst + 8192, mb, fb, n0 + 64, kb * BK);
+            } else {
+              tma_load_2d_pair(b_dst, mb, fb, kb * BK, n0);
+            }
+            issued |= 1u << s;
+            issued_ph = (issued_ph & ~(1u << s)) | (ph << s);
+            if (++s == STAGES) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+        }
+      }
+      if (rank == 0) {
+        for (int i = 0; i < STAGES; ++i)
+          if ((issued >> i) & 1u) mbar_drain(&ctrl->full[i], (issued_ph >> i) & 1u, status);
+      } else if (!ok) {
+        // aborted: give this CTA's copies in flight, which land on the
+        // leader's barriers, a bounded moment before shared memory goes
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 200000ull) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMA issuer (leader)
+    if (lane == 0 && rank == 0) {
+      int s = 0, b = 0;
+      uint32_t ph = 0, aph = 0;
+      bool ok = true;
+      for (int u = pair; ok && u < num_units; u += npairs) {
+        const Unit un = find_unit(p, u);
+        const PairJob& job = p.job[un.job];
+        const int kbs = job.kb[0] + job.kb[1];
+        const bool a_mn = job.a_mn != 0, b_mn = job.b_mn != 0;
+        const uint32_t idesc = a_mn   ? idesc_bf16_f32(2 * BM, kBN, true, true)
+                               : b_mn ? idesc_bf16_f32(2 * BM, kBN, false, true)
+                                      : idesc_bf16_f32(2 * BM, kBN, false, false);
+        if (!mbar_wait(&ctrl->tempty[b], aph ^ 1u, abort_flag, status)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(b * kBN);
+        for (int kb = 0; kb < kbs; ++kb) {
+          if (!mbar_wait(&ctrl->full[s], ph, abort_flag, status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_addr = tiles + s * L::STAGE_BYTES;
+          const uint32_t b_addr = a_addr + L::A_BYTES;
+#pragma unroll
+          for (int k = 0; k < BK / UMMA_K; ++k) {
+            const uint64_t ad = a_mn ? sdesc_sw128(a_addr + k * 2048, 8192, 1024)
+                                     : sdesc_sw128(a_addr + k * 32, 16, 1024);
+            const uint64_t bd = b_mn ? sdesc_sw128(b_addr + k * 2048, 8192, 1024)
+                                     : sdesc_sw128(b_addr + k * 32, 16, 1024);
+            mma_bf16_pair(d_tmem, ad, bd, idesc, (kb | k) != 0 ? 1u : 0u);
+          }
+          mma_commit_pair(&ctrl->empty[s], 0x3);
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+        mma_commit_pair(&ctrl->tfull[b], 0x3);
+        if (++b == 2) {
+          b = 0;
+          aph ^= 1u;
+        }
+      }
+      mma_commit_pair(&ctrl->drain, 0x1);
+      mbar_drain(&ctrl->drain, 0, status);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------ epilogue (both CTAs)
+    const int q = warp & 3;         // TMEM lane quarter this warp may access
+    const int cg = (warp - 2) / 4;  // column group
+    const int row = q * 32 + lane;
+    const bool leader = ((threadIdx.x - 64) & 127) == 0;  // of the column group
+    const int bar = 1 + 2 * cg;                           // the group's named barrier
+    const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    // this group's staging
+    constexpr uint32_t kBufBytes = C::kTensors * kChunkBytes;
+    const uint32_t stage = tiles + L::EPI_OFFSET + static_cast<uint32_t>(cg * C::kBufs) * kBufBytes;
+    const uint64_t seed = KIND == kDown ? drop_seed(p.drop) : 0;
+    int b = 0;
+    uint32_t aph = 0;
+
+    // kGradAct: round r of this group is chunk r % 4 of its tile r / 4; the G
+    // and U chunks of round r are loaded two rounds ahead into buffer r % 3,
+    // replaced there by dG and dU, and stored from there.
+    [[maybe_unused]] int round = 0, n_rounds = 0;
+    [[maybe_unused]] auto chunk_at = [&](int r, int& col, int& mrow) {
+      const Unit un = find_unit(p, pair + (r >> 2) * npairs);
+      col = un.nt * kBN + cg * 128 + (r & 3) * 32;
+      mrow = (un.mt * 2 + static_cast<int>(rank)) * BM;
+    };
+    [[maybe_unused]] auto load_round = [&](int r) {  // by the group's leader
+      int col, mrow;
+      chunk_at(r, col, mrow);
+      const int buf = r % 3;
+      uint64_t* bar_ld = &s_load[cg][buf];
+      mbar_arrive_expect_tx(bar_ld, 2 * kChunkBytes);
+      const uint32_t dst = stage + static_cast<uint32_t>(buf) * kBufBytes;
+      tma_load_2d(dst, &p.m[0], bar_ld, col, mrow);
+      tma_load_2d(dst + kChunkBytes, &p.m[1], bar_ld, col, mrow);
+    };
+    if constexpr (KIND == kGradAct) {
+      const int my_units = pair < num_units ? (num_units - pair + npairs - 1) / npairs : 0;
+      n_rounds = my_units * 4;
+      if (leader)
+        for (int r = 0; r < min(2, n_rounds); ++r) load_round(r);
+    }
+
+    for (int u = pair; u < num_units; u += npairs) {
+      const bool ok = mbar_wait(&ctrl->tfull[b], aph, abort_flag, status);
+      bool go = __all_sync(0xffffffffu, ok);
+      if constexpr (C::kBufs > 0) {  // the epilogue's warps meet at barriers: agree first
+        if (lane == 0) ctrl->vote[(u / npairs) & 1][warp - 2] = go ? 1 : 0;
+        named_bar_sync(2, 32 * kEpiWarps);
+        const int* v = ctrl->vote[(u / npairs) & 1];
+        int all = 1;
+#pragma unroll
+        for (int i = 0; i < kEpiWarps; ++i) all &= v[i];
+        go = all != 0;
+      }
+      if (!go) break;
+      tc_fence_after();
+      const Unit un = find_unit(p, u);
+      const int mrow = (un.mt * 2 + static_cast<int>(rank)) * BM;  // first row of this CTA
+      const int t = mrow + row;
+      const uint32_t acc = lane_addr + static_cast<uint32_t>(b * kBN);
+      // hands the accumulator back once it is in registers
+      auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (rank == 0) mbar_arrive(&ctrl->tempty[b]);
+          else mbar_arrive_cluster(mapa_shared(smem_u32(&ctrl->tempty[b]), 0));
+        }
+      };
+
+      if constexpr (KIND == kUp) {
+        dispatch_act(p.act, [&](auto act) {
+          constexpr int ACT = decltype(act)::value;
+#pragma unroll 1
+          for (int i = 0; i < 2; ++i) {
+            const int c0 = cg * 64 + i * 32;  // within the tile's 128 features
+            const int f0 = un.nt * (kBN / 2) + c0;
+            uint32_t rg[32], ru[32];
+            tmem_ld32(acc + c0, rg);
+            tmem_ld32(acc + kBN / 2 + c0, ru);
+            tmem_ld_wait(rg);
+            tmem_ld_wait(ru);
+            if (i == 1) release();
+            // the last store from the staging buffer has read it
+            if (leader) bulk_wait_read<0>();
+            named_bar_sync(bar, 128);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t ga[4], gg[4], gu[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int at = c * 8 + 2 * k;
+                const float g0 = __uint_as_float(rg[at]), g1 = __uint_as_float(rg[at + 1]);
+                const float u0 = __uint_as_float(ru[at]), u1 = __uint_as_float(ru[at + 1]);
+                float a0, a1, unused;
+                act_eval<ACT, false>(g0, a0, unused);
+                act_eval<ACT, false>(g1, a1, unused);
+                ga[k] = pack_bf16x2(a0 * u0, a1 * u1);
+                gg[k] = pack_bf16x2(g0, g1);
+                gu[k] = pack_bf16x2(u0, u1);
+              }
+              const uint32_t at = chunk_addr(stage, row, c);
+              st_shared_v4(at, ga[0], ga[1], ga[2], ga[3]);
+              if (p.save) {
+                st_shared_v4(at + kChunkBytes, gg[0], gg[1], gg[2], gg[3]);
+                st_shared_v4(at + 2 * kChunkBytes, gu[0], gu[1], gu[2], gu[3]);
+              }
+            }
+            fence_proxy_async_smem();
+            named_bar_sync(bar, 128);
+            if (leader) {
+              if (f0 < p.F && mrow < p.T) {
+                tma_store_2d(&p.m[2], stage, f0, mrow);
+                if (p.save) {
+                  tma_store_2d(&p.m[0], stage + kChunkBytes, f0, mrow);
+                  tma_store_2d(&p.m[1], stage + 2 * kChunkBytes, f0, mrow);
+                }
+              }
+              bulk_commit();
+            }
+          }
+        });
+      } else if constexpr (KIND == kGradAct) {
+        dispatch_act(p.act, [&](auto act) {
+          constexpr int ACT = decltype(act)::value;
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i, ++round) {
+            const int c0 = cg * 128 + i * 32;
+            const int f0 = un.nt * kBN + c0;
+            const int buf = round % 3;
+            const uint32_t sg = stage + static_cast<uint32_t>(buf) * kBufBytes;
+            uint32_t r[32];
+            tmem_ld32(acc + c0, r);
+            mbar_wait(&s_load[cg][buf], (round / 3) & 1, abort_flag, status);
+            tmem_ld_wait(r);
+            if (i == 3) release();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t at = chunk_addr(sg, row, c);
+              uint32_t wg[4], wu[4];
+              ld_shared_v4(at, wg);
+              ld_shared_v4(at + kChunkBytes, wu);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                float o[4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const float dA = __uint_as_float(r[c * 8 + 2 * k + h]) * p.scale;
+                  const float g = h ? bf16_hi(wg[k]) : bf16_lo(wg[k]);
+                  const float uu = h ? bf16_hi(wu[k]) : bf16_lo(wu[k]);
+                  float a, d;
+                  act_eval<ACT, true>(g, a, d);
+                  o[h] = dA * uu * d;
+                  o[2 + h] = dA * a;
+                }
+                wg[k] = pack_bf16x2(o[0], o[1]);
+                wu[k] = pack_bf16x2(o[2], o[3]);
+              }
+              st_shared_v4(at, wg[0], wg[1], wg[2], wg[3]);
+              st_shared_v4(at + kChunkBytes, wu[0], wu[1], wu[2], wu[3]);
+            }
+            fence_proxy_async_smem();
+            named_bar_sync(bar, 128);
+            if (leader) {
+              if (f0 < p.F && mrow < p.T) {
+                tma_store_2d(&p.m[2], sg, f0, mrow);
+                tma_store_2d(&p.m[3], sg + kChunkBytes, f0, mrow);
+              }
+              bulk_commit();
+              if (round + 2 < n_rounds) {
+                bulk_wait_read<1>();  // the store of round - 1, from buffer (round + 2) % 3
+                load_round(round + 2);
+              }
+            }
+          }
+        });
+      } else if constexpr (KIND == kDown) {
+        const bool valid = t < p.T;
+        const int n0 = un.nt * kBN + cg * 128;
+        const int ncols = min(128, p.D - n0);
+        const size_t base = static_cast<size_t>(valid ? t : 0) * p.D;
+        if (ncols <= 0) release();
+        else
+          for_tmem_chunks<4>(
+              acc, cg * 4,
+              [&](const uint32_t(&r)[32], int i) {
+                const int nv = min(32, ncols - i * 32);
+                if (nv <= 0 || !valid) return;
+                const size_t at = base + n0 + i * 32;
+                uint32_t kept = 0xffffffffu;  // bit k: column k stays
+                if (p.drop.mode == kDropAll) kept = 0u;
+                if (p.drop.mode == kDropRandom) {
+                  kept = 0u;
+                  auto keep = [&](int k, bool yes) { kept |= (yes ? 1u : 0u) << k; };
+                  const uint64_t e = p.drop.offset + at;
+                  if (e & 1) for_kept<32, true>(seed, e, p.drop.thr, keep);
+                  else for_kept<32, false>(seed, e, p.drop.thr, keep);
+                }
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                  if (v * 8 >= nv) break;
+                  uint32_t w[4] = {0u, 0u, 0u, 0u};
+                  if (p.residual) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(p.residual + at + v * 8);
+                    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+                  }
+                  uint32_t o[4];
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const int j = v * 8 + 2 * k;
+                    float lo = bf16_lo(w[k]), hi = bf16_hi(w[k]);
+                    if ((kept >> j) & 1u) lo = fmaf(__uint_as_float(r[j]), p.drop.scale, lo);
+                    if ((kept >> (j + 1)) & 1u) hi = fmaf(__uint_as_float(r[j + 1]), p.drop.scale, hi);
+                    o[k] = pack_bf16x2(lo, hi);
+                  }
+                  *reinterpret_cast<uint4*>(p.Y + at + v * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+              },
+              release);
+      } else {
+        const GradOut& go_ = p.grad[un.job];
+        const bool valid = t < go_.rows;
+        const int n0 = un.nt * kBN + cg * 128;
+        const int ncols = min(128, go_.cols - n0);
+        const size_t base = static_cast<size_t>(valid ? t : 0) * go_.cols + n0;
+        const float scale = go_.scale;
+        if (ncols <= 0) release();
+        else if (go_.fp32)
+          for_tmem_chunks<4>(
+              acc, cg * 4,
+              [&](const uint32_t(&r)[32], int i) {
+                const int nv = min(32, ncols - i * 32);
+                if (nv <= 0 || !valid) return;
+                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(go_.out) + base + i * 32);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  if (k * 4 >= nv) break;
+                  float4 o = make_float4(
+                      __uint_as_float(r[4 * k]) * scale, __uint_as_float(r[4 * k + 1]) * scale,
+                      __uint_as_float(r[4 * k + 2]) * scale, __uint_as_float(r[4 * k + 3]) * scale);
+                  if (go_.accumulate) {
+                    const float4 old = dst[k];
+                    o.x += old.x, o.y += old.y, o.z += old.z, o.w += old.w;
+                  }
+                  dst[k] = o;
+                }
+              },
+              release);
+        else
+          for_tmem_chunks<4>(
+              acc, cg * 4,
+              [&](const uint32_t(&r)[32], int i) {
+                const int nv = min(32, ncols - i * 32);
+                if (nv <= 0 || !valid) return;
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(go_.out) + base + i * 32);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                  if (v * 8 >= nv) break;
+                  uint32_t w[4] = {0u, 0u, 0u, 0u}, o[4];
+                  if (go_.accumulate) {
+                    const uint4 x = dst[v];
+                    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+                  }
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const int j = v * 8 + 2 * k;
+                    o[k] = pack_bf16x2(fmaf(__uint_as_float(r[j]), scale, bf16_lo(w[k])),
+                                       fmaf(__uint_as_float(r[j + 1]), scale, bf16_hi(w[k])));
+                  }
+                  dst[v] = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+              },
+              release);
+      }
+      if (++b == 2) {
+        b = 0;
+        aph ^= 1u;
+      }
+    }
+    if constexpr (KIND == kGradAct) {
+      // aborted: the chunk loads in flight land before shared memory goes
+      if (leader && round < n_rounds)
+        for (int r = round; r < min(round + 2, n_rounds); ++r)
+          mbar_drain(&s_load[cg][r % 3], (r / 3) & 1, status);
+    }
+    if constexpr (C::kBufs > 0) {
+      if (leader) bulk_wait<0>();
+    }
+  }
+  __syncthreads();
+  cluster_sync_all();  // the leader's MMAs are drained before either CTA frees TMEM
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 2 * kBN);
+  }
+}
+
+// ------------------------------------------------------------- host side
+
+// The units walk groups of this many row tiles column by column: a round of
+// the 76 pairs then reads about as many row tiles of A as column tiles of B.
+constexpr int kGroupM = 8;
+
+int tiles_of(int64_t n, int tile) { return static_cast<int>((n + tile - 1) / tile); }
+
+// K-major operand [rows, k]: boxes of 128 rows x 64 of k. MN-major operand
+// [k, cols]: boxes of 64 columns x 64 of k.
+bool map_kmajor(CUtensorMap* m, const uint16_t* p, int64_t rows, int64_t k) {
+  return make_bf16_map(m, p, k, rows, k * 2, BK, 128);
+}
+bool map_mnmajor(CUtensorMap* m, const uint16_t* p, int64_t k, int64_t cols) {
+  return make_bf16_map(m, p, cols, k, cols * 2, 64, BK);
+}
+bool map_chunk(CUtensorMap* m, const uint16_t* p, int64_t rows, int64_t cols) {
+  return make_bf16_map(m, p, cols, rows, cols * 2, 32, 128);
+}
+
+template <int KIND>
+cudaError_t launch_pair(PairArgs<KIND>& p, int num_sms, cudaStream_t s) {
+  int end = 0;
+  for (int j = 0; j < p.n_jobs; ++j) {
+    end += p.job[j].m_tiles * p.job[j].n_tiles;
+    p.job[j].units_end = end;
+  }
+  p.group_m = kGroupM;
+  const int pairs = end < num_sms / 2 ? end : num_sms / 2;
+  constexpr int smem = Gemm2Smem<kBN, PairCfg<KIND>::kStages, epi_bytes<KIND>()>::TOTAL;
+  return launch_pdl(k_ffn_pair<KIND>, dim3(2 * pairs), dim3(kThreads), smem, s, p);
+}
+
+}  // namespace
+
+cudaError_t pair_gate_up(const FfnForward& f, cudaStream_t s) {
+  PairArgs<kUp> p = {};
+  PairJob& j = p.job[0];
+  const bool save = f.G != nullptr;
+  if (!map_kmajor(&j.a[0], f.X, f.T, f.D) || !map_kmajor(&j.b[0], f.Wg, f.F, f.D) ||
+      !map_kmajor(&j.b[1], f.Wu, f.F, f.D) || !map_chunk(&p.m[2], f.A, f.T, f.F) ||
+      (save && (!map_chunk(&p.m[0], f.G, f.T, f.F) || !map_chunk(&p.m[1], f.U, f.T, f.F))))
+    return cudaErrorInvalidValue;
+  j.kb[0] = tiles_of(f.D, BK);
+  j.m_tiles = tiles_of(f.T, 2 * BM);
+  j.n_tiles = tiles_of(f.F, kBN / 2);
+  p.n_jobs = 1;
+  p.T = f.T, p.D = f.D, p.F = f.F, p.act = f.act, p.save = save;
+  p.status = f.status;
+  return launch_pair(p, f.num_sms, s);
+}
+
+cudaError_t pair_down(const FfnForward& f, cudaStream_t s) {
+  PairArgs<kDown> p = {};
+  PairJob& j = p.job[0];
+  if (!map_kmajor(&j.a[0], f.A, f.T, f.F) || !map_kmajor(&j.b[0], f.Wd, f.D, f.F))
+    return cudaErrorInvalidValue;
+  j.kb[0] = tiles_of(f.F, BK);
+  j.m_tiles = tiles_of(f.T, 2 * BM);
+  j.n_tiles = tiles_of(f.D, kBN);
+  p.n_jobs = 1;
+  p.T = f.T, p.D = f.D, p.F = f.F;
+  p.residual = f.residual, p.Y = f.Y, p.drop = f.drop;
+  p.status = f.status;
+  return launch_pair(p, f.num_sms, s);
+}
+
+cudaError_t pair_grad_act(const FfnBackward& f, cudaStream_t s) {
+  PairArgs<kGradAct> p = {};
+  PairJob& j = p.job[0];
+  if (!map_kmajor(&j.a[0], f.dZ, f.T, f.D) || !map_mnmajor(&j.b[0], f.Wd, f.D, f.F) ||
+      !map_chunk(&p.m[0], f.G, f.T, f.F) || !map_chunk(&p.m[1], f.U, f.T, f.F) ||
+      !map_chunk(&p.m[2], f.dG, f.T, f.F) || !map_chunk(&p.m[3], f.dU, f.T, f.F))
+    return cudaErrorInvalidValue;
+  j.kb[0] = tiles_of(f.D, BK);
+  j.b_mn = 1;
+  j.m_tiles = tiles_of(f.T, 2 * BM);
+  j.n_tiles = tiles_of(f.F, kBN);
+  p.n_jobs = 1;
+  p.T = f.T, p.D = f.D, p.F = f.F, p.act = f.act, p.scale = f.scale;
+  p.status = f.status;
+  return launch_pair(p, f.num_sms, s);
+}
+
+cudaError_t pair_grads(const FfnBackward& f, cudaStream_t s) {
+  PairArgs<kGrads> p = {};
+  const int64_t T = f.T, D = f.D, F = f.F;
+  // dWg, dWu = dG^T X, dU^T X; dWd = dZ^T A: K = T
+  const uint16_t* a[3] = {f.dG, f.dU, f.dZ};
+  const uint16_t* b[3] = {f.X, f.X, f.A};
+  const int64_t rows[3] = {F, F, D}, cols[3] = {D, D, F};
+  void* out[3] = {f.dWg, f.dWu, f.dWd};
+  for (int i = 0; i < 3; ++i) {
+    PairJob& j = p.job[i];
+    if (!map_mnmajor(&j.a[0], a[i], T, rows[i]) || !map_mnmajor(&j.b[0], b[i], T, cols[i]))
+      return cudaErrorInvalidValue;
+    j.kb[0] = tiles_of(T, BK);
+    j.a_mn = j.b_mn = 1;
+    j.m_tiles = tiles_of(rows[i], 2 * BM);
+    j.n_tiles = tiles_of(cols[i], kBN);
+    p.grad[i] = GradOut{out[i], static_cast<int>(rows[i]), static_cast<int>(cols[i]),
+                        i == 2 ? f.scale : 1.f, f.dw_fp32, f.accumulate};
+  }
+  PairJob& j = p.job[3];  // dX = dG Wg + dU Wu: K = F twice
+  if (!map_kmajor(&j.a[0], f.dG, T, F) || !map_kmajor(&j.a[1], f.dU, T, F) ||
+      !map_mnmajor(&j.b[0], f.Wg, F, D) || !map_mnmajor(&j.b[1], f.Wu, F, D))
+    return cudaErrorInvalidValue;
+  j.kb[0] = j.kb[1] = tiles_of(F, BK);
+  j.b_mn = 1;
+  j.m_tiles = tiles_of(T, 2 * BM);
+  j.n_tiles = tiles_of(D, kBN);
+  p.grad[3] = GradOut{f.dX, f.T, f.D, 1.f, 0, 0};
+  p.n_jobs = 4;
+  p.T = f.T, p.D = f.D, p.F = f.F;
+  p.status = f.status;
+  return launch_pair(p, f.num_sms, s);
+}
+
+}  // namespace ss
