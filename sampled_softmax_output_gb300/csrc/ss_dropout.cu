@@ -2,18 +2,32 @@
 //   y = residual + (kept ? scale * x : 0)
 // The mask comes from ss_dropout.cuh and is stored nowhere.
 //
-// Bound by memory: 4 bytes an element in bf16 (6 with a residual). Next to
-// that stand about 11 integer instructions an element for the hash. Groups of
-// 8 elements keep every access 16 bytes wide, and two groups per thread are in
-// flight before the first is hashed.
+// Groups of 8 elements keep every access 16 bytes wide. In fp32 and with a
+// residual (6 bytes an element or more) memory bounds it. bf16 without a
+// residual moves 4 bytes an element, next to about 11 integer instructions for
+// the hash and its comparison: there the integer pipe is the busiest unit (79%
+// of its cycles) and the two overlap imperfectly.
+//   bf16 65536 x 768 with residual : 49.8 us, 6.1 TB/s
+//   fp32 16411 x 1021              : 23.2 us, 5.8 TB/s
+//   bf16 65536 x 2048              : 94.5 us, 5.7 TB/s (with p = 0, that is
+//                                    without hashes, 88; a copy takes 81.8)
+// Tried and slower: two groups in flight per thread (more registers, fewer
+// threads: 114 us), the next group's loads issued ahead of the hash (105 to
+// 115), and the hash's shifts as high products on the other pipe (95 to 112).
+#include <algorithm>
+
 #include "ss_ffn.cuh"
 
 namespace ss {
 
 namespace {
 
-constexpr int kDropThreads = 256;
-constexpr int kDropGroups = 2;  // groups of 8 elements in flight per thread
+// Threads per block: kDropSmall, a block per kDropSmall groups, where memory
+// bounds the kernel and where there are few groups; kDropLarge, two resident
+// blocks per SM that walk the data, where the integer pipe does (bf16 without a
+// residual): 94.5 us against 110.4 at 65536 x 2048, where the small blocks' own
+// setup takes issue slots, but 52.2 against 49.8 us with a residual.
+constexpr int kDropSmall = 256, kDropLarge = 1024;
 
 struct Vec8 {
   float v[8];
@@ -74,66 +88,67 @@ __device__ __forceinline__ void drop_element(const T* x, const T* res, T* y, int
 
 // 16-byte aligned buffers; y may be x or residual (each element is read by the
 // thread that writes it, before it writes).
-template <class T, bool RES, bool ODD>
-__global__ void __launch_bounds__(kDropThreads)
+template <class T, bool RES, bool ODD, int THREADS>
+__global__ void __launch_bounds__(THREADS, 2048 / THREADS)
     k_dropout(const T* x, const T* res, int64_t n, const DropArgs d, T* y) {
   pdl_enter();
   const uint64_t seed = drop_seed(d);
   const int64_t n8 = n >> 3;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kDropThreads;
-  int64_t g = static_cast<int64_t>(blockIdx.x) * kDropThreads + threadIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * THREADS;
+  int64_t g = static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x;
   if (g < (n & 7)) drop_element<T, RES>(x, res, y, (n8 << 3) + g, d, seed);
-  for (; g < n8; g += kDropGroups * step) {
-    Vec8 a[kDropGroups], r[kDropGroups];
+  for (; g < n8; g += step) {
+    const int64_t at = g << 3;
+    Vec8 a = load8(x + at), r;
+    if (RES) r = load8(res + at);
+    if (d.mode == kDropRandom) {
+      for_kept<8, ODD>(seed, d.offset + static_cast<uint64_t>(at), d.thr, [&](int i, bool kept) {
+        a.v[i] = drop_one<RES>(a.v[i], RES ? r.v[i] : 0.f, kept, d.scale);
+      });
+    } else {
 #pragma unroll
-    for (int u = 0; u < kDropGroups; ++u) {
-      const int64_t at = (g + u * step) << 3;
-      if (g + u * step < n8) {
-        a[u] = load8(x + at);
-        if (RES) r[u] = load8(res + at);
-      }
+      for (int i = 0; i < 8; ++i)
+        a.v[i] = drop_one<RES>(a.v[i], RES ? r.v[i] : 0.f, d.mode == kDropNone, d.scale);
     }
-#pragma unroll
-    for (int u = 0; u < kDropGroups; ++u) {
-      if (g + u * step >= n8) break;
-      const int64_t at = (g + u * step) << 3;
-      if (d.mode == kDropRandom) {
-        for_kept<8, ODD>(seed, d.offset + static_cast<uint64_t>(at), d.thr, [&](int i, bool kept) {
-          a[u].v[i] = drop_one<RES>(a[u].v[i], r[u].v[i], kept, d.scale);
-        });
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          a[u].v[i] = drop_one<RES>(a[u].v[i], r[u].v[i], d.mode == kDropNone, d.scale);
-      }
-      store8(y + at, a[u]);
-    }
+    store8(y + at, a);
   }
 }
 
 template <class T, bool RES>
-__global__ void __launch_bounds__(kDropThreads)
+__global__ void __launch_bounds__(kDropSmall)
     k_dropout_unaligned(const T* x, const T* res, int64_t n, const DropArgs d, T* y) {
   pdl_enter();
   const uint64_t seed = drop_seed(d);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kDropThreads;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kDropThreads + threadIdx.x; i < n; i += step)
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kDropSmall;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kDropSmall + threadIdx.x; i < n; i += step)
     drop_element<T, RES>(x, res, y, i, d, seed);
+}
+
+template <class T, bool RES, int THREADS>
+cudaError_t launch_aligned(const T* x, const T* res, int64_t n, const DropArgs& d, T* y,
+                           int64_t blocks, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(blocks)), block(THREADS);
+  return (d.offset & 1)
+             ? launch_pdl(k_dropout<T, RES, true, THREADS>, grid, block, 0, s, x, res, n, d, y)
+             : launch_pdl(k_dropout<T, RES, false, THREADS>, grid, block, 0, s, x, res, n, d, y);
 }
 
 template <class T, bool RES>
 cudaError_t launch(const T* x, const T* res, int64_t n, const DropArgs& d, T* y, int num_sms,
                    cudaStream_t s) {
+  constexpr int64_t kMostBlocks = (int64_t(1) << 31) - 1;  // more groups are walked
   const bool aligned16 = (reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y) |
                           reinterpret_cast<uintptr_t>(res)) % 16 == 0;
-  const int64_t items = aligned16 ? (n >> 3) + 1 : n;  // + 1: the tail
-  const int64_t per_block = kDropThreads * static_cast<int64_t>(aligned16 ? kDropGroups : 1);
-  const int64_t blocks = (items + per_block - 1) / per_block;
-  const int64_t most = static_cast<int64_t>(num_sms) * 8;
-  const dim3 grid(static_cast<unsigned>(blocks < most ? blocks : most)), block(kDropThreads);
-  if (!aligned16) return launch_pdl(k_dropout_unaligned<T, RES>, grid, block, 0, s, x, res, n, d, y);
-  if (d.offset & 1) return launch_pdl(k_dropout<T, RES, true>, grid, block, 0, s, x, res, n, d, y);
-  return launch_pdl(k_dropout<T, RES, false>, grid, block, 0, s, x, res, n, d, y);
+  const int64_t items = aligned16 ? (n >> 3) + ((n & 7) != 0) : n;
+  const int64_t small = std::min((items + kDropSmall - 1) / kDropSmall, kMostBlocks);
+  if (!aligned16)
+    return launch_pdl(k_dropout_unaligned<T, RES>, dim3(static_cast<unsigned>(small)),
+                      dim3(kDropSmall), 0, s, x, res, n, d, y);
+  if constexpr (sizeof(T) == 2 && !RES) {
+    const int64_t large = 2 * static_cast<int64_t>(num_sms);
+    if (items >= large * kDropLarge) return launch_aligned<T, RES, kDropLarge>(x, res, n, d, y, large, s);
+  }
+  return launch_aligned<T, RES, kDropSmall>(x, res, n, d, y, small, s);
 }
 
 template <class T>
