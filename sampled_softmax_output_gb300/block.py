@@ -11,17 +11,17 @@ tensors, results on the current stream of the tensors' device.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
 import torch
 
-from . import WORKSPACE_HEADER_BYTES, SSError, _check, _lib, _need, _ptr, _stream
+from . import WORKSPACE_HEADER_BYTES, SSError, _lib, _need
 
 HEADER_BLOCK = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                             "include", "ss_block.h")
 MAX_F = 65536
+_BF16 = torch.bfloat16
 ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 
@@ -51,28 +51,56 @@ def _declare(L):
 _declare(_lib)
 
 
-def _on(device):
-    """The library launches on the current device: make it the tensors'."""
-    if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+# The checks below run in front of launches of a few microseconds, so each call
+# asks the cheap questions first and goes through _need, which says what is
+# wrong, only where one of them fails.
+
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, by device index
+
+
+def _fits(t, dtype, index, shape) -> bool:
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
+            and t.shape == shape and t.is_contiguous())
+
+
+def _call(fn, index, args):
+    """fn(*args, stream) with device `index` current: the library launches on
+    the current device. The C entry point's name is the function's."""
+    if index == torch.cuda.current_device():
+        code = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            code = fn(*args, _raw_stream(index))
+    if code != 0:
+        raise SSError(code, fn.__name__)
 
 
 def _dropout_spec(p, seed, offset, device):
+    if offset < 0:
+        raise ValueError(f"offset must not be negative, got {offset}")
     if isinstance(seed, torch.Tensor):
         _need(seed, "seed", torch.int64, device)
         if seed.numel() != 1:
             raise ValueError(f"seed must hold one value, got {seed.numel()}")
-        return DropoutSpec(float(p), 0, seed.data_ptr(), offset)
-    return DropoutSpec(float(p), seed & (2**64 - 1), None, offset)
+        return DropoutSpec(p, 0, seed.data_ptr(), offset)
+    return DropoutSpec(p, seed & (2**64 - 1), None, offset)
 
 
-def _float_tensor(t, name, device=None, shape=None, dtype=None):
-    if not isinstance(t, torch.Tensor):
+def _dropout_args(x, name, out, p, seed, offset):
+    """Checked (dtype code, device index, out, spec) of an elementwise call."""
+    if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in _DTYPES:
-        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
-    _need(t, name, dtype if dtype is not None else t.dtype, device, shape)
+    code = _DTYPES.get(x.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {x.dtype}")
+    index = x.get_device()
+    if index < 0 or not x.is_contiguous():
+        _need(x, name, x.dtype)
+    if out is None:
+        out = torch.empty_like(x)
+    elif not _fits(out, x.dtype, index, x.shape):
+        _need(out, "out", x.dtype, x.device, x.shape)
+    return code, index, out, _dropout_spec(p, seed, offset, x.device)
 
 
 def dropout(x: torch.Tensor, p: float, seed, residual: torch.Tensor | None = None,
@@ -82,21 +110,12 @@ def dropout(x: torch.Tensor, p: float, seed, residual: torch.Tensor | None = Non
     kernel reads when it runs (a captured graph then draws a new mask whenever
     the tensor has changed). offset: the position of x's first element in the
     stream of random numbers. out may be x or residual."""
-    _float_tensor(x, "x")
-    dev = x.device
-    if residual is not None:
-        _need(residual, "residual", x.dtype, dev, x.shape)
-    if offset < 0:
-        raise ValueError(f"offset must not be negative, got {offset}")
-    if out is None:
-        out = torch.empty_like(x)
-    else:
-        _need(out, "out", x.dtype, dev, x.shape)
-    spec = _dropout_spec(p, seed, offset, dev)
-    with _on(dev):
-        code = _lib.ss_dropout(_ptr(x), _ptr(residual), x.numel(), _DTYPES[x.dtype], spec,
-                               _ptr(out), _stream(dev))
-    _check(code, "ss_dropout")
+    code, index, out, spec = _dropout_args(x, "x", out, p, seed, offset)
+    if residual is not None and not _fits(residual, x.dtype, index, x.shape):
+        _need(residual, "residual", x.dtype, x.device, x.shape)
+    _call(_lib.ss_dropout, index,
+          (x.data_ptr(), None if residual is None else residual.data_ptr(), x.numel(), code, spec,
+           out.data_ptr()))
     return out
 
 
@@ -104,19 +123,9 @@ def dropout_backward(dy: torch.Tensor, p: float, seed, offset: int = 0,
                      out: torch.Tensor | None = None):
     """The gradient of dropout(x, p, seed, offset=offset) with respect to x
     (ss_dropout_backward); that of its residual is dy itself. out may be dy."""
-    _float_tensor(dy, "dy")
-    dev = dy.device
-    if offset < 0:
-        raise ValueError(f"offset must not be negative, got {offset}")
-    if out is None:
-        out = torch.empty_like(dy)
-    else:
-        _need(out, "out", dy.dtype, dev, dy.shape)
-    spec = _dropout_spec(p, seed, offset, dev)
-    with _on(dev):
-        code = _lib.ss_dropout_backward(_ptr(dy), dy.numel(), _DTYPES[dy.dtype], spec, _ptr(out),
-                                        _stream(dev))
-    _check(code, "ss_dropout_backward")
+    code, index, out, spec = _dropout_args(dy, "dy", out, p, seed, offset)
+    _call(_lib.ss_dropout_backward, index,
+          (dy.data_ptr(), dy.numel(), code, spec, out.data_ptr()))
     return out
 
 
@@ -137,25 +146,26 @@ def ffn_workspace(T: int, D: int, F: int, device=None) -> torch.Tensor:
 
 
 def _act(act):
-    if act not in ACTS:
+    code = ACTS.get(act)
+    if code is None:
         raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
-    return ACTS[act]
+    return code
 
 
 def _block_args(X, Wg, Wu, Wd, ws):
-    bf16 = torch.bfloat16
-    _need(X, "X", bf16)
+    """Checked (device index, T, D, F)."""
+    _need(X, "X", _BF16)
     if X.dim() != 2:
         raise ValueError(f"X must be [T, D], got {tuple(X.shape)}")
-    dev = X.device
+    index = X.get_device()
     T, D = X.shape
-    _need(Wg, "Wg", bf16, dev)
-    F = Wg.shape[0]
-    _need(Wg, "Wg", bf16, dev, (F, D))
-    _need(Wu, "Wu", bf16, dev, (F, D))
-    _need(Wd, "Wd", bf16, dev, (D, F))
-    _need(ws, "workspace", torch.uint8, dev)
-    return dev, T, D, F
+    F = Wg.shape[0] if isinstance(Wg, torch.Tensor) and Wg.dim() else 0
+    for t, name, shape in ((Wg, "Wg", (F, D)), (Wu, "Wu", (F, D)), (Wd, "Wd", (D, F))):
+        if not _fits(t, _BF16, index, shape):
+            _need(t, name, _BF16, X.device, shape)
+    if ws.dtype is not torch.uint8 or ws.get_device() != index or not ws.is_contiguous():
+        _need(ws, "workspace", torch.uint8, X.device)
+    return index, T, D, F
 
 
 def ffn_forward(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: torch.Tensor,
@@ -167,24 +177,22 @@ def ffn_forward(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: torch.T
     X [T, D], Wg, Wu [F, D], Wd [D, F], all bf16. Returns Y, or with save=True
     (Y, (G, U, A)), what ffn_backward needs. out may be residual. p, seed and
     offset as for dropout()."""
-    dev, T, D, F = _block_args(X, Wg, Wu, Wd, ws)
-    bf16 = torch.bfloat16
-    if residual is not None:
-        _need(residual, "residual", bf16, dev, (T, D))
-    if offset < 0:
-        raise ValueError(f"offset must not be negative, got {offset}")
+    index, T, D, F = _block_args(X, Wg, Wu, Wd, ws)
+    if residual is not None and not _fits(residual, _BF16, index, X.shape):
+        _need(residual, "residual", _BF16, X.device, X.shape)
     if out is None:
-        out = torch.empty(T, D, dtype=bf16, device=dev)
-    else:
-        _need(out, "out", bf16, dev, (T, D))
-    saved = (tuple(torch.empty(T, F, dtype=bf16, device=dev) for _ in range(3)) if save
-             else (None, None, None))
-    spec = _dropout_spec(p, seed, offset, dev)
-    with _on(dev):
-        code = _lib.ss_ffn_forward(_ptr(X), _ptr(Wg), _ptr(Wu), _ptr(Wd), _ptr(residual), T, D, F,
-                                   _act(act), spec, _ptr(out), *(_ptr(t) for t in saved),
-                                   _ptr(ws), ws.numel(), _stream(dev))
-    _check(code, "ss_ffn_forward")
+        out = torch.empty_like(X)
+    elif not _fits(out, _BF16, index, X.shape):
+        _need(out, "out", _BF16, X.device, X.shape)
+    saved, kept = None, (None, None, None)
+    if save:
+        saved = torch.empty((3, T, F), dtype=_BF16, device=X.device).unbind(0)
+        kept = [t.data_ptr() for t in saved]
+    _call(_lib.ss_ffn_forward, index,
+          (X.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(),
+           None if residual is None else residual.data_ptr(), T, D, F, _act(act),
+           _dropout_spec(p, seed, offset, X.device), out.data_ptr(), *kept, ws.data_ptr(),
+           ws.numel()))
     return (out, saved) if save else out
 
 
@@ -197,33 +205,32 @@ def ffn_backward(dY: torch.Tensor, X: torch.Tensor, Wg: torch.Tensor, Wu: torch.
     `saved` tensors: {"dX", "dWg", "dWu", "dWd"}, dX bf16 and the weight
     gradients of dw_dtype (fp32 or bf16), zero-filled when accumulate=True and
     none is given. The gradient of the residual is dY itself."""
-    dev, T, D, F = _block_args(X, Wg, Wu, Wd, ws)
-    bf16 = torch.bfloat16
-    if dw_dtype not in _DTYPES:
+    index, T, D, F = _block_args(X, Wg, Wu, Wd, ws)
+    dev = X.device
+    dw = _DTYPES.get(dw_dtype)
+    if dw is None:
         raise TypeError(f"dw_dtype must be torch.bfloat16 or torch.float32, got {dw_dtype}")
-    if offset < 0:
-        raise ValueError(f"offset must not be negative, got {offset}")
-    _need(dY, "dY", bf16, dev, (T, D))
+    if not _fits(dY, _BF16, index, X.shape):
+        _need(dY, "dY", _BF16, dev, X.shape)
     G, U, A = saved
     for t, name in ((G, "G"), (U, "U"), (A, "A")):
-        _need(t, name, bf16, dev, (T, F))
+        if not _fits(t, _BF16, index, (T, F)):
+            _need(t, name, _BF16, dev, (T, F))
     if dX is None:
-        dX = torch.empty(T, D, dtype=bf16, device=dev)
-    else:
-        _need(dX, "dX", bf16, dev, (T, D))
+        dX = torch.empty_like(X)
+    elif not _fits(dX, _BF16, index, X.shape):
+        _need(dX, "dX", _BF16, dev, X.shape)
     new = torch.zeros if accumulate else torch.empty
     grads = []
     for t, name, shape in ((dWg, "dWg", (F, D)), (dWu, "dWu", (F, D)), (dWd, "dWd", (D, F))):
         if t is None:
             t = new(shape, dtype=dw_dtype, device=dev)
-        else:
+        elif not _fits(t, dw_dtype, index, shape):
             _need(t, name, dw_dtype, dev, shape)
         grads.append(t)
-    spec = _dropout_spec(p, seed, offset, dev)
-    with _on(dev):
-        code = _lib.ss_ffn_backward(_ptr(dY), _ptr(X), _ptr(Wg), _ptr(Wu), _ptr(Wd), _ptr(G),
-                                    _ptr(U), _ptr(A), T, D, F, _act(act), spec,
-                                    _DTYPES[dw_dtype], 1 if accumulate else 0, _ptr(dX),
-                                    *(_ptr(t) for t in grads), _ptr(ws), ws.numel(), _stream(dev))
-    _check(code, "ss_ffn_backward")
+    _call(_lib.ss_ffn_backward, index,
+          (dY.data_ptr(), X.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(),
+           G.data_ptr(), U.data_ptr(), A.data_ptr(), T, D, F, _act(act),
+           _dropout_spec(p, seed, offset, dev), dw, 1 if accumulate else 0, dX.data_ptr(),
+           *[t.data_ptr() for t in grads], ws.data_ptr(), ws.numel()))
     return {"dX": dX, "dWg": grads[0], "dWu": grads[1], "dWd": grads[2]}
