@@ -22,7 +22,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libss.so")
 SOURCES = ["ss_api.cu", "ss_candidates.cu", "ss_gemm_logits.cu", "ss_gemm_logits_mtp.cu",
-           "ss_gemm_grads.cu", "ss_dropout.cu", "ss_ffn_pair.cu", "ss_ffn_api.cu"]
+           "ss_gemm_grads.cu", "ss_dropout.cu", "ss_ffn_pair.cu", "ss_ffn_split.cu",
+           "ss_ffn_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -98,10 +98,52 @@ struct FfnBackward {
 cudaError_t launch_drop_mask(const uint16_t* x, int64_t n, const DropArgs& drop, uint16_t* y,
                              int num_sms, cudaStream_t stream);
 
+// ------------------------------------------------- which family, which tile
+//
+// A problem is N rows of output (tokens, or rows of a weight gradient) by M
+// columns, K = 64 kb. The two families' times are estimated in microseconds
+// from constants fitted to graph-replayed calls on one GB300 (T 1 to 4096, D
+// 256 to 4096, F 256 to 12288); the fits are within about 2 us up to 30.
+
+// The choice for one problem on the split family.
+struct SplitPlan {
+  int bn, cluster;
+  float us;
+};
+
+// A CTA pair takes 0.36 us a k-block; launch, first loads, the last tile's
+// epilogue and the exit together 5.5 us.
+constexpr float kPairUsPerKb = 0.36f, kPairUsFixed = 5.5f;
+// out_us: what the outputs of the epilogue cost beyond one bf16 value (gate/up
+// and dA: two to four values read or written for each sum).
+inline float pair_us(int64_t units, int64_t kb, float out_us, int num_sms) {
+  const int64_t pairs = num_sms / 2, waves = (units + pairs - 1) / pairs;
+  return kPairUsFixed + out_us + kPairUsPerKb * static_cast<float>(waves * kb);
+}
+
+// 128 x bn tiles (m_tile = 64 features of two matrices for gate/up), bn the
+// narrowest that takes all tokens, up to 64, or 128; K over up to 8 CTAs.
+SplitPlan split_plan(int64_t n, int64_t m, int m_tile, int64_t kb, float out_us, bool wide_only,
+                     int num_sms);
+
+// ------------------------------------------------------------- the kernels
+
+// y = x with the dropped elements zeroed, not scaled (ss_dropout.cu)
+cudaError_t launch_drop_mask(const uint16_t* x, int64_t n, const DropArgs& drop, uint16_t* y,
+                             int num_sms, cudaStream_t stream);
+
 // CTA pairs, 256 x 256 tiles (ss_ffn_pair.cu)
+enum GradWhich { kDoX = 1, kDoW = 2 };  // the products of one pair_grads launch
 cudaError_t pair_gate_up(const FfnForward& p, cudaStream_t s);
 cudaError_t pair_down(const FfnForward& p, cudaStream_t s);
 cudaError_t pair_grad_act(const FfnBackward& p, cudaStream_t s);  // dG, dU
-cudaError_t pair_grads(const FfnBackward& p, cudaStream_t s);     // dX, dWg, dWu, dWd
+cudaError_t pair_grads(const FfnBackward& p, int which, cudaStream_t s);
+
+// 128 x (16 to 128) tiles, K split over a cluster (ss_ffn_split.cu)
+cudaError_t split_gate_up(const FfnForward& p, const SplitPlan& plan, cudaStream_t s);
+cudaError_t split_down(const FfnForward& p, const SplitPlan& plan, cudaStream_t s);
+cudaError_t split_grad_act(const FfnBackward& p, const SplitPlan& plan, cudaStream_t s);
+cudaError_t split_grad_x(const FfnBackward& p, const SplitPlan& plan, cudaStream_t s);
+cudaError_t split_grad_w(const FfnBackward& p, const SplitPlan& plan, cudaStream_t s);
 
 }  // namespace ss

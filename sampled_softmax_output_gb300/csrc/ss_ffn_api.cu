@@ -41,6 +41,15 @@ bool usable(std::initializer_list<const void*> ps) {
   });
 }
 
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t units(int64_t rows, int64_t cols, int col_tile = 256) {
+  return cdiv(rows, 256) * cdiv(cols, col_tile);
+}
+
+// What an epilogue's further outputs cost, in us: gate/up writes G, U and A,
+// dA reads G and U and writes dG and dU.
+constexpr float kUpOutUs = 0.8f, kActOutUs = 1.3f;
+
 bool known_act(int act) { return act >= SS_ACT_SILU && act <= SS_ACT_RELU; }
 
 }  // namespace
@@ -83,12 +92,16 @@ ss_status ss_ffn_forward(const uint16_t* X, const uint16_t* Wg, const uint16_t* 
   cudaError_t e;
   {
     StageTrace trace(s, "ffn_gate_up");
-    e = pair_gate_up(f, s);
+    const SplitPlan plan = split_plan(T, F, 64, cdiv(D, 64), kUpOutUs, false, f.num_sms);
+    e = pair_us(units(T, F, 128), cdiv(D, 64), 2.f, f.num_sms) < plan.us ? pair_gate_up(f, s)
+                                                                      : split_gate_up(f, plan, s);
   }
   if (e != cudaSuccess) return record_failure("ss_ffn_forward (gate/up)", e);
   {
     StageTrace trace(s, "ffn_down");
-    e = pair_down(f, s);
+    const SplitPlan plan = split_plan(T, D, 128, cdiv(F, 64), 0.f, false, f.num_sms);
+    e = pair_us(units(T, D), cdiv(F, 64), 0.f, f.num_sms) < plan.us ? pair_down(f, s)
+                                                                    : split_down(f, plan, s);
   }
   return e == cudaSuccess ? SS_OK : record_failure("ss_ffn_forward (down)", e);
 }
@@ -142,12 +155,30 @@ ss_status ss_ffn_backward(const uint16_t* dY, const uint16_t* X, const uint16_t*
   if (e != cudaSuccess) return record_failure("ss_ffn_backward (mask)", e);
   {
     StageTrace trace(s, "ffn_grad_act");
-    e = pair_grad_act(b, s);
+    const SplitPlan plan = split_plan(T, F, 128, cdiv(D, 64), kActOutUs, false, b.num_sms);
+    e = pair_us(units(T, F), cdiv(D, 64), 2.f, b.num_sms) < plan.us ? pair_grad_act(b, s)
+                                                                    : split_grad_act(b, plan, s);
   }
   if (e != cudaSuccess) return record_failure("ss_ffn_backward (dG, dU)", e);
   {
     StageTrace trace(s, "ffn_grads");
-    e = pair_grads(b, s);
+    // dX (K = 2 F) and the three dW (K = T): each on either family, or all in
+    // one launch of pairs, as long as its busiest pair
+    const int64_t kx = 2 * cdiv(F, 64), kw = cdiv(T, 64);
+    const int64_t ux = units(T, D), uw = 3 * units(F, D);
+    const SplitPlan px = split_plan(T, D, 128, kx, 0.f, false, b.num_sms);
+    // three gradients of F x D, as one of 3 F rows
+    const SplitPlan pw = split_plan(3 * cdiv(F, 128) * 128, D, 128, kw, 0.f, true, b.num_sms);
+    const float x_us = pair_us(ux, kx, 0.f, b.num_sms), w_us = pair_us(uw, kw, 0.f, b.num_sms);
+    const int64_t share = cdiv(ux * kx + uw * kw, b.num_sms / 2);
+    const float both_us =
+        kPairUsFixed + kPairUsPerKb * static_cast<float>(std::max(share, std::max(kx, kw)));
+    if (both_us <= std::min(x_us, px.us) + std::min(w_us, pw.us)) {
+      e = pair_grads(b, kDoX | kDoW, s);
+    } else {
+      e = x_us < px.us ? pair_grads(b, kDoX, s) : split_grad_x(b, px, s);
+      if (e == cudaSuccess) e = w_us < pw.us ? pair_grads(b, kDoW, s) : split_grad_w(b, pw, s);
+    }
   }
   return e == cudaSuccess ? SS_OK : record_failure("ss_ffn_backward (dX, dW)", e);
 }

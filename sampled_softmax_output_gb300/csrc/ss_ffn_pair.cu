@@ -17,7 +17,10 @@
 // 2-9 epilogue: two column groups of four warps, one accumulator row per
 // thread, two TMEM accumulators so that the epilogue of a tile runs beside the
 // MMAs of the next.
+#include <algorithm>
+#include <functional>
 #include <type_traits>
+#include <utility>
 
 #include "ss_ffn.cuh"
 #include "ss_gemm.cuh"
@@ -83,6 +86,15 @@ constexpr int epi_bytes() {
   return 2 * PairCfg<KIND>::kBufs * PairCfg<KIND>::kTensors * static_cast<int>(kChunkBytes);
 }
 
+// kGrads with both K lengths: which units each pair runs, in order (else pair p
+// runs p, p + pairs, ...).
+constexpr int kSchedPairs = 128, kSchedUnits = 2048;
+struct PairSchedule {
+  uint16_t first[kSchedPairs + 1];  // pair p runs unit[first[p] .. first[p + 1])
+  uint16_t unit[kSchedUnits];
+};
+struct NoSchedule {};
+
 template <int KIND>
 struct PairArgs {
   PairJob job[KIND == kGrads ? kMaxJobs : 1];
@@ -98,6 +110,26 @@ struct PairArgs {
   float scale;  // kGradAct
   GradOut grad[KIND == kGrads ? kMaxJobs : 1];
   int* status;
+  int listed;  // kGrads: 1 if sched holds the units
+  std::conditional_t<KIND == kGrads, PairSchedule, NoSchedule> sched;
+};
+
+// The units of one pair, one after the other.
+template <int KIND>
+struct UnitWalk {
+  int at, end, step;
+  __device__ __forceinline__ UnitWalk(const PairArgs<KIND>& p, int pair, int npairs)
+      : at(pair), end(p.job[p.n_jobs - 1].units_end), step(npairs) {
+    if constexpr (KIND == kGrads)
+      if (p.listed) at = p.sched.first[pair], end = p.sched.first[pair + 1], step = 1;
+  }
+  __device__ __forceinline__ bool more() const { return at < end; }
+  __device__ __forceinline__ void next() { at += step; }
+  __device__ __forceinline__ int unit(const PairArgs<KIND>& p) const {
+    if constexpr (KIND == kGrads)
+      if (p.listed) return p.sched.unit[at];
+    return at;
+  }
 };
 
 struct Unit {
@@ -134,7 +166,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
   int* status = p.status;
-  const int num_units = p.job[p.n_jobs - 1].units_end;
 
   // Both CTAs take the same decision (see ss_gemm2.cuh).
   if (threadIdx.x == 0) s_go = read_status(status) == 0;
@@ -174,8 +205,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int s = 0;
       uint32_t ph = 0, issued = 0, issued_ph = 0;
       bool ok = true;
-      for (int u = pair; ok && u < num_units; u += npairs) {
-        const Unit un = find_unit(p, u);
+      for (UnitWalk<KIND> w(p, pair, npairs); ok && w.more(); w.next()) {
+        const Unit un = find_unit(p, w.unit(p));
         const PairJob& job = p.job[un.job];
         const int m0 = un.mt * 2 * BM + static_cast<int>(rank) * BM;
         // this CTA's half of the tile's N; gate/up: the same 128 features of
@@ -235,8 +266,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int s = 0, b = 0;
       uint32_t ph = 0, aph = 0;
       bool ok = true;
-      for (int u = pair; ok && u < num_units; u += npairs) {
-        const Unit un = find_unit(p, u);
+      for (UnitWalk<KIND> w(p, pair, npairs); ok && w.more(); w.next()) {
+        const Unit un = find_unit(p, w.unit(p));
         const PairJob& job = p.job[un.job];
         const int kbs = job.kb[0] + job.kb[1];
         const bool a_mn = job.a_mn != 0, b_mn = job.b_mn != 0;
@@ -314,19 +345,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tma_load_2d(dst + kChunkBytes, &p.m[1], bar_ld, col, mrow);
     };
     if constexpr (KIND == kGradAct) {
+      const int num_units = p.job[0].units_end;
       const int my_units = pair < num_units ? (num_units - pair + npairs - 1) / npairs : 0;
       n_rounds = my_units * 4;
       if (leader)
         for (int r = 0; r < min(2, n_rounds); ++r) load_round(r);
     }
 
-    for (int u = pair; u < num_units; u += npairs) {
+    int turn = 0;
+    for (UnitWalk<KIND> w(p, pair, npairs); w.more(); w.next(), ++turn) {
       const bool ok = mbar_wait(&ctrl->tfull[b], aph, abort_flag, status);
       bool go = __all_sync(0xffffffffu, ok);
       if constexpr (C::kBufs > 0) {  // the epilogue's warps meet at barriers: agree first
-        if (lane == 0) ctrl->vote[(u / npairs) & 1][warp - 2] = go ? 1 : 0;
+        if (lane == 0) ctrl->vote[turn & 1][warp - 2] = go ? 1 : 0;
         named_bar_sync(2, 32 * kEpiWarps);
-        const int* v = ctrl->vote[(u / npairs) & 1];
+        const int* v = ctrl->vote[turn & 1];
         int all = 1;
 #pragma unroll
         for (int i = 0; i < kEpiWarps; ++i) all &= v[i];
@@ -334,7 +367,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (!go) break;
       tc_fence_after();
-      const Unit un = find_unit(p, u);
+      const Unit un = find_unit(p, w.unit(p));
       const int mrow = (un.mt * 2 + static_cast<int>(rank)) * BM;  // first row of this CTA
       const int t = mrow + row;
       const uint32_t acc = lane_addr + static_cast<uint32_t>(b * kBN);
@@ -595,6 +628,39 @@ bool map_chunk(CUtensorMap* m, const uint16_t* p, int64_t rows, int64_t cols) {
   return make_bf16_map(m, p, cols, rows, cols * 2, 32, 128);
 }
 
+// The units of two groups with different K, 0 .. n_a - 1 of kb_a k-blocks and
+// the n_b after them of kb_b, handed to the pair that is free first, the longer
+// group first: units that run at the same time are neighbours, which share
+// operands in L2, and the pairs finish within one short unit of each other.
+// Walked round-robin instead, T 8192, D 2048, F 5504 loses 7%. False: too many
+// units for the kernel's parameters (which 32 or more to a pair balance alone).
+bool balance(int n_a, int64_t kb_a, int n_b, int64_t kb_b, int pairs, PairSchedule* out) {
+  if (n_a + n_b > kSchedUnits || pairs > kSchedPairs) return false;
+  using Slot = std::pair<int64_t, int>;  // (time the pair becomes free, pair), earliest on top
+  Slot heap[kSchedPairs];
+  for (int p = 0; p < pairs; ++p) heap[p] = Slot(0, p);
+  uint8_t owner[kSchedUnits];
+  int count[kSchedPairs] = {};
+  const bool a_first = kb_a >= kb_b;
+  for (int i = 0; i < n_a + n_b; ++i) {
+    const bool is_a = a_first ? i < n_a : i >= n_b;
+    std::pop_heap(heap, heap + pairs, std::greater<Slot>());
+    Slot& slot = heap[pairs - 1];
+    slot.first += is_a ? kb_a : kb_b;
+    owner[i] = static_cast<uint8_t>(slot.second);
+    ++count[slot.second];
+    std::push_heap(heap, heap + pairs, std::greater<Slot>());
+  }
+  out->first[0] = 0;
+  for (int p = 0; p < pairs; ++p) out->first[p + 1] = static_cast<uint16_t>(out->first[p] + count[p]);
+  std::fill(count, count + pairs, 0);
+  for (int i = 0; i < n_a + n_b; ++i) {
+    const int unit = a_first ? i : i < n_b ? n_a + i : i - n_b;
+    out->unit[out->first[owner[i]] + count[owner[i]]++] = static_cast<uint16_t>(unit);
+  }
+  return true;
+}
+
 template <int KIND>
 cudaError_t launch_pair(PairArgs<KIND>& p, int num_sms, cudaStream_t s) {
   int end = 0;
@@ -604,6 +670,13 @@ cudaError_t launch_pair(PairArgs<KIND>& p, int num_sms, cudaStream_t s) {
   }
   p.group_m = kGroupM;
   const int pairs = end < num_sms / 2 ? end : num_sms / 2;
+  if constexpr (KIND == kGrads) {
+    if (p.n_jobs == kMaxJobs) {  // the three dW, then dX
+      const int n_dw = p.job[2].units_end;
+      p.listed = balance(n_dw, p.job[0].kb[0], end - n_dw, p.job[3].kb[0] + p.job[3].kb[1], pairs,
+                         &p.sched);
+    }
+  }
   constexpr int smem = Gemm2Smem<kBN, PairCfg<KIND>::kStages, epi_bytes<KIND>()>::TOTAL;
   return launch_pdl(k_ffn_pair<KIND>, dim3(2 * pairs), dim3(kThreads), smem, s, p);
 }
@@ -659,35 +732,37 @@ cudaError_t pair_grad_act(const FfnBackward& f, cudaStream_t s) {
   return launch_pair(p, f.num_sms, s);
 }
 
-cudaError_t pair_grads(const FfnBackward& f, cudaStream_t s) {
+cudaError_t pair_grads(const FfnBackward& f, int which, cudaStream_t s) {
   PairArgs<kGrads> p = {};
   const int64_t T = f.T, D = f.D, F = f.F;
-  // dWg, dWu = dG^T X, dU^T X; dWd = dZ^T A: K = T
-  const uint16_t* a[3] = {f.dG, f.dU, f.dZ};
-  const uint16_t* b[3] = {f.X, f.X, f.A};
-  const int64_t rows[3] = {F, F, D}, cols[3] = {D, D, F};
-  void* out[3] = {f.dWg, f.dWu, f.dWd};
-  for (int i = 0; i < 3; ++i) {
-    PairJob& j = p.job[i];
-    if (!map_mnmajor(&j.a[0], a[i], T, rows[i]) || !map_mnmajor(&j.b[0], b[i], T, cols[i]))
-      return cudaErrorInvalidValue;
-    j.kb[0] = tiles_of(T, BK);
-    j.a_mn = j.b_mn = 1;
-    j.m_tiles = tiles_of(rows[i], 2 * BM);
-    j.n_tiles = tiles_of(cols[i], kBN);
-    p.grad[i] = GradOut{out[i], static_cast<int>(rows[i]), static_cast<int>(cols[i]),
-                        i == 2 ? f.scale : 1.f, f.dw_fp32, f.accumulate};
+  if (which & kDoW) {  // dWg, dWu = dG^T X, dU^T X; dWd = dZ^T A: K = T
+    const uint16_t* a[3] = {f.dG, f.dU, f.dZ};
+    const uint16_t* b[3] = {f.X, f.X, f.A};
+    const int64_t rows[3] = {F, F, D}, cols[3] = {D, D, F};
+    void* out[3] = {f.dWg, f.dWu, f.dWd};
+    for (int i = 0; i < 3; ++i) {
+      PairJob& j = p.job[p.n_jobs];
+      if (!map_mnmajor(&j.a[0], a[i], T, rows[i]) || !map_mnmajor(&j.b[0], b[i], T, cols[i]))
+        return cudaErrorInvalidValue;
+      j.kb[0] = tiles_of(T, BK);
+      j.a_mn = j.b_mn = 1;
+      j.m_tiles = tiles_of(rows[i], 2 * BM);
+      j.n_tiles = tiles_of(cols[i], kBN);
+      p.grad[p.n_jobs++] = GradOut{out[i], static_cast<int>(rows[i]), static_cast<int>(cols[i]),
+                                   i == 2 ? f.scale : 1.f, f.dw_fp32, f.accumulate};
+    }
   }
-  PairJob& j = p.job[3];  // dX = dG Wg + dU Wu: K = F twice
-  if (!map_kmajor(&j.a[0], f.dG, T, F) || !map_kmajor(&j.a[1], f.dU, T, F) ||
-      !map_mnmajor(&j.b[0], f.Wg, F, D) || !map_mnmajor(&j.b[1], f.Wu, F, D))
-    return cudaErrorInvalidValue;
-  j.kb[0] = j.kb[1] = tiles_of(F, BK);
-  j.b_mn = 1;
-  j.m_tiles = tiles_of(T, 2 * BM);
-  j.n_tiles = tiles_of(D, kBN);
-  p.grad[3] = GradOut{f.dX, f.T, f.D, 1.f, 0, 0};
-  p.n_jobs = 4;
+  if (which & kDoX) {  // dX = dG Wg + dU Wu: K = F twice
+    PairJob& j = p.job[p.n_jobs];
+    if (!map_kmajor(&j.a[0], f.dG, T, F) || !map_kmajor(&j.a[1], f.dU, T, F) ||
+        !map_mnmajor(&j.b[0], f.Wg, F, D) || !map_mnmajor(&j.b[1], f.Wu, F, D))
+      return cudaErrorInvalidValue;
+    j.kb[0] = j.kb[1] = tiles_of(F, BK);
+    j.b_mn = 1;
+    j.m_tiles = tiles_of(T, 2 * BM);
+    j.n_tiles = tiles_of(D, kBN);
+    p.grad[p.n_jobs++] = GradOut{f.dX, f.T, f.D, 1.f, 0, 0};
+  }
   p.T = f.T, p.D = f.D, p.F = f.F;
   p.status = f.status;
   return launch_pair(p, f.num_sms, s);
