@@ -21,7 +21,6 @@ from . import WORKSPACE_HEADER_BYTES, SSError, _lib, _need
 HEADER_BLOCK = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                             "include", "ss_block.h")
 MAX_F = 65536
-_BF16 = torch.bfloat16
 ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 
@@ -56,34 +55,41 @@ _declare(_lib)
 # wrong, only where one of them fails.
 
 _raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, by device index
+_current_device = torch._C._cuda_getDevice
+_BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
 
 
 def _fits(t, dtype, index, shape) -> bool:
-    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
-            and t.shape == shape and t.is_contiguous())
+    try:
+        return (t.dtype is dtype and t.get_device() == index and t.shape == shape
+                and t.is_contiguous())
+    except AttributeError:  # no tensor: _need says so
+        return False
 
 
-def _call(fn, index, args):
+def _call(fn, index, *args):
     """fn(*args, stream) with device `index` current: the library launches on
     the current device. The C entry point's name is the function's."""
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         code = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
             code = fn(*args, _raw_stream(index))
-    if code != 0:
+    if code:
         raise SSError(code, fn.__name__)
 
 
 def _dropout_spec(p, seed, offset, device):
     if offset < 0:
         raise ValueError(f"offset must not be negative, got {offset}")
+    if seed.__class__ is int:
+        return DropoutSpec(p, seed & 0xFFFFFFFFFFFFFFFF, None, offset)
     if isinstance(seed, torch.Tensor):
         _need(seed, "seed", torch.int64, device)
         if seed.numel() != 1:
             raise ValueError(f"seed must hold one value, got {seed.numel()}")
         return DropoutSpec(p, 0, seed.data_ptr(), offset)
-    return DropoutSpec(p, seed & (2**64 - 1), None, offset)
+    return DropoutSpec(p, int(seed) & 0xFFFFFFFFFFFFFFFF, None, offset)
 
 
 def _dropout_args(x, name, out, p, seed, offset):
@@ -113,9 +119,8 @@ def dropout(x: torch.Tensor, p: float, seed, residual: torch.Tensor | None = Non
     code, index, out, spec = _dropout_args(x, "x", out, p, seed, offset)
     if residual is not None and not _fits(residual, x.dtype, index, x.shape):
         _need(residual, "residual", x.dtype, x.device, x.shape)
-    _call(_lib.ss_dropout, index,
-          (x.data_ptr(), None if residual is None else residual.data_ptr(), x.numel(), code, spec,
-           out.data_ptr()))
+    _call(_lib.ss_dropout, index, x.data_ptr(), None if residual is None else residual.data_ptr(),
+          x.numel(), code, spec, out.data_ptr())
     return out
 
 
@@ -124,8 +129,7 @@ def dropout_backward(dy: torch.Tensor, p: float, seed, offset: int = 0,
     """The gradient of dropout(x, p, seed, offset=offset) with respect to x
     (ss_dropout_backward); that of its residual is dy itself. out may be dy."""
     code, index, out, spec = _dropout_args(dy, "dy", out, p, seed, offset)
-    _call(_lib.ss_dropout_backward, index,
-          (dy.data_ptr(), dy.numel(), code, spec, out.data_ptr()))
+    _call(_lib.ss_dropout_backward, index, dy.data_ptr(), dy.numel(), code, spec, out.data_ptr())
     return out
 
 
@@ -154,17 +158,20 @@ def _act(act):
 
 def _block_args(X, Wg, Wu, Wd, ws):
     """Checked (device index, T, D, F)."""
-    _need(X, "X", _BF16)
+    if not (isinstance(X, torch.Tensor) and X.dtype is _BF16 and X.is_cuda and X.is_contiguous()):
+        _need(X, "X", _BF16)
     if X.dim() != 2:
         raise ValueError(f"X must be [T, D], got {tuple(X.shape)}")
     index = X.get_device()
     T, D = X.shape
     F = Wg.shape[0] if isinstance(Wg, torch.Tensor) and Wg.dim() else 0
-    for t, name, shape in ((Wg, "Wg", (F, D)), (Wu, "Wu", (F, D)), (Wd, "Wd", (D, F))):
-        if not _fits(t, _BF16, index, shape):
+    up = (F, D)
+    if not (_fits(Wg, _BF16, index, up) and _fits(Wu, _BF16, index, up)
+            and _fits(Wd, _BF16, index, (D, F))):
+        for t, name, shape in ((Wg, "Wg", up), (Wu, "Wu", up), (Wd, "Wd", (D, F))):
             _need(t, name, _BF16, X.device, shape)
-    if ws.dtype is not torch.uint8 or ws.get_device() != index or not ws.is_contiguous():
-        _need(ws, "workspace", torch.uint8, X.device)
+    if not _fits(ws, _U8, index, ws.shape):
+        _need(ws, "workspace", _U8, X.device)
     return index, T, D, F
 
 
@@ -188,11 +195,10 @@ def ffn_forward(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: torch.T
     if save:
         saved = torch.empty((3, T, F), dtype=_BF16, device=X.device).unbind(0)
         kept = [t.data_ptr() for t in saved]
-    _call(_lib.ss_ffn_forward, index,
-          (X.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(),
-           None if residual is None else residual.data_ptr(), T, D, F, _act(act),
-           _dropout_spec(p, seed, offset, X.device), out.data_ptr(), *kept, ws.data_ptr(),
-           ws.numel()))
+    _call(_lib.ss_ffn_forward, index, X.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(),
+          None if residual is None else residual.data_ptr(), T, D, F, _act(act),
+          _dropout_spec(p, seed, offset, X.device), out.data_ptr(), *kept, ws.data_ptr(),
+          ws.numel())
     return (out, saved) if save else out
 
 
@@ -228,9 +234,8 @@ def ffn_backward(dY: torch.Tensor, X: torch.Tensor, Wg: torch.Tensor, Wu: torch.
         elif not _fits(t, dw_dtype, index, shape):
             _need(t, name, dw_dtype, dev, shape)
         grads.append(t)
-    _call(_lib.ss_ffn_backward, index,
-          (dY.data_ptr(), X.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(),
-           G.data_ptr(), U.data_ptr(), A.data_ptr(), T, D, F, _act(act),
-           _dropout_spec(p, seed, offset, dev), dw, 1 if accumulate else 0, dX.data_ptr(),
-           *[t.data_ptr() for t in grads], ws.data_ptr(), ws.numel()))
+    _call(_lib.ss_ffn_backward, index, dY.data_ptr(), X.data_ptr(), Wg.data_ptr(), Wu.data_ptr(),
+          Wd.data_ptr(), G.data_ptr(), U.data_ptr(), A.data_ptr(), T, D, F, _act(act),
+          _dropout_spec(p, seed, offset, dev), dw, 1 if accumulate else 0, dX.data_ptr(),
+          *[t.data_ptr() for t in grads], ws.data_ptr(), ws.numel())
     return {"dX": dX, "dWg": grads[0], "dWu": grads[1], "dWd": grads[2]}

@@ -13,6 +13,19 @@
 // so the epilogue has both in one thread and the activation and product need
 // no exchange.
 //
+// What bounds it: in short runs a k-block of 256 x 256 x 64 takes 635 to 660
+// cycles (512 at the tensor cores' nominal rate), and what an epilogue moves
+// through shared memory comes on top, about 9 cycles a KB. So outputs are
+// stored from registers, 32 bytes a lane, wherever rows lie on 32-byte
+// boundaries (gate/up with G, U and A kept: 784 -> 698 cycles a k-block at D
+// 768); else (gate/up, dA) through shared memory by TMA, since half sectors
+// cost more than that (T 3001, D 1352, F 3640: 56 us against 68). In a steady
+// loop the board's power does: it runs at 1380 W and 1.6 to 1.7 GHz, and the
+// time follows the flops plus the DRAM bytes.
+//   single launches           gate/up      down         dA           dX and dW
+//   T 65536, D 768, F 2048    274 us 1.50  147 us 1.40  223 us 0.92  621 us 1.66 PFLOP/s
+//   T 8192, D 2048, F 5504    233    1.58  133    1.39  166    1.11  582    1.59
+//
 // Roles per CTA: warp 0 TMA producer, warp 1 MMA issuer (the leader's), warps
 // 2-9 epilogue: two column groups of four warps, one accumulator row per
 // thread, two TMEM accumulators so that the epilogue of a tile runs beside the
@@ -30,7 +43,8 @@ namespace ss {
 
 namespace {
 
-enum Kind { kUp, kDown, kGradAct, kGrads };
+// kUp, kGradAct: outputs staged in shared memory; ...Wide: stored from registers
+enum Kind { kUp, kUpWide, kDown, kGradAct, kGradActWide, kGrads };
 
 constexpr int kBN = 256;
 constexpr int kEpiWarps = 8;
@@ -51,6 +65,7 @@ struct GradOut {
   int rows, cols;
   float scale;
   int fp32, accumulate;
+  int wide;  // rows on 32-byte boundaries
 };
 
 // Staging of 32-column chunks: 128 rows x 64 bytes, 64-byte swizzle (16-byte
@@ -62,11 +77,40 @@ __device__ __forceinline__ uint32_t chunk_addr(uint32_t buf, int row, int c) {
          static_cast<uint32_t>((c ^ ((row >> 1) & 3)) * 16);
 }
 
+// Up to 32 columns (nv of them, a multiple of 8) of one row of bf16: whole
+// sectors where the rows are 32-byte aligned.
+__device__ __forceinline__ void store_row32(uint16_t* dst, const uint32_t (&w)[16], int nv,
+                                            bool wide) {
+  if (wide) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      if (c * 16 >= nv) break;
+      const uint32_t x[8] = {w[8 * c],     w[8 * c + 1], w[8 * c + 2], w[8 * c + 3],
+                             w[8 * c + 4], w[8 * c + 5], w[8 * c + 6], w[8 * c + 7]};
+      st_global_v8(dst + c * 16, x);
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      if (v * 8 < nv)
+        reinterpret_cast<uint4*>(dst)[v] =
+            make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+  }
+}
+
 template <int KIND>
 struct PairCfg;
 template <>
 struct PairCfg<kUp> {
   static constexpr int kStages = 5, kBufs = 1, kTensors = 3;  // G, U, A chunks
+};
+template <>
+struct PairCfg<kUpWide> {
+  static constexpr int kStages = 6, kBufs = 0, kTensors = 0;
+};
+template <>
+struct PairCfg<kGradActWide> {
+  static constexpr int kStages = 5, kBufs = 2, kTensors = 2;  // G, U in
 };
 template <>
 struct PairCfg<kDown> {
@@ -100,14 +144,17 @@ struct PairArgs {
   PairJob job[KIND == kGrads ? kMaxJobs : 1];
   int n_jobs, group_m;
   int T, D, F, act;
+  const uint16_t *G_in, *U_in;
+  uint16_t *G, *U, *A;
   // kUp: G, U, A (stores); kGradAct: G, U (loads), dG, dU (stores)
   CUtensorMap m[4];
   int save;  // kUp: G and U are kept
   // kDown
   const uint16_t* residual;
   uint16_t* Y;
+  int wide;  // Y's rows on 32-byte boundaries
   DropArgs drop;
-  float scale;  // kGradAct
+  float scale;  // kGradAct, kGradActWide
   GradOut grad[KIND == kGrads ? kMaxJobs : 1];
   int* status;
   int listed;  // kGrads: 1 if sched holds the units
@@ -157,7 +204,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   static_assert(sizeof(GemmCtrl) <= L::CTRL_BYTES, "control block");
   extern __shared__ uint8_t smem_raw[];
   __shared__ int s_go;
-  __shared__ uint64_t s_load[2][3];  // kGradAct: chunk loads per column group and buffer
+  __shared__ uint64_t s_load[2][4];  // kGradAct: chunk loads per column group and buffer
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   GemmCtrl* ctrl = reinterpret_cast<GemmCtrl*>(smem + L::CTRL_OFFSET);
@@ -166,14 +213,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
   int* status = p.status;
-
-  // Both CTAs take the same decision (see ss_gemm2.cuh).
-  if (threadIdx.x == 0) s_go = read_status(status) == 0;
-  cluster_sync_all();
-  if (threadIdx.x == 0)
-    s_go = s_go && ld_shared_cluster_u32(mapa_shared(smem_u32(&s_go), rank ^ 1u));
-  cluster_sync_all();
-  if (!s_go) return;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -184,22 +223,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&ctrl->tfull[b], 1);
       mbar_init(&ctrl->tempty[b], 2 * kEpiWarps);
     }
-    for (int i = 0; i < 6; ++i) mbar_init(&s_load[0][0] + i, 1);
+    for (int i = 0; i < 8; ++i) mbar_init(&s_load[0][0] + i, 1);
     mbar_init(&ctrl->drain, 1);
     ctrl->abort_flag = 0;
+    s_go = read_status(status) == 0;
     fence_mbar_init();
+    for (int j = 0; j < p.n_jobs; ++j) {
+      tma_prefetch_map(&p.job[j].a[0]);
+      tma_prefetch_map(&p.job[j].b[0]);
+    }
   }
   if (warp == 1) {
     tmem_alloc_pair(&ctrl->tmem_base, 2 * kBN);
     tmem_relinquish_pair();
   }
   tc_fence_before();
-  cluster_sync_all();
+  cluster_sync_all();  // barriers of both CTAs initialised, TMEM allocated
   tc_fence_after();
+  // Both CTAs take the same decision: an earlier error seen by either ends both.
+  const bool go_pair = s_go && ld_shared_cluster_u32(mapa_shared(smem_u32(&s_go), rank ^ 1u));
   const uint32_t tmem_base = ctrl->tmem_base;
   volatile int* abort_flag = &ctrl->abort_flag;
 
-  if (warp == 0) {
+  if (!go_pair) {
+    // nothing to do but to meet the peer below
+  } else if (warp == 0) {
     // ------------------------------------------------ producer (both CTAs)
     if (lane == 0) {
       int s = 0;
@@ -211,12 +259,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int m0 = un.mt * 2 * BM + static_cast<int>(rank) * BM;
         // this CTA's half of the tile's N; gate/up: the same 128 features of
         // the CTA's own matrix
-        const int n0 = KIND == kUp ? un.nt * (kBN / 2)
+        const int n0 = KIND == kUp || KIND == kUpWide ? un.nt * (kBN / 2)
                                    : un.nt * kBN + static_cast<int>(rank) * (kBN / 2);
 #pragma unroll 1
         for (int seg = 0; ok && seg < 2; ++seg) {
           const CUtensorMap* ma = &job.a[seg];
-          const CUtensorMap* mb = &job.b[KIND == kUp ? static_cast<int>(rank) : seg];
+          const CUtensorMap* mb = &job.b[KIND == kUp || KIND == kUpWide ? static_cast<int>(rank) : seg];
           for (int kb = 0; kb < job.kb[seg]; ++kb) {
             if (!mbar_wait(&ctrl->empty[s], ph ^ 1u, abort_flag, status)) {
               ok = false;
@@ -227,17 +275,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t fb = rank == 0 ? fb_local : mapa_shared(fb_local, 0);
             const uint32_t a_dst = tiles + s * L::STAGE_BYTES;
             const uint32_t b_dst = a_dst + L::A_BYTES;
+            // A is read by the few column tiles of its rows at about the same
+            // time (transposed operands of dW: evict-first took the launch from
+            // 708 to 660 cycles a k-block); B by every row tile: kept in L2
             if (job.a_mn) {
-              tma_load_2d_pair(a_dst, ma, fb, m0, kb * BK);
-              tma_load_2d_pair(a_dst + 8192, ma, fb, m0 + 64, kb * BK);
+              const uint64_t stream = l2_evict_first();
+              tma_load_2d_pair_hint(a_dst, ma, fb, m0, kb * BK, stream);
+              tma_load_2d_pair_hint(a_dst + 8192, ma, fb, m0 + 64, kb * BK, stream);
             } else {
               tma_load_2d_pair(a_dst, ma, fb, kb * BK, m0);
             }
+            const uint64_t keep = l2_evict_last();
             if (job.b_mn) {
-              tma_load_2d_pair(b_dst, mb, fb, n0, kb * BK);
-              tma_load_2d_pair(b_dst + 8192, mb, fb, n0 + 64, kb * BK);
+              tma_load_2d_pair_hint(b_dst, mb, fb, n0, kb * BK, keep);
+              tma_load_2d_pair_hint(b_dst + 8192, mb, fb, n0 + 64, kb * BK, keep);
             } else {
-              tma_load_2d_pair(b_dst, mb, fb, kb * BK, n0);
+              tma_load_2d_pair_hint(b_dst, mb, fb, kb * BK, n0, keep);
             }
             issued |= 1u << s;
             issued_ph = (issued_ph & ~(1u << s)) | (ph << s);
@@ -277,14 +330,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!mbar_wait(&ctrl->tempty[b], aph ^ 1u, abort_flag, status)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(b * kBN);
+        bool ready = false;
         for (int kb = 0; kb < kbs; ++kb) {
-          if (!mbar_wait(&ctrl->full[s], ph, abort_flag, status)) {
+          if (!ready && !mbar_wait(&ctrl->full[s], ph, abort_flag, status)) {
             ok = false;
             break;
           }
-          tc_fence_after();
           const uint32_t a_addr = tiles + s * L::STAGE_BYTES;
           const uint32_t b_addr = a_addr + L::A_BYTES;
+          const int sn = s + 1 == STAGES ? 0 : s + 1;
+          const uint32_t pn = sn == 0 ? ph ^ 1u : ph;
 #pragma unroll
           for (int k = 0; k < BK / UMMA_K; ++k) {
             const uint64_t ad = a_mn ? sdesc_sw128(a_addr + k * 2048, 8192, 1024)
@@ -292,12 +347,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint64_t bd = b_mn ? sdesc_sw128(b_addr + k * 2048, 8192, 1024)
                                      : sdesc_sw128(b_addr + k * 32, 16, 1024);
             mma_bf16_pair(d_tmem, ad, bd, idesc, (kb | k) != 0 ? 1u : 0u);
+            // the next stage is asked for while this one's MMAs queue (2 to 3%)
+            if (k == 1) ready = mbar_try_wait(smem_u32(&ctrl->full[sn]), pn);
           }
           mma_commit_pair(&ctrl->empty[s], 0x3);
-          if (++s == STAGES) {
-            s = 0;
-            ph ^= 1u;
-          }
+          s = sn;
+          ph = pn;
         }
         if (!ok) break;
         mma_commit_pair(&ctrl->tfull[b], 0x3);
@@ -325,9 +380,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int b = 0;
     uint32_t aph = 0;
 
-    // kGradAct: round r of this group is chunk r % 4 of its tile r / 4; the G
-    // and U chunks of round r are loaded two rounds ahead into buffer r % 3,
-    // replaced there by dG and dU, and stored from there.
+    // dA: round r of this group is chunk r % 4 of its tile r / 4; the G and U
+    // chunks of round r are loaded ahead into buffer r % kBufs. kGradAct: two
+    // rounds ahead, replaced there by dG and dU and stored from there;
+    // kGradActWide: read into registers, and the buffer is loaded again at once.
     [[maybe_unused]] int round = 0, n_rounds = 0;
     [[maybe_unused]] auto chunk_at = [&](int r, int& col, int& mrow) {
       const Unit un = find_unit(p, pair + (r >> 2) * npairs);
@@ -337,19 +393,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     [[maybe_unused]] auto load_round = [&](int r) {  // by the group's leader
       int col, mrow;
       chunk_at(r, col, mrow);
-      const int buf = r % 3;
+      const int buf = r % C::kBufs;
       uint64_t* bar_ld = &s_load[cg][buf];
       mbar_arrive_expect_tx(bar_ld, 2 * kChunkBytes);
       const uint32_t dst = stage + static_cast<uint32_t>(buf) * kBufBytes;
       tma_load_2d(dst, &p.m[0], bar_ld, col, mrow);
       tma_load_2d(dst + kChunkBytes, &p.m[1], bar_ld, col, mrow);
     };
-    if constexpr (KIND == kGradAct) {
+    if constexpr (KIND == kGradAct || KIND == kGradActWide) {
+      constexpr int kAhead = KIND == kGradAct ? 2 : C::kBufs;
       const int num_units = p.job[0].units_end;
       const int my_units = pair < num_units ? (num_units - pair + npairs - 1) / npairs : 0;
       n_rounds = my_units * 4;
       if (leader)
-        for (int r = 0; r < min(2, n_rounds); ++r) load_round(r);
+        for (int r = 0; r < min(kAhead, n_rounds); ++r) load_round(r);
     }
 
     int turn = 0;
@@ -381,7 +438,98 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       };
 
-      if constexpr (KIND == kUp) {
+      if constexpr (KIND == kUpWide) {
+        const bool valid = t < p.T;
+        dispatch_act(p.act, [&](auto act) {
+          constexpr int ACT = decltype(act)::value;
+#pragma unroll 1
+          for (int i = 0; i < 2; ++i) {
+            const int c0 = cg * 64 + i * 32;  // within the tile's 128 features
+            const int f0 = un.nt * (kBN / 2) + c0;
+            uint32_t rg[32], ru[32];
+            tmem_ld32(acc + c0, rg);
+            tmem_ld32(acc + kBN / 2 + c0, ru);
+            tmem_ld_wait(rg);
+            tmem_ld_wait(ru);
+            if (i == 1) release();
+            const size_t at = static_cast<size_t>(valid ? t : 0) * p.F + f0;
+            const int nv = valid ? min(32, p.F - f0) : 0;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              if (c * 16 >= nv) break;
+              uint32_t oa[8], og[8], ou[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int j = c * 16 + 2 * k;
+                const float g0 = __uint_as_float(rg[j]), g1 = __uint_as_float(rg[j + 1]);
+                const float u0 = __uint_as_float(ru[j]), u1 = __uint_as_float(ru[j + 1]);
+                float a0, a1, unused;
+                act_eval<ACT, false>(g0, a0, unused);
+                act_eval<ACT, false>(g1, a1, unused);
+                oa[k] = pack_bf16x2(a0 * u0, a1 * u1);
+                og[k] = pack_bf16x2(g0, g1);
+                ou[k] = pack_bf16x2(u0, u1);
+              }
+              st_global_v8(p.A + at + c * 16, oa);
+              if (p.save) {
+                st_global_v8(p.G + at + c * 16, og);
+                st_global_v8(p.U + at + c * 16, ou);
+              }
+            }
+          }
+        });
+      } else if constexpr (KIND == kGradActWide) {
+        const bool valid = t < p.T;
+        dispatch_act(p.act, [&](auto act) {
+          constexpr int ACT = decltype(act)::value;
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i, ++round) {
+            const int c0 = cg * 128 + i * 32;
+            const int f0 = un.nt * kBN + c0;
+            const int buf = round % C::kBufs;
+            const uint32_t sg = stage + static_cast<uint32_t>(buf) * kBufBytes;
+            uint32_t r[32];
+            tmem_ld32(acc + c0, r);
+            mbar_wait(&s_load[cg][buf], (round / C::kBufs) & 1, abort_flag, status);
+            uint32_t g[16], v[16];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t at = chunk_addr(sg, row, c);
+              uint32_t x[4];
+              ld_shared_v4(at, x);
+              g[4 * c] = x[0], g[4 * c + 1] = x[1], g[4 * c + 2] = x[2], g[4 * c + 3] = x[3];
+              ld_shared_v4(at + kChunkBytes, x);
+              v[4 * c] = x[0], v[4 * c + 1] = x[1], v[4 * c + 2] = x[2], v[4 * c + 3] = x[3];
+            }
+            tmem_ld_wait(r);
+            if (i == 3) release();
+            named_bar_sync(bar, 128);  // the group has read the buffer
+            if (leader && round + C::kBufs < n_rounds) load_round(round + C::kBufs);
+            const int nv = valid ? min(32, p.F - f0) : 0;
+            if (nv > 0) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                float o[4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const float dA = __uint_as_float(r[2 * k + h]) * p.scale;
+                  const float gv = h ? bf16_hi(g[k]) : bf16_lo(g[k]);
+                  const float uv = h ? bf16_hi(v[k]) : bf16_lo(v[k]);
+                  float a, d;
+                  act_eval<ACT, true>(gv, a, d);
+                  o[h] = dA * uv * d;
+                  o[2 + h] = dA * a;
+                }
+                g[k] = pack_bf16x2(o[0], o[1]);
+                v[k] = pack_bf16x2(o[2], o[3]);
+              }
+              const size_t at = static_cast<size_t>(t) * p.F + f0;
+              store_row32(p.G + at, g, nv, true);
+              store_row32(p.U + at, v, nv, true);
+            }
+          }
+        });
+      } else if constexpr (KIND == kUp) {
         dispatch_act(p.act, [&](auto act) {
           constexpr int ACT = decltype(act)::value;
 #pragma unroll 1
@@ -490,46 +638,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       } else if constexpr (KIND == kDown) {
         const bool valid = t < p.T;
         const int n0 = un.nt * kBN + cg * 128;
-        const int ncols = min(128, p.D - n0);
-        const size_t base = static_cast<size_t>(valid ? t : 0) * p.D;
-        if (ncols <= 0) release();
-        else
-          for_tmem_chunks<4>(
-              acc, cg * 4,
-              [&](const uint32_t(&r)[32], int i) {
-                const int nv = min(32, ncols - i * 32);
-                if (nv <= 0 || !valid) return;
-                const size_t at = base + n0 + i * 32;
-                uint32_t kept = 0xffffffffu;  // bit k: column k stays
-                if (p.drop.mode == kDropAll) kept = 0u;
-                if (p.drop.mode == kDropRandom) {
-                  kept = 0u;
-                  auto keep = [&](int k, bool yes) { kept |= (yes ? 1u : 0u) << k; };
-                  const uint64_t e = p.drop.offset + at;
-                  if (e & 1) for_kept<32, true>(seed, e, p.drop.thr, keep);
-                  else for_kept<32, false>(seed, e, p.drop.thr, keep);
-                }
+        const int ncols = valid ? min(128, p.D - n0) : 0;
+        const size_t base = static_cast<size_t>(valid ? t : 0) * p.D + n0;
+        // the residual of the next chunk, loaded one chunk ahead
+        uint32_t rn[16];
+        auto load_residual = [&](int i) {
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                  if (v * 8 >= nv) break;
-                  uint32_t w[4] = {0u, 0u, 0u, 0u};
-                  if (p.residual) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(p.residual + at + v * 8);
-                    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-                  }
-                  uint32_t o[4];
+          for (int v = 0; v < 4; ++v) {
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (p.residual && i * 32 + v * 8 < ncols)
+              x = *reinterpret_cast<const uint4*>(p.residual + base + i * 32 + v * 8);
+            rn[4 * v] = x.x, rn[4 * v + 1] = x.y, rn[4 * v + 2] = x.z, rn[4 * v + 3] = x.w;
+          }
+        };
+        load_residual(0);
+        for_tmem_chunks<4>(
+            acc, cg * 4,
+            [&](const uint32_t(&r)[32], int i) {
+              uint32_t w[16];
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    const int j = v * 8 + 2 * k;
-                    float lo = bf16_lo(w[k]), hi = bf16_hi(w[k]);
-                    if ((kept >> j) & 1u) lo = fmaf(__uint_as_float(r[j]), p.drop.scale, lo);
-                    if ((kept >> (j + 1)) & 1u) hi = fmaf(__uint_as_float(r[j + 1]), p.drop.scale, hi);
-                    o[k] = pack_bf16x2(lo, hi);
-                  }
-                  *reinterpret_cast<uint4*>(p.Y + at + v * 8) = make_uint4(o[0], o[1], o[2], o[3]);
-                }
-              },
-              release);
+              for (int k = 0; k < 16; ++k) w[k] = rn[k];
+              if (i < 3) load_residual(i + 1);
+              const int nv = min(32, ncols - i * 32);
+              if (nv <= 0) return;
+              const size_t at = base + i * 32;
+              uint32_t kept = 0xffffffffu;  // bit k: column k stays
+              if (p.drop.mode == kDropAll) kept = 0u;
+              if (p.drop.mode == kDropRandom) {
+                kept = 0u;
+                auto keep = [&](int k, bool yes) { kept |= (yes ? 1u : 0u) << k; };
+                const uint64_t e = p.drop.offset + at;
+                if (e & 1) for_kept<32, true>(seed, e, p.drop.thr, keep);
+                else for_kept<32, false>(seed, e, p.drop.thr, keep);
+              }
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                float lo = bf16_lo(w[k]), hi = bf16_hi(w[k]);
+                if ((kept >> (2 * k)) & 1u) lo = fmaf(__uint_as_float(r[2 * k]), p.drop.scale, lo);
+                if ((kept >> (2 * k + 1)) & 1u)
+                  hi = fmaf(__uint_as_float(r[2 * k + 1]), p.drop.scale, hi);
+                w[k] = pack_bf16x2(lo, hi);
+              }
+              store_row32(p.Y + at, w, nv, p.wide);
+            },
+            release);
       } else {
         const GradOut& go_ = p.grad[un.job];
         const bool valid = t < go_.rows;
@@ -565,23 +717,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               [&](const uint32_t(&r)[32], int i) {
                 const int nv = min(32, ncols - i * 32);
                 if (nv <= 0 || !valid) return;
-                uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(go_.out) + base + i * 32);
+                uint16_t* dst = static_cast<uint16_t*>(go_.out) + base + i * 32;
+                uint32_t w[16] = {};
+                if (go_.accumulate) {
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                  if (v * 8 >= nv) break;
-                  uint32_t w[4] = {0u, 0u, 0u, 0u}, o[4];
-                  if (go_.accumulate) {
-                    const uint4 x = dst[v];
-                    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-                  }
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    const int j = v * 8 + 2 * k;
-                    o[k] = pack_bf16x2(fmaf(__uint_as_float(r[j]), scale, bf16_lo(w[k])),
-                                       fmaf(__uint_as_float(r[j + 1]), scale, bf16_hi(w[k])));
-                  }
-                  dst[v] = make_uint4(o[0], o[1], o[2], o[3]);
+                  for (int v = 0; v < 4; ++v)
+                    if (v * 8 < nv) {
+                      const uint4 x = reinterpret_cast<const uint4*>(dst)[v];
+                      w[4 * v] = x.x, w[4 * v + 1] = x.y, w[4 * v + 2] = x.z, w[4 * v + 3] = x.w;
+                    }
                 }
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                  w[k] = pack_bf16x2(fmaf(__uint_as_float(r[2 * k]), scale, bf16_lo(w[k])),
+                                     fmaf(__uint_as_float(r[2 * k + 1]), scale, bf16_hi(w[k])));
+                store_row32(dst, w, nv, go_.wide);
               },
               release);
       }
@@ -590,13 +740,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         aph ^= 1u;
       }
     }
-    if constexpr (KIND == kGradAct) {
+    if constexpr (KIND == kGradAct || KIND == kGradActWide) {
       // aborted: the chunk loads in flight land before shared memory goes
+      constexpr int kAhead = KIND == kGradAct ? 2 : C::kBufs;
       if (leader && round < n_rounds)
-        for (int r = round; r < min(round + 2, n_rounds); ++r)
-          mbar_drain(&s_load[cg][r % 3], (r / 3) & 1, status);
+        for (int r = round; r < min(round + kAhead, n_rounds); ++r)
+          mbar_drain(&s_load[cg][r % C::kBufs], (r / C::kBufs) & 1, status);
     }
-    if constexpr (C::kBufs > 0) {
+    if constexpr (KIND == kUp || KIND == kGradAct) {
       if (leader) bulk_wait<0>();
     }
   }
@@ -610,9 +761,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------- host side
 
+// From this K on the MMAs, not the eight bytes of G, U, dG and dU for each
+// element of dA, bound that product: 256 x 256 elements move 512 KB, as long as
+// about 17 k-blocks. kGradActWide leaves more shared-memory bandwidth to the
+// MMAs (T 16384, D 1024, F 4096: 129 us against 135); kGradAct keeps more
+// copies in flight (T 65536, D 768, F 2048: 205 us against 225).
+constexpr int kActWideKb = 16;
+
 // The units walk groups of this many row tiles column by column: a round of
 // the 76 pairs then reads about as many row tiles of A as column tiles of B.
 constexpr int kGroupM = 8;
+
+// rows of `cols` bf16 values at each of these on 32-byte boundaries
+bool rows_on_sectors(int64_t cols, std::initializer_list<const void*> ps) {
+  return cols % 16 == 0 && std::all_of(ps.begin(), ps.end(), [](const void* p) {
+           return reinterpret_cast<uintptr_t>(p) % 32 == 0;
+         });
+}
 
 int tiles_of(int64_t n, int tile) { return static_cast<int>((n + tile - 1) / tile); }
 
@@ -683,21 +848,60 @@ cudaError_t launch_pair(PairArgs<KIND>& p, int num_sms, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t pair_gate_up(const FfnForward& f, cudaStream_t s) {
-  PairArgs<kUp> p = {};
+namespace {
+
+template <int KIND>
+cudaError_t gate_up(const FfnForward& f, cudaStream_t s) {
+  PairArgs<KIND> p = {};
   PairJob& j = p.job[0];
   const bool save = f.G != nullptr;
   if (!map_kmajor(&j.a[0], f.X, f.T, f.D) || !map_kmajor(&j.b[0], f.Wg, f.F, f.D) ||
-      !map_kmajor(&j.b[1], f.Wu, f.F, f.D) || !map_chunk(&p.m[2], f.A, f.T, f.F) ||
-      (save && (!map_chunk(&p.m[0], f.G, f.T, f.F) || !map_chunk(&p.m[1], f.U, f.T, f.F))))
+      !map_kmajor(&j.b[1], f.Wu, f.F, f.D))
+    return cudaErrorInvalidValue;
+  if (KIND == kUp &&
+      (!map_chunk(&p.m[2], f.A, f.T, f.F) ||
+       (save && (!map_chunk(&p.m[0], f.G, f.T, f.F) || !map_chunk(&p.m[1], f.U, f.T, f.F)))))
     return cudaErrorInvalidValue;
   j.kb[0] = tiles_of(f.D, BK);
   j.m_tiles = tiles_of(f.T, 2 * BM);
   j.n_tiles = tiles_of(f.F, kBN / 2);
   p.n_jobs = 1;
   p.T = f.T, p.D = f.D, p.F = f.F, p.act = f.act, p.save = save;
+  p.G = f.G, p.U = f.U, p.A = f.A;
   p.status = f.status;
   return launch_pair(p, f.num_sms, s);
+}
+
+template <int KIND>
+cudaError_t grad_act(const FfnBackward& f, cudaStream_t s) {
+  PairArgs<KIND> p = {};
+  PairJob& j = p.job[0];
+  if (!map_kmajor(&j.a[0], f.dZ, f.T, f.D) || !map_mnmajor(&j.b[0], f.Wd, f.D, f.F))
+    return cudaErrorInvalidValue;
+  if ((!map_chunk(&p.m[0], f.G, f.T, f.F) || !map_chunk(&p.m[1], f.U, f.T, f.F) ||
+       !map_chunk(&p.m[2], f.dG, f.T, f.F) || !map_chunk(&p.m[3], f.dU, f.T, f.F)))
+    return cudaErrorInvalidValue;
+  j.kb[0] = tiles_of(f.D, BK);
+  j.b_mn = 1;
+  j.m_tiles = tiles_of(f.T, 2 * BM);
+  j.n_tiles = tiles_of(f.F, kBN);
+  p.n_jobs = 1;
+  p.T = f.T, p.D = f.D, p.F = f.F, p.act = f.act, p.scale = f.scale;
+  p.G_in = f.G, p.U_in = f.U, p.G = f.dG, p.U = f.dU;
+  p.status = f.status;
+  return launch_pair(p, f.num_sms, s);
+}
+
+}  // namespace
+
+cudaError_t pair_gate_up(const FfnForward& f, cudaStream_t s) {
+  return rows_on_sectors(f.F, {f.G, f.U, f.A}) ? gate_up<kUpWide>(f, s) : gate_up<kUp>(f, s);
+}
+
+cudaError_t pair_grad_act(const FfnBackward& f, cudaStream_t s) {
+  return tiles_of(f.D, BK) >= kActWideKb && rows_on_sectors(f.F, {f.dG, f.dU})
+             ? grad_act<kGradActWide>(f, s)
+             : grad_act<kGradAct>(f, s);
 }
 
 cudaError_t pair_down(const FfnForward& f, cudaStream_t s) {
@@ -711,23 +915,7 @@ cudaError_t pair_down(const FfnForward& f, cudaStream_t s) {
   p.n_jobs = 1;
   p.T = f.T, p.D = f.D, p.F = f.F;
   p.residual = f.residual, p.Y = f.Y, p.drop = f.drop;
-  p.status = f.status;
-  return launch_pair(p, f.num_sms, s);
-}
-
-cudaError_t pair_grad_act(const FfnBackward& f, cudaStream_t s) {
-  PairArgs<kGradAct> p = {};
-  PairJob& j = p.job[0];
-  if (!map_kmajor(&j.a[0], f.dZ, f.T, f.D) || !map_mnmajor(&j.b[0], f.Wd, f.D, f.F) ||
-      !map_chunk(&p.m[0], f.G, f.T, f.F) || !map_chunk(&p.m[1], f.U, f.T, f.F) ||
-      !map_chunk(&p.m[2], f.dG, f.T, f.F) || !map_chunk(&p.m[3], f.dU, f.T, f.F))
-    return cudaErrorInvalidValue;
-  j.kb[0] = tiles_of(f.D, BK);
-  j.b_mn = 1;
-  j.m_tiles = tiles_of(f.T, 2 * BM);
-  j.n_tiles = tiles_of(f.F, kBN);
-  p.n_jobs = 1;
-  p.T = f.T, p.D = f.D, p.F = f.F, p.act = f.act, p.scale = f.scale;
+  p.wide = rows_on_sectors(f.D, {f.Y});
   p.status = f.status;
   return launch_pair(p, f.num_sms, s);
 }
@@ -749,7 +937,8 @@ cudaError_t pair_grads(const FfnBackward& f, int which, cudaStream_t s) {
       j.m_tiles = tiles_of(rows[i], 2 * BM);
       j.n_tiles = tiles_of(cols[i], kBN);
       p.grad[p.n_jobs++] = GradOut{out[i], static_cast<int>(rows[i]), static_cast<int>(cols[i]),
-                                   i == 2 ? f.scale : 1.f, f.dw_fp32, f.accumulate};
+                                   i == 2 ? f.scale : 1.f, f.dw_fp32, f.accumulate,
+                                   rows_on_sectors(cols[i], {out[i]})};
     }
   }
   if (which & kDoX) {  // dX = dG Wg + dU Wu: K = F twice
@@ -761,7 +950,7 @@ cudaError_t pair_grads(const FfnBackward& f, int which, cudaStream_t s) {
     j.b_mn = 1;
     j.m_tiles = tiles_of(T, 2 * BM);
     j.n_tiles = tiles_of(D, kBN);
-    p.grad[p.n_jobs++] = GradOut{f.dX, f.T, f.D, 1.f, 0, 0};
+    p.grad[p.n_jobs++] = GradOut{f.dX, f.T, f.D, 1.f, 0, 0, rows_on_sectors(D, {f.dX})};
   }
   p.T = f.T, p.D = f.D, p.F = f.F;
   p.status = f.status;
@@ -769,3 +958,4 @@ cudaError_t pair_grads(const FfnBackward& f, int which, cudaStream_t s) {
 }
 
 }  // namespace ss
+
