@@ -193,7 +193,8 @@ def ffn_forward(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: torch.T
         _need(out, "out", _BF16, X.device, X.shape)
     saved, kept = None, (None, None, None)
     if save:
-        saved = torch.empty((3, T, F), dtype=_BF16, device=X.device).unbind(0)
+        dev = X.device
+        saved = tuple([torch.empty((T, F), dtype=_BF16, device=dev) for _ in range(3)])
         kept = [t.data_ptr() for t in saved]
     _call(_lib.ss_ffn_forward, index, X.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(),
           None if residual is None else residual.data_ptr(), T, D, F, _act(act),

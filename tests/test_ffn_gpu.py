@@ -1,6 +1,9 @@
 """The gated feed-forward block on the GPU against 64 bits, every element within
 the bound that block_util counts from the stated roundings."""
-import numpy as np
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -15,7 +18,8 @@ BF16 = torch.bfloat16
 SIZES = [(1, 8, 8), (1, 768, 2048), (2, 72, 136), (7, 64, 64), (16, 1096, 520), (33, 256, 768),
          (64, 520, 1000), (127, 136, 264), (128, 128, 128), (129, 768, 256), (200, 1032, 2056),
          (255, 256, 264), (256, 768, 2048), (257, 264, 520), (513, 1352, 904), (1003, 392, 2952)]
-LARGE = [(4099, 768, 2048), (2050, 2048, 1032), (16384, 264, 520)]
+LARGE = [(4099, 768, 2048), (2050, 2048, 1032), (16384, 264, 520), (70001, 16, 24),
+         (1500, 1096, 1280)]
 
 
 def _inputs(T, D, F, seed=0, residual=True):
@@ -181,13 +185,17 @@ def test_deterministic():
         assert all(torch.equal(a, b) for a, b in zip(r, runs[0]))
 
 
-@pytest.mark.parametrize("T", [1, 5, 100, 130, 600])
-def test_rows_behind_the_last_stay(T):
-    D, F = 264, 392
+@pytest.mark.parametrize("T", [1, 5, 100, 130, 600, 2100])
+@pytest.mark.parametrize("shift", [0, 8])
+@pytest.mark.parametrize("D,F", [(264, 392), (272, 1040)])
+def test_rows_behind_the_last_stay(T, shift, D, F):
+    """Rows behind the batch keep what they held; buffers on 16-byte boundaries
+    that are no 32-byte ones give the same results (shift = 8 values)."""
     x = _inputs(T, D, F, seed=10)
     ws = ss.ffn_workspace(T, D, F)
     L = ss.lib()
-    bufs = {k: torch.full((T + 300, w), 7.0, dtype=BF16, device="cuda")
+    bufs = {k: torch.full(((T + 300) * w + 8,), 7.0, dtype=BF16, device="cuda")[shift:][
+        :(T + 300) * w].view(T + 300, w)
             for k, w in (("Y", D), ("G", F), ("U", F), ("A", F), ("dX", D))}
     ptr = {k: v.data_ptr() for k, v in {**x, **bufs}.items()}
     s = torch.cuda.current_stream().cuda_stream
@@ -201,7 +209,14 @@ def test_rows_behind_the_last_stay(T):
     torch.cuda.synchronize()
     for k, b in bufs.items():
         assert (b[T:] == 7).all(), k
-        assert not (b[:T] == 7).all(), k
+    saved = [bufs[k][:T] for k in "GUA"]
+    ref = forward64(*_weights(x), "silu", x["residual"])
+    for k in "YGUA":
+        assert_within(bufs[k][:T], ref[k], k)
+    ref = backward64(x["dY"], *_weights(x), saved, "silu")
+    assert_within(bufs["dX"][:T], ref["dX"], "dX")
+    for w, k, shape in zip(dW, ("dWg", "dWu", "dWd"), ((F, D), (F, D), (D, F))):
+        assert_within(w.view(shape), ref[k], k)
 
 
 def test_residual_in_place_and_empty_batch():
@@ -251,6 +266,34 @@ def test_captured_step_draws_new_masks(T):
         graph.replay()
         want = step(k, ws2)
         assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_first_call_of_a_process_may_be_captured():
+    """No warm-up: the kernels are loaded while the stream is being captured."""
+    code = """
+import torch, sampled_softmax_output_gb300 as ss
+g = torch.Generator("cuda").manual_seed(1)
+n = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)
+for T, D, F in ((3, 64, 72), (2100, 272, 1040)):
+    X, Wg, Wu, Wd, dY = n(T, D), n(F, D), n(F, D), n(D, F), n(T, D)
+    ws = ss.ffn_workspace(T, D, F)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        Y, saved = ss.ffn_forward(X, Wg, Wu, Wd, ws, p=0.1, seed=2, save=True)
+        out = ss.ffn_backward(dY, X, Wg, Wu, Wd, saved, ws, p=0.1, seed=2)
+        Z = ss.dropout(Y, 0.5, 3)
+    graph.replay()
+    Y2, saved2 = ss.ffn_forward(X, Wg, Wu, Wd, ws, p=0.1, seed=2, save=True)
+    out2 = ss.ffn_backward(dY, X, Wg, Wu, Wd, saved2, ws, p=0.1, seed=2)
+    assert torch.equal(Y, Y2) and torch.equal(Z, ss.dropout(Y2, 0.5, 3))
+    assert all(torch.equal(out[k], out2[k]) for k in out)
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 def test_smaller_batches_share_a_workspace_and_other_streams():
