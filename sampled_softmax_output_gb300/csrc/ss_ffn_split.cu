@@ -5,7 +5,9 @@
 // Out[n, m] = sum_k B[n, k] A[m, k] with the output's contiguous dimension on
 // the MMA's M (128 rows of weights) and the tokens on its N (16 to 128). One
 // token thus costs a 16-wide MMA next to the weights' bytes, which bound the
-// decoding forms: every weight is read once, by TMA, and all SMs stream.
+// decoding forms: every weight is read once, by TMA, and all SMs stream (T 16,
+// D 4096, F 12288: 302 MB in 51 us, 5.9 TB/s; tiles of 56 to 128 rows, so that
+// the CTAs number the SMs exactly, took as long).
 // Small batches of training have too few 256 x 256 tiles for 76 CTA pairs;
 // here a tile is an eighth of that and K gives up to eight CTAs more.
 //
@@ -67,8 +69,8 @@ struct SplitSmem {
   static constexpr int A_BYTES = BM * BK * 2;
   static constexpr int B_BYTES = BN * BK * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  // about 96 KB: two CTAs per SM
-  static constexpr int STAGES = 96 * 1024 / STAGE_BYTES;
+  // two CTAs per SM
+  static constexpr int STAGES = 110 * 1024 / STAGE_BYTES;
   static constexpr int RING = STAGES * STAGE_BYTES;
   static constexpr int TOTAL = RING + 1024;  // + alignment
   static_assert(BN * BM * 4 <= RING, "the partial tile takes the ring's place");
@@ -508,9 +510,9 @@ SplitPlan split_plan(int64_t n, int64_t m, int m_tile, int64_t kb, float out_us,
       const float load = share <= 1.f ? 1.f : share <= 2.f ? 1.f + 0.25f * (share - 1.f) : share;
       const float us = kFixed + (S > 1 ? kJoin : 0.f) +
                        load * (per_kb * kb / S + (kTile + out_us) * bn / 64);
-      // few tokens: the weights' bytes bound the kernel and the SMs share the
-      // memory evenly only with about one CTA each
-      if (n <= 64 && S > 1 && share > 1.3f) continue;
+      // few tokens: the weights' bytes bound the kernel; every CTA has a place
+      // from the start, so that all of K streams at once
+      if (n <= 64 && S > 1 && share > 2.f) continue;
       if (best.bn == 0 || us < best.us) best = SplitPlan{bn, S, us};
     }
     if (n <= bn) break;
