@@ -13,18 +13,19 @@
 // so the epilogue has both in one thread and the activation and product need
 // no exchange.
 //
-// What bounds it: in short runs a k-block of 256 x 256 x 64 takes 635 to 660
-// cycles (512 at the tensor cores' nominal rate), and what an epilogue moves
-// through shared memory comes on top, about 9 cycles a KB. So outputs are
-// stored from registers, 32 bytes a lane, wherever rows lie on 32-byte
-// boundaries (gate/up with G, U and A kept: 784 -> 698 cycles a k-block at D
-// 768); else (gate/up, dA) through shared memory by TMA, since half sectors
-// cost more than that (T 3001, D 1352, F 3640: 56 us against 68). In a steady
-// loop the board's power does: it runs at 1380 W and 1.6 to 1.7 GHz, and the
-// time follows the flops plus the DRAM bytes.
-//   single launches           gate/up      down         dA           dX and dW
-//   T 65536, D 768, F 2048    274 us 1.50  147 us 1.40  223 us 0.92  621 us 1.66 PFLOP/s
-//   T 8192, D 2048, F 5504    233    1.58  133    1.39  166    1.11  582    1.59
+// What bounds it: the MMAs of a k-block of 256 x 256 x 64 take 512 cycles from
+// resident operands; with TMA feeding them 575 to 580 (K of 4096 and more), and
+// what an epilogue moves through shared memory or to global memory comes on top,
+// about 9 cycles a KB. So outputs are stored from registers, 32 bytes a lane,
+// wherever rows lie on 32-byte boundaries (gate/up with G, U and A kept: 784 ->
+// 675 cycles a k-block at D 768); else (gate/up, dA) through shared memory by
+// TMA, since half sectors cost more than that (T 3001, D 1352, F 3640: 56 us
+// against 68). In a steady loop the board's power does: it draws 1380 W at 1.55
+// to 1.75 GHz.
+//   in-kernel time, rate      gate/up       down          dA            dX and dW
+//   T 65536, D 768, F 2048    249 us 1.66   133 us 1.55   206 us 1.00   567 us 1.82 PFLOP/s
+//   T 8192, D 2048, F 5504    205    1.80   112    1.65   143    1.29   508    1.82
+// (K-blocks lost to the last, partly filled round of tiles included.)
 //
 // Roles per CTA: warp 0 TMA producer, warp 1 MMA issuer (the leader's), warps
 // 2-9 epilogue: two column groups of four warps, one accumulator row per
@@ -250,8 +251,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 0) {
     // ------------------------------------------------ producer (both CTAs)
     if (lane == 0) {
+      // A is read by the few column tiles of its rows at about the same time
+      // (transposed operands of dW: evict-first took the launch from 708 to 660
+      // cycles a k-block); B by every row tile: kept in L2
+      const uint64_t stream = l2_evict_first(), keep = l2_evict_last();
+      const uint32_t full0 = mapa_shared(smem_u32(&ctrl->full[0]), 0);  // the leader's
       int s = 0;
-      uint32_t ph = 0, issued = 0, issued_ph = 0;
+      uint32_t ph = 0, issued = 0;  // k-blocks issued
       bool ok = true;
       for (UnitWalk<KIND> w(p, pair, npairs); ok && w.more(); w.next()) {
         const Unit un = find_unit(p, w.unit(p));
@@ -261,49 +267,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // the CTA's own matrix
         const int n0 = KIND == kUp || KIND == kUpWide ? un.nt * (kBN / 2)
                                    : un.nt * kBN + static_cast<int>(rank) * (kBN / 2);
+        // one k-loop per form of the operands, chosen once per unit: this thread
+        // issues every copy, and branches between them cost 8% of dX and dW
+        auto load_unit = [&](auto a_form, auto b_form) {
+          constexpr bool A_MN = decltype(a_form)::value, B_MN = decltype(b_form)::value;
 #pragma unroll 1
-        for (int seg = 0; ok && seg < 2; ++seg) {
-          const CUtensorMap* ma = &job.a[seg];
-          const CUtensorMap* mb = &job.b[KIND == kUp || KIND == kUpWide ? static_cast<int>(rank) : seg];
-          for (int kb = 0; kb < job.kb[seg]; ++kb) {
-            if (!mbar_wait(&ctrl->empty[s], ph ^ 1u, abort_flag, status)) {
-              ok = false;
-              break;
-            }
-            const uint32_t fb_local = smem_u32(&ctrl->full[s]);
-            if (rank == 0) mbar_arrive_expect_tx(&ctrl->full[s], 2 * L::STAGE_BYTES);
-            const uint32_t fb = rank == 0 ? fb_local : mapa_shared(fb_local, 0);
-            const uint32_t a_dst = tiles + s * L::STAGE_BYTES;
-            const uint32_t b_dst = a_dst + L::A_BYTES;
-            // A is read by the few column tiles of its rows at about the same
-            // time (transposed operands of dW: evict-first took the launch from
-            // 708 to 660 cycles a k-block); B by every row tile: kept in L2
-            if (job.a_mn) {
-              const uint64_t stream = l2_evict_first();
-              tma_load_2d_pair_hint(a_dst, ma, fb, m0, kb * BK, stream);
-              tma_load_2d_pair_hint(a_dst + 8192, ma, fb, m0 + 64, kb * BK, stream);
-            } else {
-              tma_load_2d_pair(a_dst, ma, fb, kb * BK, m0);
-            }
-            const uint64_t keep = l2_evict_last();
-            if (job.b_mn) {
-              tma_load_2d_pair_hint(b_dst, mb, fb, n0, kb * BK, keep);
-              tma_load_2d_pair_hint(b_dst + 8192, mb, fb, n0 + 64, kb * BK, keep);
-            } else {
-              tma_load_2d_pair_hint(b_dst, mb, fb, kb * BK, n0, keep);
-            }
-            issued |= 1u << s;
-            issued_ph = (issued_ph & ~(1u << s)) | (ph << s);
-            if (++s == STAGES) {
-              s = 0;
-              ph ^= 1u;
+          for (int seg = 0; ok && seg < 2; ++seg) {
+            const CUtensorMap* ma = &job.a[seg];
+            const CUtensorMap* mb =
+                &job.b[KIND == kUp || KIND == kUpWide ? static_cast<int>(rank) : seg];
+            const int k_end = job.kb[seg] * BK;
+#pragma unroll 1
+            for (int k = 0; k < k_end; k += BK) {
+              if (!mbar_wait(&ctrl->empty[s], ph ^ 1u, abort_flag, status)) {
+                ok = false;
+                break;
+              }
+              if (rank == 0) mbar_arrive_expect_tx(&ctrl->full[s], 2 * L::STAGE_BYTES);
+              const uint32_t fb = full0 + s * 8;
+              const uint32_t a_dst = tiles + s * L::STAGE_BYTES;
+              const uint32_t b_dst = a_dst + L::A_BYTES;
+              if constexpr (A_MN) {
+                tma_load_2d_pair_hint(a_dst, ma, fb, m0, k, stream);
+                tma_load_2d_pair_hint(a_dst + 8192, ma, fb, m0 + 64, k, stream);
+              } else {
+                tma_load_2d_pair(a_dst, ma, fb, k, m0);
+              }
+              if constexpr (B_MN) {
+                tma_load_2d_pair_hint(b_dst, mb, fb, n0, k, keep);
+                tma_load_2d_pair_hint(b_dst + 8192, mb, fb, n0 + 64, k, keep);
+              } else {
+                tma_load_2d_pair_hint(b_dst, mb, fb, k, n0, keep);
+              }
+              ++issued;
+              if (++s == STAGES) {
+                s = 0;
+                ph ^= 1u;
+              }
             }
           }
+        };
+        if constexpr (KIND == kGradAct || KIND == kGradActWide) {
+          load_unit(std::false_type{}, std::true_type{});
+        } else if constexpr (KIND == kGrads) {
+          if (job.a_mn) load_unit(std::true_type{}, std::true_type{});
+          else load_unit(std::false_type{}, std::true_type{});
+        } else {
+          load_unit(std::false_type{}, std::false_type{});
         }
       }
       if (rank == 0) {
-        for (int i = 0; i < STAGES; ++i)
-          if ((issued >> i) & 1u) mbar_drain(&ctrl->full[i], (issued_ph >> i) & 1u, status);
+        // every copy of both CTAs that the leader armed must land
+        for (uint32_t i = issued > STAGES ? issued - STAGES : 0u; i < issued; ++i)
+          mbar_drain(&ctrl->full[i % STAGES], (i / STAGES) & 1u, status);
       } else if (!ok) {
         // aborted: give this CTA's copies in flight, which land on the
         // leader's barriers, a bounded moment before shared memory goes
@@ -878,11 +894,11 @@ cudaError_t grad_act(const FfnBackward& f, cudaStream_t s) {
   PairJob& j = p.job[0];
   if (!map_kmajor(&j.a[0], f.dZ, f.T, f.D) || !map_mnmajor(&j.b[0], f.Wd, f.D, f.F))
     return cudaErrorInvalidValue;
+  j.b_mn = 1;
   if ((!map_chunk(&p.m[0], f.G, f.T, f.F) || !map_chunk(&p.m[1], f.U, f.T, f.F) ||
        !map_chunk(&p.m[2], f.dG, f.T, f.F) || !map_chunk(&p.m[3], f.dU, f.T, f.F)))
     return cudaErrorInvalidValue;
   j.kb[0] = tiles_of(f.D, BK);
-  j.b_mn = 1;
   j.m_tiles = tiles_of(f.T, 2 * BM);
   j.n_tiles = tiles_of(f.F, kBN);
   p.n_jobs = 1;
@@ -946,8 +962,8 @@ cudaError_t pair_grads(const FfnBackward& f, int which, cudaStream_t s) {
     if (!map_kmajor(&j.a[0], f.dG, T, F) || !map_kmajor(&j.a[1], f.dU, T, F) ||
         !map_mnmajor(&j.b[0], f.Wg, F, D) || !map_mnmajor(&j.b[1], f.Wu, F, D))
       return cudaErrorInvalidValue;
-    j.kb[0] = j.kb[1] = tiles_of(F, BK);
     j.b_mn = 1;
+    j.kb[0] = j.kb[1] = tiles_of(F, BK);
     j.m_tiles = tiles_of(T, 2 * BM);
     j.n_tiles = tiles_of(D, kBN);
     p.grad[p.n_jobs++] = GradOut{f.dX, f.T, f.D, 1.f, 0, 0, rows_on_sectors(D, {f.dX})};
