@@ -79,6 +79,7 @@ struct FfnForward {
   int T, D, F, act;
   DropArgs drop;
   uint16_t *Y, *G, *U, *A;  // G, U null: not kept
+  int ldo;                  // elements between the rows of G, U and A
   int* status;
   int num_sms;
 };
@@ -89,6 +90,7 @@ struct FfnBackward {
   float scale;  // 1 / (1 - p): dZ above times this is the gradient of Z
   int dw_fp32, accumulate;
   uint16_t *dX, *dG, *dU;
+  int ldg;  // elements between the rows of dG and dU
   void *dWg, *dWu, *dWd;
   int* status;
   int num_sms;

@@ -16,9 +16,14 @@ struct FfnLayout {
   size_t a, dg, du, dz, total;
 };
 
+// Rows of the workspace's [T, F] matrices start on 128-byte boundaries, so that
+// no copy of 128 bytes touches a fifth sector and outputs are stored as whole
+// sectors whatever F is (backward of T 3001, D 1352, F 3640: 189 -> 172 us).
+int64_t workspace_pitch(int64_t F) { return (F + 63) / 64 * 64; }
+
 FfnLayout ffn_layout(int64_t T, int64_t D, int64_t F) {
   FfnLayout L;
-  const size_t tf = up1024(static_cast<size_t>(T) * F * 2);
+  const size_t tf = up1024(static_cast<size_t>(T) * workspace_pitch(F) * 2);
   L.a = L.dg = kHeaderBytes;
   L.du = L.dg + tf;
   L.dz = L.du + tf;
@@ -87,6 +92,7 @@ ss_status ss_ffn_forward(const uint16_t* X, const uint16_t* Wg, const uint16_t* 
   f.X = X, f.Wg = Wg, f.Wu = Wu, f.Wd = Wd, f.residual = residual;
   f.T = static_cast<int>(T), f.D = static_cast<int>(D), f.F = static_cast<int>(F), f.act = act;
   f.Y = Y, f.G = G, f.U = U, f.A = save ? A : reinterpret_cast<uint16_t*>(ws + L.a);
+  f.ldo = static_cast<int>(save ? F : workspace_pitch(F));
   f.status = reinterpret_cast<int*>(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
@@ -144,6 +150,7 @@ ss_status ss_ffn_backward(const uint16_t* dY, const uint16_t* X, const uint16_t*
   b.dw_fp32 = dw_dtype == SS_FP32, b.accumulate = accumulate;
   b.dX = dX, b.dWg = dWg, b.dWu = dWu, b.dWd = dWd;
   b.dG = reinterpret_cast<uint16_t*>(ws + L.dg), b.dU = reinterpret_cast<uint16_t*>(ws + L.du);
+  b.ldg = static_cast<int>(workspace_pitch(F));
   b.status = reinterpret_cast<int*>(ws);
   cudaError_t e = cudaSuccess;
   if (d.mode != kDropNone) {

@@ -145,6 +145,7 @@ struct PairArgs {
   PairJob job[KIND == kGrads ? kMaxJobs : 1];
   int n_jobs, group_m;
   int T, D, F, act;
+  int ldo;  // elements between the rows of G, U, A (gate/up) or dG, dU (dA)
   const uint16_t *G_in, *U_in;
   uint16_t *G, *U, *A;
   // kUp: G, U, A (stores); kGradAct: G, U (loads), dG, dU (stores)
@@ -468,7 +469,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tmem_ld_wait(rg);
             tmem_ld_wait(ru);
             if (i == 1) release();
-            const size_t at = static_cast<size_t>(valid ? t : 0) * p.F + f0;
+            const size_t at = static_cast<size_t>(valid ? t : 0) * p.ldo + f0;
             const int nv = valid ? min(32, p.F - f0) : 0;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -539,7 +540,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 g[k] = pack_bf16x2(o[0], o[1]);
                 v[k] = pack_bf16x2(o[2], o[3]);
               }
-              const size_t at = static_cast<size_t>(t) * p.F + f0;
+              const size_t at = static_cast<size_t>(t) * p.ldo + f0;
               store_row32(p.G + at, g, nv, true);
               store_row32(p.U + at, v, nv, true);
             }
@@ -798,15 +799,15 @@ bool rows_on_sectors(int64_t cols, std::initializer_list<const void*> ps) {
 int tiles_of(int64_t n, int tile) { return static_cast<int>((n + tile - 1) / tile); }
 
 // K-major operand [rows, k]: boxes of 128 rows x 64 of k. MN-major operand
-// [k, cols]: boxes of 64 columns x 64 of k.
-bool map_kmajor(CUtensorMap* m, const uint16_t* p, int64_t rows, int64_t k) {
-  return make_bf16_map(m, p, k, rows, k * 2, BK, 128);
+// [k, cols]: boxes of 64 columns x 64 of k. ld: elements between rows.
+bool map_kmajor(CUtensorMap* m, const uint16_t* p, int64_t rows, int64_t k, int64_t ld) {
+  return make_bf16_map(m, p, k, rows, ld * 2, BK, 128);
 }
-bool map_mnmajor(CUtensorMap* m, const uint16_t* p, int64_t k, int64_t cols) {
-  return make_bf16_map(m, p, cols, k, cols * 2, 64, BK);
+bool map_mnmajor(CUtensorMap* m, const uint16_t* p, int64_t k, int64_t cols, int64_t ld) {
+  return make_bf16_map(m, p, cols, k, ld * 2, 64, BK);
 }
-bool map_chunk(CUtensorMap* m, const uint16_t* p, int64_t rows, int64_t cols) {
-  return make_bf16_map(m, p, cols, rows, cols * 2, 32, 128);
+bool map_chunk(CUtensorMap* m, const uint16_t* p, int64_t rows, int64_t cols, int64_t ld) {
+  return make_bf16_map(m, p, cols, rows, ld * 2, 32, 128);
 }
 
 // The units of two groups with different K, 0 .. n_a - 1 of kb_a k-blocks and
@@ -871,19 +872,19 @@ cudaError_t gate_up(const FfnForward& f, cudaStream_t s) {
   PairArgs<KIND> p = {};
   PairJob& j = p.job[0];
   const bool save = f.G != nullptr;
-  if (!map_kmajor(&j.a[0], f.X, f.T, f.D) || !map_kmajor(&j.b[0], f.Wg, f.F, f.D) ||
-      !map_kmajor(&j.b[1], f.Wu, f.F, f.D))
+  if (!map_kmajor(&j.a[0], f.X, f.T, f.D, f.D) || !map_kmajor(&j.b[0], f.Wg, f.F, f.D, f.D) ||
+      !map_kmajor(&j.b[1], f.Wu, f.F, f.D, f.D))
     return cudaErrorInvalidValue;
   if (KIND == kUp &&
-      (!map_chunk(&p.m[2], f.A, f.T, f.F) ||
-       (save && (!map_chunk(&p.m[0], f.G, f.T, f.F) || !map_chunk(&p.m[1], f.U, f.T, f.F)))))
+      (!map_chunk(&p.m[2], f.A, f.T, f.F, f.ldo) ||
+       (save && (!map_chunk(&p.m[0], f.G, f.T, f.F, f.ldo) || !map_chunk(&p.m[1], f.U, f.T, f.F, f.ldo)))))
     return cudaErrorInvalidValue;
   j.kb[0] = tiles_of(f.D, BK);
   j.m_tiles = tiles_of(f.T, 2 * BM);
   j.n_tiles = tiles_of(f.F, kBN / 2);
   p.n_jobs = 1;
   p.T = f.T, p.D = f.D, p.F = f.F, p.act = f.act, p.save = save;
-  p.G = f.G, p.U = f.U, p.A = f.A;
+  p.ldo = f.ldo, p.G = f.G, p.U = f.U, p.A = f.A;
   p.status = f.status;
   return launch_pair(p, f.num_sms, s);
 }
@@ -892,18 +893,18 @@ template <int KIND>
 cudaError_t grad_act(const FfnBackward& f, cudaStream_t s) {
   PairArgs<KIND> p = {};
   PairJob& j = p.job[0];
-  if (!map_kmajor(&j.a[0], f.dZ, f.T, f.D) || !map_mnmajor(&j.b[0], f.Wd, f.D, f.F))
+  if (!map_kmajor(&j.a[0], f.dZ, f.T, f.D, f.D) || !map_mnmajor(&j.b[0], f.Wd, f.D, f.F, f.F))
     return cudaErrorInvalidValue;
   j.b_mn = 1;
-  if ((!map_chunk(&p.m[0], f.G, f.T, f.F) || !map_chunk(&p.m[1], f.U, f.T, f.F) ||
-       !map_chunk(&p.m[2], f.dG, f.T, f.F) || !map_chunk(&p.m[3], f.dU, f.T, f.F)))
+  if ((!map_chunk(&p.m[0], f.G, f.T, f.F, f.F) || !map_chunk(&p.m[1], f.U, f.T, f.F, f.F) ||
+       !map_chunk(&p.m[2], f.dG, f.T, f.F, f.ldg) || !map_chunk(&p.m[3], f.dU, f.T, f.F, f.ldg)))
     return cudaErrorInvalidValue;
   j.kb[0] = tiles_of(f.D, BK);
   j.m_tiles = tiles_of(f.T, 2 * BM);
   j.n_tiles = tiles_of(f.F, kBN);
   p.n_jobs = 1;
   p.T = f.T, p.D = f.D, p.F = f.F, p.act = f.act, p.scale = f.scale;
-  p.G_in = f.G, p.U_in = f.U, p.G = f.dG, p.U = f.dU;
+  p.G_in = f.G, p.U_in = f.U, p.ldo = f.ldg, p.G = f.dG, p.U = f.dU;
   p.status = f.status;
   return launch_pair(p, f.num_sms, s);
 }
@@ -911,11 +912,11 @@ cudaError_t grad_act(const FfnBackward& f, cudaStream_t s) {
 }  // namespace
 
 cudaError_t pair_gate_up(const FfnForward& f, cudaStream_t s) {
-  return rows_on_sectors(f.F, {f.G, f.U, f.A}) ? gate_up<kUpWide>(f, s) : gate_up<kUp>(f, s);
+  return rows_on_sectors(f.ldo, {f.G, f.U, f.A}) ? gate_up<kUpWide>(f, s) : gate_up<kUp>(f, s);
 }
 
 cudaError_t pair_grad_act(const FfnBackward& f, cudaStream_t s) {
-  return tiles_of(f.D, BK) >= kActWideKb && rows_on_sectors(f.F, {f.dG, f.dU})
+  return tiles_of(f.D, BK) >= kActWideKb && rows_on_sectors(f.ldg, {f.dG, f.dU})
              ? grad_act<kGradActWide>(f, s)
              : grad_act<kGradAct>(f, s);
 }
@@ -923,7 +924,7 @@ cudaError_t pair_grad_act(const FfnBackward& f, cudaStream_t s) {
 cudaError_t pair_down(const FfnForward& f, cudaStream_t s) {
   PairArgs<kDown> p = {};
   PairJob& j = p.job[0];
-  if (!map_kmajor(&j.a[0], f.A, f.T, f.F) || !map_kmajor(&j.b[0], f.Wd, f.D, f.F))
+  if (!map_kmajor(&j.a[0], f.A, f.T, f.F, f.ldo) || !map_kmajor(&j.b[0], f.Wd, f.D, f.F, f.F))
     return cudaErrorInvalidValue;
   j.kb[0] = tiles_of(f.F, BK);
   j.m_tiles = tiles_of(f.T, 2 * BM);
@@ -946,7 +947,8 @@ cudaError_t pair_grads(const FfnBackward& f, int which, cudaStream_t s) {
     void* out[3] = {f.dWg, f.dWu, f.dWd};
     for (int i = 0; i < 3; ++i) {
       PairJob& j = p.job[p.n_jobs];
-      if (!map_mnmajor(&j.a[0], a[i], T, rows[i]) || !map_mnmajor(&j.b[0], b[i], T, cols[i]))
+      if (!map_mnmajor(&j.a[0], a[i], T, rows[i], i == 2 ? D : f.ldg) ||
+          !map_mnmajor(&j.b[0], b[i], T, cols[i], cols[i]))
         return cudaErrorInvalidValue;
       j.kb[0] = tiles_of(T, BK);
       j.a_mn = j.b_mn = 1;
@@ -959,8 +961,8 @@ cudaError_t pair_grads(const FfnBackward& f, int which, cudaStream_t s) {
   }
   if (which & kDoX) {  // dX = dG Wg + dU Wu: K = F twice
     PairJob& j = p.job[p.n_jobs];
-    if (!map_kmajor(&j.a[0], f.dG, T, F) || !map_kmajor(&j.a[1], f.dU, T, F) ||
-        !map_mnmajor(&j.b[0], f.Wg, F, D) || !map_mnmajor(&j.b[1], f.Wu, F, D))
+    if (!map_kmajor(&j.a[0], f.dG, T, F, f.ldg) || !map_kmajor(&j.a[1], f.dU, T, F, f.ldg) ||
+        !map_mnmajor(&j.b[0], f.Wg, F, D, D) || !map_mnmajor(&j.b[1], f.Wu, F, D, D))
       return cudaErrorInvalidValue;
     j.b_mn = 1;
     j.kb[0] = j.kb[1] = tiles_of(F, BK);

@@ -57,6 +57,7 @@ struct SplitArgs {
   SplitJob job[KIND == kSGradW ? kSplitMaxJobs : 1];
   int n_jobs, wait;
   int T, D, F, act;
+  int ldo;  // elements between the rows of G, U, A (gate/up) or dG, dU (dA)
   const uint16_t *residual, *G_in, *U_in;
   uint16_t *Y, *G, *U, *A;  // kSUp: outputs (G null: not kept); kSGradAct: dG, dU in G, U
   DropArgs drop;
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
           const int row = row0 + i * kStep;
           if constexpr (KIND == kSUp) {
             if (row >= p.T || m >= p.F) continue;
-            const size_t o = static_cast<size_t>(row) * p.F + m;
+            const size_t o = static_cast<size_t>(row) * p.ldo + m;
             F4 a;
             dispatch_act(p.act, [&](auto act) {
               constexpr int ACT = decltype(act)::value;
@@ -387,7 +388,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
             store_bf16x4(p.Y + o, y);
           } else if constexpr (KIND == kSGradAct) {
             if (row >= p.T || m >= p.F) continue;
-            const size_t o = static_cast<size_t>(row) * p.F + m;
+            const size_t o = static_cast<size_t>(row) * p.ldo + m;
             dispatch_act(p.act, [&](auto act) {
               constexpr int ACT = decltype(act)::value;
 #pragma unroll
@@ -483,12 +484,13 @@ cudaError_t launch_split(SplitArgs<KIND>& p, const SplitPlan& plan, cudaStream_t
 }
 
 // K-major operand [rows, k]: boxes of box_rows x 64 of k
-bool map_kmajor(CUtensorMap* m, const uint16_t* p, int64_t rows, int64_t k, int box_rows) {
-  return make_bf16_map(m, p, k, rows, k * 2, BK, box_rows);
+bool map_kmajor(CUtensorMap* m, const uint16_t* p, int64_t rows, int64_t k, int64_t ld,
+                int box_rows) {
+  return make_bf16_map(m, p, k, rows, ld * 2, BK, box_rows);
 }
 // MN-major operand [k, cols]: boxes of 64 columns x 64 of k
-bool map_mnmajor(CUtensorMap* m, const uint16_t* p, int64_t k, int64_t cols) {
-  return make_bf16_map(m, p, cols, k, cols * 2, 64, BK);
+bool map_mnmajor(CUtensorMap* m, const uint16_t* p, int64_t k, int64_t cols, int64_t ld) {
+  return make_bf16_map(m, p, cols, k, ld * 2, 64, BK);
 }
 
 }  // namespace
@@ -524,8 +526,8 @@ cudaError_t split_gate_up(const FfnForward& f, const SplitPlan& plan, cudaStream
   SplitArgs<kSUp> p = {};
   SplitJob& j = p.job[0];
   const int bn = plan.bn;
-  if (!map_kmajor(&j.a[0], f.Wg, f.F, f.D, 64) || !map_kmajor(&j.a[1], f.Wu, f.F, f.D, 64) ||
-      !map_kmajor(&j.b[0], f.X, f.T, f.D, bn))
+  if (!map_kmajor(&j.a[0], f.Wg, f.F, f.D, f.D, 64) || !map_kmajor(&j.a[1], f.Wu, f.F, f.D, f.D, 64) ||
+      !map_kmajor(&j.b[0], f.X, f.T, f.D, f.D, bn))
     return cudaErrorInvalidValue;
   j.kb[0] = tiles_of(f.D, BK);
   j.m_tiles = tiles_of(f.F, 64);
@@ -533,7 +535,7 @@ cudaError_t split_gate_up(const FfnForward& f, const SplitPlan& plan, cudaStream
   p.n_jobs = 1;
   p.wait = kWaitFirst;
   p.T = f.T, p.D = f.D, p.F = f.F, p.act = f.act;
-  p.G = f.G, p.U = f.U, p.A = f.A;
+  p.ldo = f.ldo, p.G = f.G, p.U = f.U, p.A = f.A;
   p.status = f.status;
   return launch_split(p, plan, s);
 }
@@ -542,7 +544,7 @@ cudaError_t split_down(const FfnForward& f, const SplitPlan& plan, cudaStream_t 
   SplitArgs<kSDown> p = {};
   SplitJob& j = p.job[0];
   const int bn = plan.bn;
-  if (!map_kmajor(&j.a[0], f.Wd, f.D, f.F, 128) || !map_kmajor(&j.b[0], f.A, f.T, f.F, bn))
+  if (!map_kmajor(&j.a[0], f.Wd, f.D, f.F, f.F, 128) || !map_kmajor(&j.b[0], f.A, f.T, f.F, f.ldo, bn))
     return cudaErrorInvalidValue;
   j.kb[0] = tiles_of(f.F, BK);
   j.m_tiles = tiles_of(f.D, BM);
@@ -559,7 +561,7 @@ cudaError_t split_grad_act(const FfnBackward& f, const SplitPlan& plan, cudaStre
   SplitArgs<kSGradAct> p = {};
   SplitJob& j = p.job[0];
   const int bn = plan.bn;
-  if (!map_mnmajor(&j.a[0], f.Wd, f.D, f.F) || !map_kmajor(&j.b[0], f.dZ, f.T, f.D, bn))
+  if (!map_mnmajor(&j.a[0], f.Wd, f.D, f.F, f.F) || !map_kmajor(&j.b[0], f.dZ, f.T, f.D, f.D, bn))
     return cudaErrorInvalidValue;
   j.kb[0] = tiles_of(f.D, BK);
   j.a_mn = 1;
@@ -568,7 +570,7 @@ cudaError_t split_grad_act(const FfnBackward& f, const SplitPlan& plan, cudaStre
   p.n_jobs = 1;
   p.wait = kWaitFirst;
   p.T = f.T, p.D = f.D, p.F = f.F, p.act = f.act, p.scale = f.scale;
-  p.G_in = f.G, p.U_in = f.U, p.G = f.dG, p.U = f.dU;
+  p.G_in = f.G, p.U_in = f.U, p.ldo = f.ldg, p.G = f.dG, p.U = f.dU;
   p.status = f.status;
   return launch_split(p, plan, s);
 }
@@ -577,8 +579,8 @@ cudaError_t split_grad_x(const FfnBackward& f, const SplitPlan& plan, cudaStream
   SplitArgs<kSGradX> p = {};
   SplitJob& j = p.job[0];
   const int bn = plan.bn;
-  if (!map_mnmajor(&j.a[0], f.Wg, f.F, f.D) || !map_mnmajor(&j.a[1], f.Wu, f.F, f.D) ||
-      !map_kmajor(&j.b[0], f.dG, f.T, f.F, bn) || !map_kmajor(&j.b[1], f.dU, f.T, f.F, bn))
+  if (!map_mnmajor(&j.a[0], f.Wg, f.F, f.D, f.D) || !map_mnmajor(&j.a[1], f.Wu, f.F, f.D, f.D) ||
+      !map_kmajor(&j.b[0], f.dG, f.T, f.F, f.ldg, bn) || !map_kmajor(&j.b[1], f.dU, f.T, f.F, f.ldg, bn))
     return cudaErrorInvalidValue;
   j.kb[0] = j.kb[1] = tiles_of(f.F, BK);
   j.a_mn = 1;
@@ -602,7 +604,8 @@ cudaError_t split_grad_w(const FfnBackward& f, const SplitPlan& plan, cudaStream
   void* out[3] = {f.dWg, f.dWu, f.dWd};
   for (int i = 0; i < 3; ++i) {
     SplitJob& j = p.job[i];
-    if (!map_mnmajor(&j.a[0], m_side[i], T, cols[i]) || !map_mnmajor(&j.b[0], n_side[i], T, rows[i]))
+    if (!map_mnmajor(&j.a[0], m_side[i], T, cols[i], cols[i]) ||
+        !map_mnmajor(&j.b[0], n_side[i], T, rows[i], i == 2 ? D : f.ldg))
       return cudaErrorInvalidValue;
     j.kb[0] = tiles_of(T, BK);
     j.a_mn = j.b_mn = 1;
