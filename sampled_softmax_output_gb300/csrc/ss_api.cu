@@ -19,6 +19,7 @@
 #include "ss.h"
 #include "ss_internal.h"
 #include "ss_ptx.cuh"
+#include "ss_shared.h"
 
 namespace ss {
 
@@ -35,7 +36,7 @@ struct Layout {
   int64_t ldT8, ldC8;  // row pitch (bytes) of the transposed e4m3 / e5m2 copies
 };
 
-constexpr size_t kHdrBytes = kHeaderBytes;  // int32 status, int32 U, padding, FP8 amax words
+constexpr size_t kHdrBytes = 1024;  // int32 status, int32 U, padding, FP8 amax words
 constexpr size_t kHdrAmax = 64;     // byte offset of float amax[2] (max |H|, max |W_c|)
 constexpr size_t kHdrBar = 72;      // uint32 bar[2] of k_h_prep_beside (arrivals, gave up)
 constexpr size_t kHdrQuant = 80;    // ss_quantize_e4m3's own float amax + int32 status
@@ -716,6 +717,8 @@ void trace_post(cudaStream_t s) {
 
 }  // namespace
 
+// Shared with the entry points of ss_block.h.
+static_assert(kHdrBytes == kHeaderBytes, "one workspace header");
 int current_num_sms() { return num_sms_current(); }
 ss_status record_failure(const char* what, cudaError_t e) { return fail(what, e); }
 bool make_bf16_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,

@@ -1,6 +1,6 @@
 // ss_ffn.cuh -- what the kernels of the gated feed-forward block share: the
-// activations with their slopes, the rounding of a row of outputs, and the
-// launchers of the two families of kernels.
+// activations with their slopes, the problems as the launchers take them, and
+// the choice between the two families of kernels.
 //
 // The block's seven products are all of the form Out[n, m] = sum_k B[n, k] A[m, k]
 // with operands that TMA brings to shared memory as they lie (K-major, or
@@ -21,6 +21,7 @@
 #include "ss_dropout.cuh"
 #include "ss_internal.h"
 #include "ss_ptx.cuh"
+#include "ss_shared.h"
 
 namespace ss {
 
@@ -67,6 +68,20 @@ __device__ __forceinline__ void dispatch_act(int act, F&& fn) {
     case SS_ACT_GELU_TANH: fn(std::integral_constant<int, SS_ACT_GELU_TANH>{}); break;
     default: fn(std::integral_constant<int, SS_ACT_RELU>{}); break;
   }
+}
+
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// 32 bytes per lane, one whole sector (32-byte aligned addresses).
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&r)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }

@@ -8,8 +8,6 @@
 
 #include <utility>
 
-#include "ss.h"
-
 namespace ss {
 
 // Sets a kernel's dynamic shared-memory limit and the largest shared-memory
@@ -47,27 +45,6 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
   if (le == cudaSuccess) ++g_kernel_launches;
   return le;
 }
-
-// Shared by the entry points of ss.h and ss_block.h (ss_api.cu):
-// the workspace header's size (its first word is the status word)
-constexpr size_t kHeaderBytes = 1024;
-// SM count of the current device, or <= 0 on failure
-int current_num_sms();
-// keeps the text for ss_last_error(); returns SS_ERR_CUDA
-ss_status record_failure(const char* what, cudaError_t e);
-// row-major bf16 [outer, inner], row_bytes between rows, boxes of box_outer
-// rows x box_inner elements (swizzle = the bytes of a box row, 64 or 128)
-bool make_bf16_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
-                   uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer);
-// One stage of the launch trace (ss_trace_begin), from construction to the end
-// of the scope.
-struct StageTrace {
-  StageTrace(cudaStream_t s, const char* name);
-  ~StageTrace();
-  StageTrace(const StageTrace&) = delete;
-  StageTrace& operator=(const StageTrace&) = delete;
-  cudaStream_t s_;
-};
 
 // Tile widths of the GEMMs (output columns per tile).
 constexpr int kBnLogits = 256;  // logit tiles: forward and softmax-gradient
