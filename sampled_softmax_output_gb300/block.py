@@ -158,21 +158,29 @@ def _act(act):
 
 def _block_args(X, Wg, Wu, Wd, ws):
     """Checked (device index, T, D, F)."""
-    if not (isinstance(X, torch.Tensor) and X.dtype is _BF16 and X.is_cuda and X.is_contiguous()):
-        _need(X, "X", _BF16)
+    try:
+        index = X.get_device()
+        T, D = X.shape
+        up = Wg.shape
+        F = up[0]
+        if (index >= 0 and X.dtype is Wg.dtype is Wu.dtype is Wd.dtype is _BF16
+                and ws.dtype is _U8 and up[1] == D and Wu.shape == up and Wd.shape == (D, F)
+                and Wg.get_device() == Wu.get_device() == Wd.get_device() == ws.get_device()
+                == index and X.is_contiguous() and Wg.is_contiguous() and Wu.is_contiguous()
+                and Wd.is_contiguous() and ws.is_contiguous()):
+            return index, T, D, F
+    except (AttributeError, IndexError, ValueError):
+        pass
+    _need(X, "X", _BF16)
     if X.dim() != 2:
         raise ValueError(f"X must be [T, D], got {tuple(X.shape)}")
-    index = X.get_device()
     T, D = X.shape
-    F = Wg.shape[0] if isinstance(Wg, torch.Tensor) and Wg.dim() else 0
-    up = (F, D)
-    if not (_fits(Wg, _BF16, index, up) and _fits(Wu, _BF16, index, up)
-            and _fits(Wd, _BF16, index, (D, F))):
-        for t, name, shape in ((Wg, "Wg", up), (Wu, "Wu", up), (Wd, "Wd", (D, F))):
-            _need(t, name, _BF16, X.device, shape)
-    if not _fits(ws, _U8, index, ws.shape):
-        _need(ws, "workspace", _U8, X.device)
-    return index, T, D, F
+    _need(Wg, "Wg", _BF16, X.device)
+    F = Wg.shape[0] if Wg.dim() else 0
+    for t, name, shape in ((Wg, "Wg", (F, D)), (Wu, "Wu", (F, D)), (Wd, "Wd", (D, F))):
+        _need(t, name, _BF16, X.device, shape)
+    _need(ws, "workspace", _U8, X.device)
+    raise AssertionError("unreachable: one of the checks above fails")
 
 
 def ffn_forward(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: torch.Tensor,
@@ -182,8 +190,8 @@ def ffn_forward(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: torch.T
     """The gated feed-forward block (ss_ffn_forward):
         Y = residual + dropout((act(X Wg^T) * (X Wu^T)) Wd^T)
     X [T, D], Wg, Wu [F, D], Wd [D, F], all bf16. Returns Y, or with save=True
-    (Y, (G, U, A)), what ffn_backward needs. out may be residual. p, seed and
-    offset as for dropout()."""
+    (Y, saved), saved [3, T, F] holding G, U and A, what ffn_backward needs. out
+    may be residual. p, seed and offset as for dropout()."""
     index, T, D, F = _block_args(X, Wg, Wu, Wd, ws)
     if residual is not None and not _fits(residual, _BF16, index, X.shape):
         _need(residual, "residual", _BF16, X.device, X.shape)
@@ -191,14 +199,15 @@ def ffn_forward(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: torch.T
         out = torch.empty_like(X)
     elif not _fits(out, _BF16, index, X.shape):
         _need(out, "out", _BF16, X.device, X.shape)
-    saved, kept = None, (None, None, None)
+    saved, g, u, a = None, None, None, None
     if save:
-        dev = X.device
-        saved = tuple([torch.empty((T, F), dtype=_BF16, device=dev) for _ in range(3)])
-        kept = [t.data_ptr() for t in saved]
+        saved = torch.empty((3, T, F), dtype=_BF16, device=X.device)
+        g = saved.data_ptr()
+        u = g + 2 * T * F
+        a = u + 2 * T * F
     _call(_lib.ss_ffn_forward, index, X.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(),
           None if residual is None else residual.data_ptr(), T, D, F, _act(act),
-          _dropout_spec(p, seed, offset, X.device), out.data_ptr(), *kept, ws.data_ptr(),
+          _dropout_spec(p, seed, offset, X.device), out.data_ptr(), g, u, a, ws.data_ptr(),
           ws.numel())
     return (out, saved) if save else out
 
@@ -208,10 +217,11 @@ def ffn_backward(dY: torch.Tensor, X: torch.Tensor, Wg: torch.Tensor, Wu: torch.
                  seed=0, offset: int = 0, dw_dtype=torch.float32, accumulate: bool = False,
                  dX: torch.Tensor | None = None, dWg: torch.Tensor | None = None,
                  dWu: torch.Tensor | None = None, dWd: torch.Tensor | None = None):
-    """The gradients of ffn_forward (ss_ffn_backward) from dY [T, D] and the
-    `saved` tensors: {"dX", "dWg", "dWu", "dWd"}, dX bf16 and the weight
-    gradients of dw_dtype (fp32 or bf16), zero-filled when accumulate=True and
-    none is given. The gradient of the residual is dY itself."""
+    """The gradients of ffn_forward (ss_ffn_backward) from dY [T, D] and `saved`
+    (that of ffn_forward, or any three [T, F] tensors G, U, A): {"dX", "dWg",
+    "dWu", "dWd"}, dX bf16 and the weight gradients of dw_dtype (fp32 or bf16),
+    zero-filled when accumulate=True and none is given. The gradient of the
+    residual is dY itself."""
     index, T, D, F = _block_args(X, Wg, Wu, Wd, ws)
     dev = X.device
     dw = _DTYPES.get(dw_dtype)
@@ -219,24 +229,38 @@ def ffn_backward(dY: torch.Tensor, X: torch.Tensor, Wg: torch.Tensor, Wu: torch.
         raise TypeError(f"dw_dtype must be torch.bfloat16 or torch.float32, got {dw_dtype}")
     if not _fits(dY, _BF16, index, X.shape):
         _need(dY, "dY", _BF16, dev, X.shape)
-    G, U, A = saved
-    for t, name in ((G, "G"), (U, "U"), (A, "A")):
-        if not _fits(t, _BF16, index, (T, F)):
-            _need(t, name, _BF16, dev, (T, F))
+    if isinstance(saved, torch.Tensor):
+        if not _fits(saved, _BF16, index, (3, T, F)):
+            _need(saved, "saved", _BF16, dev, (3, T, F))
+        g = saved.data_ptr()
+        u = g + 2 * T * F
+        a = u + 2 * T * F
+    else:
+        G, U, A = saved
+        for t, name in ((G, "G"), (U, "U"), (A, "A")):
+            if not _fits(t, _BF16, index, (T, F)):
+                _need(t, name, _BF16, dev, (T, F))
+        g, u, a = G.data_ptr(), U.data_ptr(), A.data_ptr()
     if dX is None:
         dX = torch.empty_like(X)
     elif not _fits(dX, _BF16, index, X.shape):
         _need(dX, "dX", _BF16, dev, X.shape)
     new = torch.zeros if accumulate else torch.empty
-    grads = []
-    for t, name, shape in ((dWg, "dWg", (F, D)), (dWu, "dWu", (F, D)), (dWd, "dWd", (D, F))):
-        if t is None:
-            t = new(shape, dtype=dw_dtype, device=dev)
-        elif not _fits(t, dw_dtype, index, shape):
-            _need(t, name, dw_dtype, dev, shape)
-        grads.append(t)
+    up, down = (F, D), (D, F)
+    if dWg is None:
+        dWg = new(up, dtype=dw_dtype, device=dev)
+    elif not _fits(dWg, dw_dtype, index, up):
+        _need(dWg, "dWg", dw_dtype, dev, up)
+    if dWu is None:
+        dWu = new(up, dtype=dw_dtype, device=dev)
+    elif not _fits(dWu, dw_dtype, index, up):
+        _need(dWu, "dWu", dw_dtype, dev, up)
+    if dWd is None:
+        dWd = new(down, dtype=dw_dtype, device=dev)
+    elif not _fits(dWd, dw_dtype, index, down):
+        _need(dWd, "dWd", dw_dtype, dev, down)
     _call(_lib.ss_ffn_backward, index, dY.data_ptr(), X.data_ptr(), Wg.data_ptr(), Wu.data_ptr(),
-          Wd.data_ptr(), G.data_ptr(), U.data_ptr(), A.data_ptr(), T, D, F, _act(act),
-          _dropout_spec(p, seed, offset, dev), dw, 1 if accumulate else 0, dX.data_ptr(),
-          *[t.data_ptr() for t in grads], ws.data_ptr(), ws.numel())
-    return {"dX": dX, "dWg": grads[0], "dWu": grads[1], "dWd": grads[2]}
+          Wd.data_ptr(), g, u, a, T, D, F, _act(act), _dropout_spec(p, seed, offset, dev), dw,
+          1 if accumulate else 0, dX.data_ptr(), dWg.data_ptr(), dWu.data_ptr(), dWd.data_ptr(),
+          ws.data_ptr(), ws.numel())
+    return {"dX": dX, "dWg": dWg, "dWu": dWu, "dWd": dWd}
