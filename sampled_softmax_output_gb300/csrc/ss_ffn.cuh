@@ -119,8 +119,9 @@ cudaError_t launch_drop_mask(const uint16_t* x, int64_t n, const DropArgs& drop,
 //
 // A problem is N rows of output (tokens, or rows of a weight gradient) by M
 // columns, K = 64 kb. The two families' times are estimated in microseconds
-// from constants fitted to graph-replayed calls on one GB300 (T 1 to 4096, D
-// 256 to 4096, F 256 to 12288); the fits are within about 2 us up to 30.
+// with constants fitted on one GB300 to 110 problem sizes (T 65 to 16000, D 64
+// to 4096, F 64 to 12288), every product in every form: what the estimates pick
+// takes 2.4% longer than the best form on average.
 
 // The choice for one problem on the split family.
 struct SplitPlan {
@@ -128,9 +129,9 @@ struct SplitPlan {
   float us;
 };
 
-// A CTA pair takes 0.36 us a k-block; launch, first loads, the last tile's
-// epilogue and the exit together 5.5 us.
-constexpr float kPairUsPerKb = 0.36f, kPairUsFixed = 5.5f;
+// A CTA pair's time per k-block; launch, first loads, the last tile's epilogue
+// and the exit together.
+constexpr float kPairUsPerKb = 0.35f, kPairUsFixed = 5.7f;
 // out_us: what the outputs of the epilogue cost beyond one bf16 value (gate/up
 // and dA: two to four values read or written for each sum).
 inline float pair_us(int64_t units, int64_t kb, float out_us, int num_sms) {

@@ -51,9 +51,10 @@ int64_t units(int64_t rows, int64_t cols, int col_tile = 256) {
   return cdiv(rows, 256) * cdiv(cols, col_tile);
 }
 
-// What an epilogue's further outputs cost, in us: gate/up writes G, U and A,
-// dA reads G and U and writes dG and dU.
-constexpr float kUpOutUs = 0.8f, kActOutUs = 1.3f;
+// What an epilogue's further outputs cost on either family, in us (on split
+// tiles, per 64 tokens): gate/up writes G, U and A, dA reads G and U and writes
+// dG and dU.
+constexpr float kPairUpUs = 0.6f, kPairActUs = 0.45f, kSplitUpUs = 2.9f, kSplitActUs = 2.f;
 
 bool known_act(int act) { return act >= SS_ACT_SILU && act <= SS_ACT_RELU; }
 
@@ -98,8 +99,8 @@ ss_status ss_ffn_forward(const uint16_t* X, const uint16_t* Wg, const uint16_t* 
   cudaError_t e;
   {
     StageTrace trace(s, "ffn_gate_up");
-    const SplitPlan plan = split_plan(T, F, 64, cdiv(D, 64), kUpOutUs, false, f.num_sms);
-    e = pair_us(units(T, F, 128), cdiv(D, 64), 2.f, f.num_sms) < plan.us ? pair_gate_up(f, s)
+    const SplitPlan plan = split_plan(T, F, 64, cdiv(D, 64), kSplitUpUs, false, f.num_sms);
+    e = pair_us(units(T, F, 128), cdiv(D, 64), kPairUpUs, f.num_sms) < plan.us ? pair_gate_up(f, s)
                                                                       : split_gate_up(f, plan, s);
   }
   if (e != cudaSuccess) return record_failure("ss_ffn_forward (gate/up)", e);
@@ -162,8 +163,8 @@ ss_status ss_ffn_backward(const uint16_t* dY, const uint16_t* X, const uint16_t*
   if (e != cudaSuccess) return record_failure("ss_ffn_backward (mask)", e);
   {
     StageTrace trace(s, "ffn_grad_act");
-    const SplitPlan plan = split_plan(T, F, 128, cdiv(D, 64), kActOutUs, false, b.num_sms);
-    e = pair_us(units(T, F), cdiv(D, 64), 2.f, b.num_sms) < plan.us ? pair_grad_act(b, s)
+    const SplitPlan plan = split_plan(T, F, 128, cdiv(D, 64), kSplitActUs, false, b.num_sms);
+    e = pair_us(units(T, F), cdiv(D, 64), kPairActUs, b.num_sms) < plan.us ? pair_grad_act(b, s)
                                                                     : split_grad_act(b, plan, s);
   }
   if (e != cudaSuccess) return record_failure("ss_ffn_backward (dG, dU)", e);

@@ -333,6 +333,15 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         const int row0 = nt * BN + n_first + n0;
         F4 v[kBatch];
         [[maybe_unused]] F4 w[kBatch];
+        // what else the epilogue reads, all of it on its way before the first use
+        // (Y may be the residual: a load after a store would have to wait for it)
+        if constexpr (KIND == kSDown) {
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i)
+            w[i] = p.residual && row0 + i * kStep < p.T && m < p.D
+                       ? load_bf16x4(p.residual + static_cast<size_t>(row0 + i * kStep) * p.D + m)
+                       : F4{{0.f, 0.f, 0.f, 0.f}};
+        }
         if constexpr (KIND == kSGradAct) {  // G and U of the same places
 #pragma unroll
           for (int i = 0; i < kBatch; ++i)
@@ -373,7 +382,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
           } else if constexpr (KIND == kSDown) {
             if (row >= p.T || m >= p.D) continue;
             const size_t o = static_cast<size_t>(row) * p.D + m;
-            F4 y = p.residual ? load_bf16x4(p.residual + o) : F4{{0.f, 0.f, 0.f, 0.f}};
+            F4& y = w[i];
             if (p.drop.mode == kDropNone) {
 #pragma unroll
               for (int k = 0; k < 4; ++k) y.v[k] += v[i].v[k];
@@ -495,21 +504,22 @@ bool map_mnmajor(CUtensorMap* m, const uint16_t* p, int64_t k, int64_t cols, int
 
 }  // namespace
 
-// A CTA alone on its SM takes 0.26 to 0.36 us a k-block (16 to 128 tokens: the
-// rate at which one SM takes operands in); two share that rate and hide each
-// other's gaps, a third waits for a place. A cluster's join costs a barrier,
-// and reading a partial tile from other SMs about as much as writing it.
+// A CTA alone on its SM takes 0.28 to 0.59 us a k-block (16 to 128 tokens, the
+// rate at which one CTA takes operands in); two on an SM share that rate and
+// hide each other's gaps, so that they hardly slow one another; a third waits
+// for a place. A cluster's join costs a barrier; the outputs' cost goes with the
+// tokens of a tile.
 SplitPlan split_plan(int64_t n, int64_t m, int m_tile, int64_t kb, float out_us, bool wide_only,
                      int num_sms) {
-  constexpr float kFixed = 3.f, kJoin = 0.8f, kTile = 0.7f;
+  constexpr float kFixed = 2.2f, kJoin = 0.1f, kTile = 1.15f;
   SplitPlan best{0, 0, 0.f};
   for (int bn = wide_only ? 128 : 16; bn <= 128; bn *= 2) {
     if (bn < 64 && n > bn) continue;  // narrower tiles only re-read the weights
-    const float per_kb = bn == 16 ? 0.26f : bn == 32 ? 0.28f : bn == 64 ? 0.32f : 0.36f;
+    const float per_kb = bn == 16 ? 0.28f : bn == 32 ? 0.3f : bn == 64 ? 0.364f : 0.59f;
     const int64_t tiles = ((n + bn - 1) / bn) * ((m + m_tile - 1) / m_tile);
     for (int S = 1; S <= kSplitMaxCluster && (S == 1 || kb / S >= 2); S *= 2) {
       const float share = static_cast<float>(tiles * S) / num_sms;
-      const float load = share <= 1.f ? 1.f : share <= 2.f ? 1.f + 0.25f * (share - 1.f) : share;
+      const float load = share <= 1.f ? 1.f : share <= 2.f ? 1.f + 0.18f * (share - 1.f) : 1.09f * share;
       const float us = kFixed + (S > 1 ? kJoin : 0.f) +
                        load * (per_kb * kb / S + (kTile + out_us) * bn / 64);
       // few tokens: the weights' bytes bound the kernel; every CTA has a place
