@@ -110,16 +110,21 @@ size_t ss_ffn_workspace_size(int64_t T, int64_t D, int64_t F); /* 0: invalid siz
  *   G, U, A [T, F] bf16 out: what the backward needs; all three, or all NULL
  *   (no backward follows). A is rounded to bf16 before the down projection,
  *   from G and U in fp32.
+ *   R [T, ss_ffn_low_bits_pitch(F)] bytes out, 32-byte aligned, or NULL: the
+ *   next four bits of G and of U for the backward, which make the error that
+ *   stems from their rounding to bf16 a sixteenth (only with G, U and A). What
+ *   lies past column F of a row is unspecified.
  * Sums are held in fp32. T = 0: nothing is enqueued.
  */
 ss_status ss_ffn_forward(const uint16_t* X, const uint16_t* Wg, const uint16_t* Wu,
                          const uint16_t* Wd, const uint16_t* residual, int64_t T, int64_t D,
                          int64_t F, int act, const ss_dropout_spec* drop, uint16_t* Y, uint16_t* G,
-                         uint16_t* U, uint16_t* A, void* workspace, size_t workspace_bytes,
-                         ss_stream stream);
+                         uint16_t* U, uint16_t* A, uint8_t* R, void* workspace,
+                         size_t workspace_bytes, ss_stream stream);
+int64_t ss_ffn_low_bits_pitch(int64_t F); /* F rounded up to 64; 0 if F <= 0 */
 
 /*
- * From dY [T, D] and the forward's G, U, A:
+ * From dY [T, D] and the forward's G, U, A (and R, or NULL: G and U as they are):
  *   dZ = dropout'(dY)   dA = dZ Wd   dG = dA U act'(G)   dU = dA act(G)
  *   dX = dG Wg + dU Wu  dWg = dG^T X  dWu = dU^T X  dWd = dZ^T A
  * (the gradient of the residual is dY itself; relu'(0) = 0).
@@ -132,8 +137,9 @@ ss_status ss_ffn_forward(const uint16_t* X, const uint16_t* Wg, const uint16_t* 
  */
 ss_status ss_ffn_backward(const uint16_t* dY, const uint16_t* X, const uint16_t* Wg,
                           const uint16_t* Wu, const uint16_t* Wd, const uint16_t* G,
-                          const uint16_t* U, const uint16_t* A, int64_t T, int64_t D, int64_t F,
-                          int act, const ss_dropout_spec* drop, int dw_dtype, int accumulate,
+                          const uint16_t* U, const uint16_t* A, const uint8_t* R, int64_t T,
+                          int64_t D, int64_t F, int act, const ss_dropout_spec* drop, int dw_dtype,
+                          int accumulate,
                           uint16_t* dX, void* dWg, void* dWu, void* dWd, void* workspace,
                           size_t workspace_bytes, ss_stream stream);
 

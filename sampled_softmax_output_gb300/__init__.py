@@ -609,5 +609,5 @@ def quantize_e4m3(x: torch.Tensor, ws: torch.Tensor):
 
 # The operators in front of the head (include/ss_block.h).
 from .block import (  # noqa: E402
-    ACTS, HEADER_BLOCK, MAX_F, DropoutSpec, dropout, dropout_backward, ffn_backward, ffn_forward,
-    ffn_workspace, ffn_workspace_size)
+    ACTS, HEADER_BLOCK, MAX_F, DropoutSpec, FfnSaved, dropout, dropout_backward, ffn_backward,
+    ffn_forward, ffn_workspace, ffn_workspace_size)

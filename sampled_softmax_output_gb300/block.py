@@ -40,10 +40,12 @@ def _declare(L):
     L.ss_dropout_backward.argtypes = [p, i64, i32, dp, p, p]
     L.ss_ffn_workspace_size.restype = sz
     L.ss_ffn_workspace_size.argtypes = [i64, i64, i64]
+    L.ss_ffn_low_bits_pitch.restype = i64
+    L.ss_ffn_low_bits_pitch.argtypes = [i64]
     L.ss_ffn_forward.restype = i32
-    L.ss_ffn_forward.argtypes = [p] * 5 + [i64, i64, i64, i32, dp] + [p] * 4 + [p, sz, p]
+    L.ss_ffn_forward.argtypes = [p] * 5 + [i64, i64, i64, i32, dp] + [p] * 5 + [p, sz, p]
     L.ss_ffn_backward.restype = i32
-    L.ss_ffn_backward.argtypes = ([p] * 8 + [i64, i64, i64, i32, dp, i32, i32] + [p] * 4
+    L.ss_ffn_backward.argtypes = ([p] * 9 + [i64, i64, i64, i32, dp, i32, i32] + [p] * 4
                                   + [p, sz, p])
 
 
@@ -149,6 +151,47 @@ def ffn_workspace(T: int, D: int, F: int, device=None) -> torch.Tensor:
     return ws
 
 
+class FfnSaved:
+    """What ffn_forward(save=True) keeps for ffn_backward: G, U and A ([T, F]
+    bf16, also saved[0], saved[1], saved[2]) and the low bits of G and U (R of
+    include/ss_block.h), in one buffer. They belong together: to change one of
+    them, pass three tensors of your own."""
+
+    __slots__ = ("buffer", "T", "F")
+
+    def __init__(self, T: int, F: int, device):
+        self.T, self.F = T, F
+        self.buffer = torch.empty((self._low_offset() + T * _low_pitch(F)) // 2, dtype=_BF16,
+                                  device=device)
+
+    def _low_offset(self) -> int:
+        return (6 * self.T * self.F + 31) // 32 * 32
+
+    def pointers(self):
+        """Device addresses of G, U, A and R."""
+        g, n = self.buffer.data_ptr(), 2 * self.T * self.F
+        return g, g + n, g + 2 * n, g + self._low_offset()
+
+    def __len__(self):
+        return 3
+
+    def __getitem__(self, i: int) -> torch.Tensor:
+        if not 0 <= i < 3:
+            raise IndexError(i)
+        n = self.T * self.F
+        return self.buffer[i * n:(i + 1) * n].view(self.T, self.F)
+
+    def low_bits(self) -> torch.Tensor:
+        """R [T, F]: uint8, G's half byte low, U's high."""
+        pitch = _low_pitch(self.F)
+        raw = self.buffer.view(torch.uint8)[self._low_offset():]
+        return raw[:self.T * pitch].view(self.T, pitch)[:, :self.F]
+
+
+def _low_pitch(F: int) -> int:
+    return (F + 63) // 64 * 64
+
+
 def _act(act):
     code = ACTS.get(act)
     if code is None:
@@ -190,8 +233,8 @@ def ffn_forward(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: torch.T
     """The gated feed-forward block (ss_ffn_forward):
         Y = residual + dropout((act(X Wg^T) * (X Wu^T)) Wd^T)
     X [T, D], Wg, Wu [F, D], Wd [D, F], all bf16. Returns Y, or with save=True
-    (Y, saved), saved [3, T, F] holding G, U and A, what ffn_backward needs. out
-    may be residual. p, seed and offset as for dropout()."""
+    (Y, saved), an FfnSaved for ffn_backward. out may be residual. p, seed and
+    offset as for dropout()."""
     index, T, D, F = _block_args(X, Wg, Wu, Wd, ws)
     if residual is not None and not _fits(residual, _BF16, index, X.shape):
         _need(residual, "residual", _BF16, X.device, X.shape)
@@ -199,15 +242,13 @@ def ffn_forward(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: torch.T
         out = torch.empty_like(X)
     elif not _fits(out, _BF16, index, X.shape):
         _need(out, "out", _BF16, X.device, X.shape)
-    saved, g, u, a = None, None, None, None
+    saved, g, u, a, r = None, None, None, None, None
     if save:
-        saved = torch.empty((3, T, F), dtype=_BF16, device=X.device)
-        g = saved.data_ptr()
-        u = g + 2 * T * F
-        a = u + 2 * T * F
+        saved = FfnSaved(T, F, X.device)
+        g, u, a, r = saved.pointers()
     _call(_lib.ss_ffn_forward, index, X.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(),
           None if residual is None else residual.data_ptr(), T, D, F, _act(act),
-          _dropout_spec(p, seed, offset, X.device), out.data_ptr(), g, u, a, ws.data_ptr(),
+          _dropout_spec(p, seed, offset, X.device), out.data_ptr(), g, u, a, r, ws.data_ptr(),
           ws.numel())
     return (out, saved) if save else out
 
@@ -218,7 +259,7 @@ def ffn_backward(dY: torch.Tensor, X: torch.Tensor, Wg: torch.Tensor, Wu: torch.
                  dX: torch.Tensor | None = None, dWg: torch.Tensor | None = None,
                  dWu: torch.Tensor | None = None, dWd: torch.Tensor | None = None):
     """The gradients of ffn_forward (ss_ffn_backward) from dY [T, D] and `saved`
-    (that of ffn_forward, or any three [T, F] tensors G, U, A): {"dX", "dWg",
+    (that of ffn_forward, or three [T, F] tensors G, U, A): {"dX", "dWg",
     "dWu", "dWd"}, dX bf16 and the weight gradients of dw_dtype (fp32 or bf16),
     zero-filled when accumulate=True and none is given. The gradient of the
     residual is dY itself."""
@@ -229,18 +270,17 @@ def ffn_backward(dY: torch.Tensor, X: torch.Tensor, Wg: torch.Tensor, Wu: torch.
         raise TypeError(f"dw_dtype must be torch.bfloat16 or torch.float32, got {dw_dtype}")
     if not _fits(dY, _BF16, index, X.shape):
         _need(dY, "dY", _BF16, dev, X.shape)
-    if isinstance(saved, torch.Tensor):
-        if not _fits(saved, _BF16, index, (3, T, F)):
-            _need(saved, "saved", _BF16, dev, (3, T, F))
-        g = saved.data_ptr()
-        u = g + 2 * T * F
-        a = u + 2 * T * F
+    if isinstance(saved, FfnSaved):
+        if (saved.T, saved.F) != (T, F) or saved.buffer.get_device() != index:
+            raise ValueError(f"saved is of [{saved.T}, {saved.F}] on {saved.buffer.device}, "
+                             f"expected [{T}, {F}] on {dev}")
+        g, u, a, r = saved.pointers()
     else:
         G, U, A = saved
         for t, name in ((G, "G"), (U, "U"), (A, "A")):
             if not _fits(t, _BF16, index, (T, F)):
                 _need(t, name, _BF16, dev, (T, F))
-        g, u, a = G.data_ptr(), U.data_ptr(), A.data_ptr()
+        g, u, a, r = G.data_ptr(), U.data_ptr(), A.data_ptr(), None
     if dX is None:
         dX = torch.empty_like(X)
     elif not _fits(dX, _BF16, index, X.shape):
@@ -260,7 +300,7 @@ def ffn_backward(dY: torch.Tensor, X: torch.Tensor, Wg: torch.Tensor, Wu: torch.
     elif not _fits(dWd, dw_dtype, index, down):
         _need(dWd, "dWd", dw_dtype, dev, down)
     _call(_lib.ss_ffn_backward, index, dY.data_ptr(), X.data_ptr(), Wg.data_ptr(), Wu.data_ptr(),
-          Wd.data_ptr(), g, u, a, T, D, F, _act(act), _dropout_spec(p, seed, offset, dev), dw,
+          Wd.data_ptr(), g, u, a, r, T, D, F, _act(act), _dropout_spec(p, seed, offset, dev), dw,
           1 if accumulate else 0, dX.data_ptr(), dWg.data_ptr(), dWu.data_ptr(), dWd.data_ptr(),
           ws.data_ptr(), ws.numel())
     return {"dX": dX, "dWg": dWg, "dWu": dWu, "dWd": dWd}

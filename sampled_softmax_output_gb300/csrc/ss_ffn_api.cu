@@ -56,6 +56,8 @@ int64_t units(int64_t rows, int64_t cols, int col_tile = 256) {
 // dG and dU.
 constexpr float kPairUpUs = 0.6f, kPairActUs = 0.45f, kSplitUpUs = 2.9f, kSplitActUs = 2.f;
 
+bool low_bits_usable(const void* p) { return reinterpret_cast<uintptr_t>(p) % 32 == 0; }
+
 bool known_act(int act) { return act >= SS_ACT_SILU && act <= SS_ACT_RELU; }
 
 }  // namespace
@@ -70,18 +72,20 @@ size_t ss_ffn_workspace_size(int64_t T, int64_t D, int64_t F) {
   return check_ffn_sizes(T, D, F) == SS_OK ? ffn_layout(T, D, F).total : 0;
 }
 
+int64_t ss_ffn_low_bits_pitch(int64_t F) { return F > 0 ? (F + 63) / 64 * 64 : 0; }
+
 ss_status ss_ffn_forward(const uint16_t* X, const uint16_t* Wg, const uint16_t* Wu,
                          const uint16_t* Wd, const uint16_t* residual, int64_t T, int64_t D,
                          int64_t F, int act, const ss_dropout_spec* drop, uint16_t* Y, uint16_t* G,
-                         uint16_t* U, uint16_t* A, void* workspace, size_t workspace_bytes,
-                         ss_stream stream) {
+                         uint16_t* U, uint16_t* A, uint8_t* R, void* workspace,
+                         size_t workspace_bytes, ss_stream stream) {
   const ss_status st = check_ffn_sizes(T, D, F);
   if (st != SS_OK) return st;
   FfnForward f = {};
   if (!known_act(act) || !make_drop_args(drop, &f.drop)) return SS_ERR_INVALID;
   const bool save = G || U || A;
   if (T > 0 && (!usable({X, Wg, Wu, Wd, Y, workspace}) || (save && !usable({G, U, A})) ||
-                (residual && !usable({residual}))))
+                (residual && !usable({residual})) || (R && (!save || !low_bits_usable(R)))))
     return SS_ERR_INVALID;
   const FfnLayout L = ffn_layout(T, D, F);
   if (workspace_bytes < L.total) return SS_ERR_WORKSPACE;
@@ -94,6 +98,7 @@ ss_status ss_ffn_forward(const uint16_t* X, const uint16_t* Wg, const uint16_t* 
   f.T = static_cast<int>(T), f.D = static_cast<int>(D), f.F = static_cast<int>(F), f.act = act;
   f.Y = Y, f.G = G, f.U = U, f.A = save ? A : reinterpret_cast<uint16_t*>(ws + L.a);
   f.ldo = static_cast<int>(save ? F : workspace_pitch(F));
+  f.R = R, f.ldr = static_cast<int>(ss_ffn_low_bits_pitch(F));
   f.status = reinterpret_cast<int*>(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
@@ -115,8 +120,9 @@ ss_status ss_ffn_forward(const uint16_t* X, const uint16_t* Wg, const uint16_t* 
 
 ss_status ss_ffn_backward(const uint16_t* dY, const uint16_t* X, const uint16_t* Wg,
                           const uint16_t* Wu, const uint16_t* Wd, const uint16_t* G,
-                          const uint16_t* U, const uint16_t* A, int64_t T, int64_t D, int64_t F,
-                          int act, const ss_dropout_spec* drop, int dw_dtype, int accumulate,
+                          const uint16_t* U, const uint16_t* A, const uint8_t* R, int64_t T,
+                          int64_t D, int64_t F, int act, const ss_dropout_spec* drop, int dw_dtype,
+                          int accumulate,
                           uint16_t* dX, void* dWg, void* dWu, void* dWd, void* workspace,
                           size_t workspace_bytes, ss_stream stream) {
   const ss_status st = check_ffn_sizes(T, D, F);
@@ -126,7 +132,8 @@ ss_status ss_ffn_backward(const uint16_t* dY, const uint16_t* X, const uint16_t*
       (dw_dtype != SS_BF16 && dw_dtype != SS_FP32) || (accumulate != 0 && accumulate != 1))
     return SS_ERR_INVALID;
   if (!usable({dWg, dWu, dWd}) ||
-      (T > 0 && !usable({dY, X, Wg, Wu, Wd, G, U, A, dX, workspace})))
+      (T > 0 && (!usable({dY, X, Wg, Wu, Wd, G, U, A, dX, workspace}) ||
+                 (R && !low_bits_usable(R)))))
     return SS_ERR_INVALID;
   const FfnLayout L = ffn_layout(T, D, F);
   if (workspace_bytes < L.total) return SS_ERR_WORKSPACE;
@@ -152,6 +159,7 @@ ss_status ss_ffn_backward(const uint16_t* dY, const uint16_t* X, const uint16_t*
   b.dX = dX, b.dWg = dWg, b.dWu = dWu, b.dWd = dWd;
   b.dG = reinterpret_cast<uint16_t*>(ws + L.dg), b.dU = reinterpret_cast<uint16_t*>(ws + L.du);
   b.ldg = static_cast<int>(workspace_pitch(F));
+  b.R = R, b.ldr = static_cast<int>(ss_ffn_low_bits_pitch(F));
   b.status = reinterpret_cast<int*>(ws);
   cudaError_t e = cudaSuccess;
   if (d.mode != kDropNone) {

@@ -99,6 +99,19 @@ __device__ __forceinline__ void store_row32(uint16_t* dst, const uint32_t (&w)[1
   }
 }
 
+// The low bits of the elements j .. j + 3 of a chunk; og, ou: packed bf16 pairs,
+// o the index of the first
+template <int N>
+__device__ __forceinline__ uint32_t low_of(const uint32_t (&rg)[32], const uint32_t (&ru)[32],
+                                           const uint32_t (&og)[N], const uint32_t (&ou)[N], int j,
+                                           int o) {
+  const float g[4] = {__uint_as_float(rg[j]), __uint_as_float(rg[j + 1]),
+                      __uint_as_float(rg[j + 2]), __uint_as_float(rg[j + 3])};
+  const float u[4] = {__uint_as_float(ru[j]), __uint_as_float(ru[j + 1]),
+                      __uint_as_float(ru[j + 2]), __uint_as_float(ru[j + 3])};
+  return low_bits4(g, u, og[o], og[o + 1], ou[o], ou[o + 1]);
+}
+
 template <int KIND>
 struct PairCfg;
 template <>
@@ -150,7 +163,9 @@ struct PairArgs {
   uint16_t *G, *U, *A;
   // kUp: G, U, A (stores); kGradAct: G, U (loads), dG, dU (stores)
   CUtensorMap m[4];
-  int save;  // kUp: G and U are kept
+  int save;  // gate/up: G and U are kept
+  uint8_t* R;  // nullable; rows of ldr bytes
+  int ldr;
   // kDown
   const uint16_t* residual;
   uint16_t* Y;
@@ -397,6 +412,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int b = 0;
     uint32_t aph = 0;
 
+    [[maybe_unused]] auto row_of = [&](const Unit& x) {
+      return (x.mt * 2 + static_cast<int>(rank)) * BM + row;
+    };
     // dA: round r of this group is chunk r % 4 of its tile r / 4; the G and U
     // chunks of round r are loaded ahead into buffer r % kBufs. kGradAct: two
     // rounds ahead, replaced there by dG and dU and stored from there;
@@ -426,6 +444,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int r = 0; r < min(kAhead, n_rounds); ++r) load_round(r);
     }
 
+    // dA: the low bits of the next chunk's G and U, loaded one chunk ahead
+    [[maybe_unused]] uint32_t low_next[8] = {};
+    [[maybe_unused]] auto load_low = [&](const Unit& x, int i) {
+      const int tt = row_of(x), f = x.nt * kBN + cg * 128 + i * 32;
+      if (p.R && tt < p.T && f < p.F)
+        ld_global_v8(p.R + static_cast<size_t>(tt) * p.ldr + f, low_next);
+    };
+    [[maybe_unused]] auto take_low = [&](uint32_t (&low)[8], const Unit& x, UnitWalk<KIND> w,
+                                         int i) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) low[k] = low_next[k];
+      if (i < 3) {
+        load_low(x, i + 1);
+      } else {
+        w.next();
+        if (w.more()) load_low(find_unit(p, w.unit(p)), 0);
+      }
+    };
+    if constexpr (KIND == kGradAct || KIND == kGradActWide) {
+      UnitWalk<KIND> w(p, pair, npairs);
+      if (w.more()) load_low(find_unit(p, w.unit(p)), 0);
+    }
     int turn = 0;
     for (UnitWalk<KIND> w(p, pair, npairs); w.more(); w.next(), ++turn) {
       const bool ok = mbar_wait(&ctrl->tfull[b], aph, abort_flag, status);
@@ -471,6 +511,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (i == 1) release();
             const size_t at = static_cast<size_t>(valid ? t : 0) * p.ldo + f0;
             const int nv = valid ? min(32, p.F - f0) : 0;
+            uint32_t low[8] = {};
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               if (c * 16 >= nv) break;
@@ -492,19 +533,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 st_global_v8(p.G + at + c * 16, og);
                 st_global_v8(p.U + at + c * 16, ou);
               }
+              if (p.R) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  low[c * 4 + k] = low_of(rg, ru, og, ou, c * 16 + 4 * k, 2 * k);
+              }
             }
+            if (p.R && nv > 0) st_global_v8(p.R + static_cast<size_t>(t) * p.ldr + f0, low);
           }
         });
       } else if constexpr (KIND == kGradActWide) {
         const bool valid = t < p.T;
-        dispatch_act(p.act, [&](auto act) {
+        dispatch_act_low(p.act, p.R != nullptr, [&](auto act, auto with_low) {
           constexpr int ACT = decltype(act)::value;
+          constexpr bool LOW = decltype(with_low)::value;
 #pragma unroll 1
           for (int i = 0; i < 4; ++i, ++round) {
             const int c0 = cg * 128 + i * 32;
             const int f0 = un.nt * kBN + c0;
             const int buf = round % C::kBufs;
             const uint32_t sg = stage + static_cast<uint32_t>(buf) * kBufBytes;
+            [[maybe_unused]] uint32_t low[8];
+            if constexpr (LOW) take_low(low, un, w, i);
             uint32_t r[32];
             tmem_ld32(acc + c0, r);
             mbar_wait(&s_load[cg][buf], (round / C::kBufs) & 1, abort_flag, status);
@@ -530,8 +580,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   const float dA = __uint_as_float(r[2 * k + h]) * p.scale;
-                  const float gv = h ? bf16_hi(g[k]) : bf16_lo(g[k]);
-                  const float uv = h ? bf16_hi(v[k]) : bf16_lo(v[k]);
+                  const int e = 2 * k + h;
+                  float gv = h ? bf16_hi(g[k]) : bf16_lo(g[k]);
+                  float uv = h ? bf16_hi(v[k]) : bf16_lo(v[k]);
+                  if constexpr (LOW) {
+                    gv = refine_g(gv, low[e >> 2], e & 3);
+                    uv = refine_u(uv, low[e >> 2], e & 3);
+                  }
                   float a, d;
                   act_eval<ACT, true>(gv, a, d);
                   o[h] = dA * uv * d;
@@ -562,6 +617,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // the last store from the staging buffer has read it
             if (leader) bulk_wait_read<0>();
             named_bar_sync(bar, 128);
+            uint32_t low[8] = {};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               uint32_t ga[4], gg[4], gu[4];
@@ -583,7 +639,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 st_shared_v4(at + kChunkBytes, gg[0], gg[1], gg[2], gg[3]);
                 st_shared_v4(at + 2 * kChunkBytes, gu[0], gu[1], gu[2], gu[3]);
               }
+              if (p.R) {
+                low[2 * c] = low_of(rg, ru, gg, gu, c * 8, 0);
+                low[2 * c + 1] = low_of(rg, ru, gg, gu, c * 8 + 4, 2);
+              }
             }
+            if (p.R && t < p.T && f0 < p.F)
+              st_global_v8(p.R + static_cast<size_t>(t) * p.ldr + f0, low);
             fence_proxy_async_smem();
             named_bar_sync(bar, 128);
             if (leader) {
@@ -599,14 +661,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         });
       } else if constexpr (KIND == kGradAct) {
-        dispatch_act(p.act, [&](auto act) {
+        dispatch_act_low(p.act, p.R != nullptr, [&](auto act, auto with_low) {
           constexpr int ACT = decltype(act)::value;
+          constexpr bool LOW = decltype(with_low)::value;
 #pragma unroll 1
           for (int i = 0; i < 4; ++i, ++round) {
             const int c0 = cg * 128 + i * 32;
             const int f0 = un.nt * kBN + c0;
             const int buf = round % 3;
             const uint32_t sg = stage + static_cast<uint32_t>(buf) * kBufBytes;
+            [[maybe_unused]] uint32_t low[8];
+            if constexpr (LOW) take_low(low, un, w, i);
             uint32_t r[32];
             tmem_ld32(acc + c0, r);
             mbar_wait(&s_load[cg][buf], (round / 3) & 1, abort_flag, status);
@@ -624,8 +689,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   const float dA = __uint_as_float(r[c * 8 + 2 * k + h]) * p.scale;
-                  const float g = h ? bf16_hi(wg[k]) : bf16_lo(wg[k]);
-                  const float uu = h ? bf16_hi(wu[k]) : bf16_lo(wu[k]);
+                  const int e = c * 8 + 2 * k + h;
+                  float g = h ? bf16_hi(wg[k]) : bf16_lo(wg[k]);
+                  float uu = h ? bf16_hi(wu[k]) : bf16_lo(wu[k]);
+                  if constexpr (LOW) {
+                    g = refine_g(g, low[e >> 2], e & 3);
+                    uu = refine_u(uu, low[e >> 2], e & 3);
+                  }
                   float a, d;
                   act_eval<ACT, true>(g, a, d);
                   o[h] = dA * uu * d;
@@ -885,6 +955,7 @@ cudaError_t gate_up(const FfnForward& f, cudaStream_t s) {
   p.n_jobs = 1;
   p.T = f.T, p.D = f.D, p.F = f.F, p.act = f.act, p.save = save;
   p.ldo = f.ldo, p.G = f.G, p.U = f.U, p.A = f.A;
+  p.R = f.R, p.ldr = f.ldr;
   p.status = f.status;
   return launch_pair(p, f.num_sms, s);
 }
@@ -905,6 +976,7 @@ cudaError_t grad_act(const FfnBackward& f, cudaStream_t s) {
   p.n_jobs = 1;
   p.T = f.T, p.D = f.D, p.F = f.F, p.act = f.act, p.scale = f.scale;
   p.G_in = f.G, p.U_in = f.U, p.ldo = f.ldg, p.G = f.dG, p.U = f.dU;
+  p.R = const_cast<uint8_t*>(f.R), p.ldr = f.ldr;
   p.status = f.status;
   return launch_pair(p, f.num_sms, s);
 }

@@ -58,6 +58,8 @@ struct SplitArgs {
   int n_jobs, wait;
   int T, D, F, act;
   int ldo;  // elements between the rows of G, U, A (gate/up) or dG, dU (dA)
+  uint8_t* R;  // nullable: low bits of G and U, rows of ldr bytes
+  int ldr;
   const uint16_t *residual, *G_in, *U_in;
   uint16_t *Y, *G, *U, *A;  // kSUp: outputs (G null: not kept); kSGradAct: dG, dU in G, U
   DropArgs drop;
@@ -333,6 +335,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         const int row0 = nt * BN + n_first + n0;
         F4 v[kBatch];
         [[maybe_unused]] F4 w[kBatch];
+        [[maybe_unused]] uint32_t low[kBatch];
         // what else the epilogue reads, all of it on its way before the first use
         // (Y may be the residual: a load after a store would have to wait for it)
         if constexpr (KIND == kSDown) {
@@ -349,6 +352,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
               const size_t o = static_cast<size_t>(row0 + i * kStep) * p.F + m;
               w[i] = load_bf16x4(p.U_in + o);
               v[i] = load_bf16x4(p.G_in + o);
+              low[i] = p.R ? *reinterpret_cast<const uint32_t*>(
+                                 p.R + static_cast<size_t>(row0 + i * kStep) * p.ldr + m)
+                           : 0u;
             }
         }
         [[maybe_unused]] F4 x[kBatch];
@@ -379,6 +385,10 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
               store_bf16x4(p.G + o, v[i]);
               store_bf16x4(p.U + o, w[i]);
             }
+            if (p.R)
+              *reinterpret_cast<uint32_t*>(p.R + static_cast<size_t>(row) * p.ldr + m) = low_bits4(
+                  v[i].v, w[i].v, pack_bf16x2(v[i].v[0], v[i].v[1]), pack_bf16x2(v[i].v[2], v[i].v[3]),
+                  pack_bf16x2(w[i].v[0], w[i].v[1]), pack_bf16x2(w[i].v[2], w[i].v[3]));
           } else if constexpr (KIND == kSDown) {
             if (row >= p.T || m >= p.D) continue;
             const size_t o = static_cast<size_t>(row) * p.D + m;
@@ -403,9 +413,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 float a, d;
-                act_eval<ACT, true>(v[i].v[k], a, d);
+                act_eval<ACT, true>(refine_g(v[i].v[k], low[i], k), a, d);
                 const float dA = x[i].v[k] * p.scale;
-                v[i].v[k] = dA * w[i].v[k] * d;
+                v[i].v[k] = dA * refine_u(w[i].v[k], low[i], k) * d;
                 w[i].v[k] = dA * a;
               }
             });
@@ -546,6 +556,7 @@ cudaError_t split_gate_up(const FfnForward& f, const SplitPlan& plan, cudaStream
   p.wait = kWaitFirst;
   p.T = f.T, p.D = f.D, p.F = f.F, p.act = f.act;
   p.ldo = f.ldo, p.G = f.G, p.U = f.U, p.A = f.A;
+  p.R = f.R, p.ldr = f.ldr;
   p.status = f.status;
   return launch_split(p, plan, s);
 }
@@ -581,6 +592,7 @@ cudaError_t split_grad_act(const FfnBackward& f, const SplitPlan& plan, cudaStre
   p.wait = kWaitFirst;
   p.T = f.T, p.D = f.D, p.F = f.F, p.act = f.act, p.scale = f.scale;
   p.G_in = f.G, p.U_in = f.U, p.ldo = f.ldg, p.G = f.dG, p.U = f.dU;
+  p.R = const_cast<uint8_t*>(f.R), p.ldr = f.ldr;
   p.status = f.status;
   return launch_split(p, plan, s);
 }

@@ -82,6 +82,19 @@ def forward64(X, Wg, Wu, Wd, act, residual=None, factor=None):
             "U": (U, du + BF * (U.abs() + du)), "A": (A, eA_bf)}
 
 
+def refined(saved):
+    """G, U (with their low bits: 16ths of a bf16 step of their bit patterns) and
+    A of an FfnSaved, as fp32 tensors."""
+    low = saved.low_bits().to(torch.int32)
+
+    def add(t, nibble):
+        q = torch.where(nibble > 7, nibble - 16, nibble)
+        bits = (t.contiguous().view(torch.int16).to(torch.int32) << 16) + (q << 12)
+        return bits.view(torch.float32)
+
+    return add(saved[0], low & 15), add(saved[1], low >> 4), saved[2]
+
+
 def backward64(dY, X, Wg, Wu, Wd, saved, act, factor=None, fp32_dw=True):
     """From the saved tensors as they are: {name: (value, bound)}."""
     dY, X, Wg, Wu, Wd = (t.to(F64) for t in (dY, X, Wg, Wu, Wd))

@@ -20,7 +20,7 @@ p = ctypes.c_void_p
 def test_exports_every_declared_symbol():
     names = ss.header_symbols(ss.HEADER_BLOCK)
     assert set(names) == {"ss_dropout", "ss_dropout_backward", "ss_ffn_workspace_size",
-                          "ss_ffn_forward", "ss_ffn_backward"}
+                          "ss_ffn_low_bits_pitch", "ss_ffn_forward", "ss_ffn_backward"}
     for n in names:
         assert hasattr(ss.lib(), n), n
 
@@ -64,6 +64,11 @@ def test_dropout_argument_errors(fn):
         assert _drop(fn, residual=FAKE + 1) == INVALID
 
 
+def test_low_bits_pitch():
+    f = ss.lib().ss_ffn_low_bits_pitch
+    assert [f(n) for n in (-8, 0, 8, 64, 72, 2048)] == [0, 0, 64, 64, 128, 2048]
+
+
 def test_ffn_workspace_size():
     f = ss.lib().ss_ffn_workspace_size
     n = f(1000, 768, 2048)
@@ -76,10 +81,10 @@ def test_ffn_workspace_size():
         ss.ffn_workspace_size(1, 100, 64)
 
 
-FWD = ("X", "Wg", "Wu", "Wd", "residual", "T", "D", "F", "act", "spec", "Y", "G", "U", "A", "ws",
-       "wsb")
-BWD = ("dY", "X", "Wg", "Wu", "Wd", "G", "U", "A", "T", "D", "F", "act", "spec", "dw", "acc", "dX",
-       "dWg", "dWu", "dWd", "ws", "wsb")
+FWD = ("X", "Wg", "Wu", "Wd", "residual", "T", "D", "F", "act", "spec", "Y", "G", "U", "A", "R",
+       "ws", "wsb")
+BWD = ("dY", "X", "Wg", "Wu", "Wd", "G", "U", "A", "R", "T", "D", "F", "act", "spec", "dw", "acc",
+       "dX", "dWg", "dWu", "dWd", "ws", "wsb")
 
 
 def _ffn(fn, names, **kw):
@@ -119,14 +124,17 @@ def test_ffn_forward_argument_errors():
     for k in ("G", "U", "A"):  # all three or none
         assert _fwd(**{k: 0}) == INVALID, k
         assert _fwd(**{k: FAKE + 8}) == INVALID, k
-    assert _fwd(T=0, X=0, Y=0, G=0, U=0, A=0) == OK
+    assert _fwd(R=FAKE + 16) == INVALID            # 32-byte alignment
+    assert _fwd(G=0, U=0, A=0) == INVALID          # low bits of nothing
+    assert _fwd(T=0, X=0, Y=0, G=0, U=0, A=0, R=0) == OK
 
 
 def test_ffn_backward_argument_errors():
     for k in ("dY", "G", "U", "A", "dX", "dWg", "dWu", "dWd"):
         assert _bwd(**{k: 0}) == INVALID and _bwd(**{k: FAKE + 8}) == INVALID, k
     assert _bwd(dw=2) == INVALID and _bwd(acc=2) == INVALID
-    assert _bwd(T=0, dY=0, X=0, G=0, U=0, A=0, dX=0, acc=1) == OK
+    assert _bwd(R=FAKE + 16) == INVALID
+    assert _bwd(T=0, dY=0, X=0, G=0, U=0, A=0, R=0, dX=0, acc=1) == OK
 
 
 def test_python_refusals_on_host_tensors():

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import sampled_softmax_output_gb300 as ss
-from block_util import assert_within, backward64, forward64, keep_factor, keep_mask
+from block_util import BF, assert_within, backward64, forward64, keep_factor, keep_mask, refined
 
 pytestmark = pytest.mark.gpu
 BF16 = torch.bfloat16
@@ -48,6 +48,14 @@ def _forward_check(x, act, p=0.0, seed=0, offset=0, save=True, ws=None):
     assert_within(Y, ref["Y"], "Y")
     for t, name in zip(saved, "GUA"):
         assert_within(t, ref[name], name)
+    if save:
+        # with their low bits: half a 16th of a step off, a whole one at the end
+        # of the nibble's range, next to the sums' own error in `dg`
+        G, U, _ = refined(saved)
+        for t, name in ((G, "G"), (U, "U")):
+            value, bound = ref[name]
+            fine = (bound - BF * value.abs()) * 1.01 + BF / 8 * value.abs()
+            assert_within(t, (value, fine), name + " with low bits")
     assert ss.read_status(ws)[0] == 0
     return Y, saved
 
@@ -58,7 +66,8 @@ def _backward_check(x, saved, act, p=0.0, seed=0, offset=0, dw_dtype=torch.float
     ws = ss.ffn_workspace(T, D, F) if ws is None else ws
     g = ss.ffn_backward(x["dY"], *_weights(x), saved, ws, act=act, p=p, seed=seed, offset=offset,
                         dw_dtype=dw_dtype)
-    ref = backward64(x["dY"], *_weights(x), saved, act, keep_factor((T, D), p, seed, offset),
+    used = refined(saved) if isinstance(saved, ss.FfnSaved) else saved
+    ref = backward64(x["dY"], *_weights(x), used, act, keep_factor((T, D), p, seed, offset),
                      dw_dtype == torch.float32)
     for k in ("dX", "dWg", "dWu", "dWd"):
         assert g[k].dtype == (BF16 if k == "dX" else dw_dtype)
@@ -82,6 +91,41 @@ def test_backward(size, dw_dtype):
     T, D, F = size
     _, saved = ss.ffn_forward(*_weights(x), ss.ffn_workspace(T, D, F), save=True)
     _backward_check(x, saved, "silu", dw_dtype=dw_dtype)
+
+
+@pytest.mark.parametrize("size", [(3, 72, 136), (130, 264, 392), (1500, 768, 1288),
+                                  (1500, 1096, 1280)])
+def test_backward_from_plain_tensors(size):
+    """Any G, U and A, without low bits."""
+    x = _inputs(*size, seed=20)
+    _, saved = ss.ffn_forward(*_weights(x), ss.ffn_workspace(*size), save=True)
+    plain = tuple(t.clone() for t in saved)
+    _backward_check(x, plain, "gelu")
+    with_low = _backward_check(x, saved, "gelu")
+    stacked = torch.stack(plain)
+    again = ss.ffn_backward(x["dY"], *_weights(x), stacked, ss.ffn_workspace(*size), act="gelu")
+    ref = backward64(x["dY"], *_weights(x), plain, "gelu")
+    assert_within(again["dX"], ref["dX"], "dX")
+    assert not torch.equal(again["dWg"], with_low["dWg"])
+
+
+def test_step_is_nearer_to_64_bits_with_low_bits():
+    """A bf16 rounding is spread evenly over a step of 2^-8 to 2^-7 of the value:
+    an error of at most 2^-7 / sqrt(12) of the norm. With the low bits dG's is the
+    only one in dWg (fp32); without them U's, as large and independent, comes on
+    top: sqrt(2) times that and more."""
+    T, D, F = 600, 264, 392
+    x = _inputs(T, D, F, seed=21)
+    ws = ss.ffn_workspace(T, D, F)
+    _, saved = ss.ffn_forward(*_weights(x), ws, save=True)
+    exact = forward64(*_weights(x), "silu")
+    ref = backward64(x["dY"], *_weights(x), [exact[k][0] for k in "GUA"], "silu")["dWg"][0]
+
+    def err(s):
+        g = ss.ffn_backward(x["dY"], *_weights(x), s, ws)["dWg"].double()
+        return float((g - ref).norm() / ref.norm())
+
+    assert err(saved) < 2.0 ** -7 / 12 ** 0.5 and err(tuple(saved)) > 1.2 * err(saved)
 
 
 @pytest.mark.parametrize("size", LARGE)
@@ -200,11 +244,11 @@ def test_rows_behind_the_last_stay(T, shift, D, F):
     ptr = {k: v.data_ptr() for k, v in {**x, **bufs}.items()}
     s = torch.cuda.current_stream().cuda_stream
     assert L.ss_ffn_forward(ptr["X"], ptr["Wg"], ptr["Wu"], ptr["Wd"], ptr["residual"], T, D, F, 0,
-                            None, ptr["Y"], ptr["G"], ptr["U"], ptr["A"], ws.data_ptr(),
+                            None, ptr["Y"], ptr["G"], ptr["U"], ptr["A"], None, ws.data_ptr(),
                             ws.numel(), s) == 0
     dW = [torch.empty(F * D, device="cuda") for _ in range(3)]
     assert L.ss_ffn_backward(ptr["dY"], ptr["X"], ptr["Wg"], ptr["Wu"], ptr["Wd"], ptr["G"],
-                             ptr["U"], ptr["A"], T, D, F, 0, None, 1, 0, ptr["dX"],
+                             ptr["U"], ptr["A"], None, T, D, F, 0, None, 1, 0, ptr["dX"],
                              *(w.data_ptr() for w in dW), ws.data_ptr(), ws.numel(), s) == 0
     torch.cuda.synchronize()
     for k, b in bufs.items():
