@@ -82,10 +82,10 @@ def forward64(X, Wg, Wu, Wd, act, residual=None, factor=None):
             "U": (U, du + BF * (U.abs() + du)), "A": (A, eA_bf)}
 
 
-def refined(saved):
+def refined(saved, low=None):
     """G, U (with their low bits: 16ths of a bf16 step of their bit patterns) and
-    A of an FfnSaved, as fp32 tensors."""
-    low = saved.low_bits().to(torch.int32)
+    A of an FfnSaved, or of some rows of one and of its low bits, as fp32 tensors."""
+    low = (saved.low_bits() if low is None else low).to(torch.int32)
 
     def add(t, nibble):
         q = torch.where(nibble > 7, nibble - 16, nibble)

@@ -353,6 +353,74 @@ def test_smaller_batches_share_a_workspace_and_other_streams():
         torch.cuda.current_stream().wait_stream(s)
 
 
+def test_past_32_bits():
+    """[T, F] of more than 2^32 values: the first and the last rows. dY is zero
+    between them, so that they alone make the weight gradients."""
+    T, D, F, n = 600_001, 64, 8192, 150
+    x = _inputs(T, D, F, seed=22)
+    x["dY"][n:-n] = 0
+    ws = ss.ffn_workspace(T, D, F)
+    Y, saved = ss.ffn_forward(*_weights(x), ws, residual=x["residual"], p=0.1, seed=3, save=True)
+    g = ss.ffn_backward(x["dY"], *_weights(x), saved, ws, p=0.1, seed=3)
+    assert ss.read_status(ws)[0] == 0
+    ends = torch.cat([torch.arange(n), torch.arange(T - n, T)]).cuda()
+    factor = torch.cat([keep_factor((n, D), 0.1, 3), keep_factor((n, D), 0.1, 3, (T - n) * D)])
+    part = {k: x[k][ends] for k in ("X", "residual", "dY")}
+    part.update({k: x[k] for k in ("Wg", "Wu", "Wd")})
+    kept = [t[ends] for t in saved]
+    ref = forward64(*_weights(part), "silu", part["residual"], factor)
+    assert_within(Y[ends], ref["Y"], "Y")
+    for t, name in zip(kept, "GUA"):
+        assert_within(t, ref[name], name)
+    low = saved.low_bits()[ends]
+    ref = backward64(part["dY"], *_weights(part), refined(kept, low), "silu", factor)
+    assert_within(g["dX"][ends], ref["dX"], "dX")
+    assert (g["dX"][n:-n] == 0).all()
+    for k in ("dWg", "dWu", "dWd"):
+        assert_within(g[k], ref[k], k)
+
+
+@pytest.mark.parametrize("sizes", [((3, 264, 392), (5, 264, 392)),
+                                   ((300, 264, 392), (2100, 776, 1288)),
+                                   ((2100, 1096, 1288), (16, 2048, 1032))])
+@pytest.mark.parametrize("graphs", [False, True])
+def test_two_at_once(sizes, graphs):
+    """Two blocks on two streams, eager or as captured graphs, a workspace each:
+    what each gives alone."""
+    blocks, streams = [], [torch.cuda.Stream() for _ in sizes]
+    for size in sizes:
+        x = _inputs(*size, seed=23)
+        blocks.append((x, ss.ffn_workspace(*size)))
+
+    def step(x, ws):
+        Y, saved = ss.ffn_forward(*_weights(x), ws, residual=x["residual"], p=0.1, seed=4,
+                                  save=True)
+        g = ss.ffn_backward(x["dY"], *_weights(x), saved, ws, p=0.1, seed=4)
+        return [ss.dropout(Y, 0.2, 5), *g.values()]
+
+    want = [[t.clone() for t in step(*b)] for b in blocks]
+    torch.cuda.synchronize()
+    got = [None, None]
+    if graphs:
+        made = []
+        for b, s in zip(blocks, streams):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                made.append((graph, step(*b)))
+        got = [out for _, out in made]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                if graphs:
+                    made[i][0].replay()
+                else:
+                    got[i] = step(*blocks[i])
+    torch.cuda.synchronize()
+    for (x, ws), outs, ref in zip(blocks, got, want):
+        assert ss.read_status(ws)[0] == 0
+        assert all(torch.equal(a, b) for a, b in zip(outs, ref))
+
+
 def test_gradients_against_differences():
     """<gradient, direction> against central differences of the forward in 64
     bits. The differences are off by the third derivative's h^2 (h = 1e-4: below
@@ -441,6 +509,11 @@ def test_refusals():
         ss.ffn_backward(x["dY"][:8], X, Wg, Wu, Wd, saved, ws)
     with pytest.raises(ValueError):
         ss.ffn_backward(x["dY"], X, Wg, Wu, Wd, (saved[0], saved[1], saved[2][:, :64]), ws)
+    _, other = ss.ffn_forward(X[:8], Wg, Wu, Wd, ws, save=True)
+    with pytest.raises(ValueError):
+        ss.ffn_backward(x["dY"], X, Wg, Wu, Wd, other, ws)
+    with pytest.raises(IndexError):
+        saved[3]
     with pytest.raises(TypeError):
         ss.ffn_backward(x["dY"], X, Wg, Wu, Wd, saved, ws, dw_dtype=torch.float16)
     with pytest.raises(TypeError):
