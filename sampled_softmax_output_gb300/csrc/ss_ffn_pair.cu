@@ -570,7 +570,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             tmem_ld_wait(r);
             if (i == 3) release();
-            named_bar_sync(bar, 128);  // the group has read the buffer
+            // The group has read the buffer. Without the fence a read may still be on
+            // its way behind the MMAs' own when the next copy lands.
+            fence_proxy_async_smem();
+            named_bar_sync(bar, 128);
             if (leader && round + C::kBufs < n_rounds) load_round(round + C::kBufs);
             const int nv = valid ? min(32, p.F - f0) : 0;
             if (nv > 0) {

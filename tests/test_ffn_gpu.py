@@ -353,6 +353,24 @@ def test_smaller_batches_share_a_workspace_and_other_streams():
         torch.cuda.current_stream().wait_stream(s)
 
 
+@pytest.mark.parametrize("size,passes", [((8192, 1024, 5504), 6), ((3001, 1352, 3640), 20),
+                                         ((8192, 768, 5504), 6)])
+def test_many_tiles_to_a_pair(size, passes):
+    """Long runs of tiles, buffers that are used again and again under the load of
+    the products: within the bounds, and the same bits every time."""
+    x = _inputs(*size, seed=24)
+    ws = ss.ffn_workspace(*size)
+    _, saved = _forward_check(x, "silu", p=0.1, seed=6, ws=ws)
+    want = _backward_check(x, saved, "silu", p=0.1, seed=6, ws=ws)
+    for _ in range(passes):
+        _, again = ss.ffn_forward(*_weights(x), ws, p=0.1, seed=6, save=True)
+        assert all(torch.equal(a, b) for a, b in zip([*again, again.low_bits()],
+                                                     [*saved, saved.low_bits()]))
+        for kept in (saved, again):
+            g = ss.ffn_backward(x["dY"], *_weights(x), kept, ws, p=0.1, seed=6)
+            assert all(torch.equal(g[k], want[k]) for k in want)
+
+
 def test_past_32_bits():
     """[T, F] of more than 2^32 values: the first and the last rows. dY is zero
     between them, so that they alone make the weight gradients."""
