@@ -77,6 +77,14 @@ __device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&r)[4]) {
                : "memory");
 }
 
+// Barrier `id` of `nthreads` threads in whole warps, after code in which the lanes
+// of a warp part (one lane's arrival or copy): it wants the warp whole, which the
+// compiler does not see in inline assembly.
+__device__ __forceinline__ void group_sync(int id, int nthreads) {
+  __syncwarp();
+  asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
 // 32 bytes per lane, one whole sector (32-byte aligned addresses).
 __device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&r)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]),

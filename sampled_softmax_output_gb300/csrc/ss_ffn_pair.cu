@@ -472,7 +472,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool go = __all_sync(0xffffffffu, ok);
       if constexpr (C::kBufs > 0) {  // the epilogue's warps meet at barriers: agree first
         if (lane == 0) ctrl->vote[turn & 1][warp - 2] = go ? 1 : 0;
-        named_bar_sync(2, 32 * kEpiWarps);
+        group_sync(2, 32 * kEpiWarps);
         const int* v = ctrl->vote[turn & 1];
         int all = 1;
 #pragma unroll
@@ -495,6 +495,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       };
 
+      // body(r, i) over the 32-column chunks of this group. What moves TMEM wants
+      // the warp whole; the rows and columns that a body leaves out part it.
+      [[maybe_unused]] auto for_chunks = [&](auto&& body) {
+        for_tmem_chunks<4>(
+            acc, cg * 4,
+            [&](const uint32_t(&r)[32], int i) {
+              body(r, i);
+              __syncwarp();
+            },
+            release);
+      };
+
       if constexpr (KIND == kUpWide) {
         const bool valid = t < p.T;
         dispatch_act(p.act, [&](auto act) {
@@ -504,6 +516,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int c0 = cg * 64 + i * 32;  // within the tile's 128 features
             const int f0 = un.nt * (kBN / 2) + c0;
             uint32_t rg[32], ru[32];
+            __syncwarp();
             tmem_ld32(acc + c0, rg);
             tmem_ld32(acc + kBN / 2 + c0, ru);
             tmem_ld_wait(rg);
@@ -556,8 +569,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             [[maybe_unused]] uint32_t low[8];
             if constexpr (LOW) take_low(low, un, w, i);
             uint32_t r[32];
+            __syncwarp();
             tmem_ld32(acc + c0, r);
             mbar_wait(&s_load[cg][buf], (round / C::kBufs) & 1, abort_flag, status);
+            __syncwarp();
             uint32_t g[16], v[16];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -573,7 +588,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // The group has read the buffer. Without the fence a read may still be on
             // its way behind the MMAs' own when the next copy lands.
             fence_proxy_async_smem();
-            named_bar_sync(bar, 128);
+            group_sync(bar, 128);
             if (leader && round + C::kBufs < n_rounds) load_round(round + C::kBufs);
             const int nv = valid ? min(32, p.F - f0) : 0;
             if (nv > 0) {
@@ -612,6 +627,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int c0 = cg * 64 + i * 32;  // within the tile's 128 features
             const int f0 = un.nt * (kBN / 2) + c0;
             uint32_t rg[32], ru[32];
+            __syncwarp();
             tmem_ld32(acc + c0, rg);
             tmem_ld32(acc + kBN / 2 + c0, ru);
             tmem_ld_wait(rg);
@@ -619,7 +635,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (i == 1) release();
             // the last store from the staging buffer has read it
             if (leader) bulk_wait_read<0>();
-            named_bar_sync(bar, 128);
+            group_sync(bar, 128);
             uint32_t low[8] = {};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -650,7 +666,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (p.R && t < p.T && f0 < p.F)
               st_global_v8(p.R + static_cast<size_t>(t) * p.ldr + f0, low);
             fence_proxy_async_smem();
-            named_bar_sync(bar, 128);
+            group_sync(bar, 128);
             if (leader) {
               if (f0 < p.F && mrow < p.T) {
                 tma_store_2d(&p.m[2], stage, f0, mrow);
@@ -676,8 +692,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             [[maybe_unused]] uint32_t low[8];
             if constexpr (LOW) take_low(low, un, w, i);
             uint32_t r[32];
+            __syncwarp();
             tmem_ld32(acc + c0, r);
             mbar_wait(&s_load[cg][buf], (round / 3) & 1, abort_flag, status);
+            __syncwarp();
             tmem_ld_wait(r);
             if (i == 3) release();
 #pragma unroll
@@ -711,7 +729,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               st_shared_v4(at + kChunkBytes, wu[0], wu[1], wu[2], wu[3]);
             }
             fence_proxy_async_smem();
-            named_bar_sync(bar, 128);
+            group_sync(bar, 128);
             if (leader) {
               if (f0 < p.F && mrow < p.T) {
                 tma_store_2d(&p.m[2], sg, f0, mrow);
@@ -742,36 +760,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         };
         load_residual(0);
-        for_tmem_chunks<4>(
-            acc, cg * 4,
-            [&](const uint32_t(&r)[32], int i) {
-              uint32_t w[16];
+        for_chunks([&](const uint32_t(&r)[32], int i) {
+          uint32_t w[16];
 #pragma unroll
-              for (int k = 0; k < 16; ++k) w[k] = rn[k];
-              if (i < 3) load_residual(i + 1);
-              const int nv = min(32, ncols - i * 32);
-              if (nv <= 0) return;
-              const size_t at = base + i * 32;
-              uint32_t kept = 0xffffffffu;  // bit k: column k stays
-              if (p.drop.mode == kDropAll) kept = 0u;
-              if (p.drop.mode == kDropRandom) {
-                kept = 0u;
-                auto keep = [&](int k, bool yes) { kept |= (yes ? 1u : 0u) << k; };
-                const uint64_t e = p.drop.offset + at;
-                if (e & 1) for_kept<32, true>(seed, e, p.drop.thr, keep);
-                else for_kept<32, false>(seed, e, p.drop.thr, keep);
-              }
+          for (int k = 0; k < 16; ++k) w[k] = rn[k];
+          if (i < 3) load_residual(i + 1);
+          const int nv = min(32, ncols - i * 32);
+          if (nv <= 0) return;
+          const size_t at = base + i * 32;
+          uint32_t kept = 0xffffffffu;  // bit k: column k stays
+          if (p.drop.mode == kDropAll) kept = 0u;
+          if (p.drop.mode == kDropRandom) {
+            kept = 0u;
+            auto keep = [&](int k, bool yes) { kept |= (yes ? 1u : 0u) << k; };
+            const uint64_t e = p.drop.offset + at;
+            if (e & 1) for_kept<32, true>(seed, e, p.drop.thr, keep);
+            else for_kept<32, false>(seed, e, p.drop.thr, keep);
+          }
 #pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                float lo = bf16_lo(w[k]), hi = bf16_hi(w[k]);
-                if ((kept >> (2 * k)) & 1u) lo = fmaf(__uint_as_float(r[2 * k]), p.drop.scale, lo);
-                if ((kept >> (2 * k + 1)) & 1u)
-                  hi = fmaf(__uint_as_float(r[2 * k + 1]), p.drop.scale, hi);
-                w[k] = pack_bf16x2(lo, hi);
-              }
-              store_row32(p.Y + at, w, nv, p.wide);
-            },
-            release);
+          for (int k = 0; k < 16; ++k) {
+            float lo = bf16_lo(w[k]), hi = bf16_hi(w[k]);
+            if ((kept >> (2 * k)) & 1u) lo = fmaf(__uint_as_float(r[2 * k]), p.drop.scale, lo);
+            if ((kept >> (2 * k + 1)) & 1u)
+              hi = fmaf(__uint_as_float(r[2 * k + 1]), p.drop.scale, hi);
+            w[k] = pack_bf16x2(lo, hi);
+          }
+          store_row32(p.Y + at, w, nv, p.wide);
+        });
       } else {
         const GradOut& go_ = p.grad[un.job];
         const bool valid = t < go_.rows;
@@ -781,49 +796,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const float scale = go_.scale;
         if (ncols <= 0) release();
         else if (go_.fp32)
-          for_tmem_chunks<4>(
-              acc, cg * 4,
-              [&](const uint32_t(&r)[32], int i) {
-                const int nv = min(32, ncols - i * 32);
-                if (nv <= 0 || !valid) return;
-                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(go_.out) + base + i * 32);
+          for_chunks([&](const uint32_t(&r)[32], int i) {
+            const int nv = min(32, ncols - i * 32);
+            if (nv <= 0 || !valid) return;
+            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(go_.out) + base + i * 32);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  if (k * 4 >= nv) break;
-                  float4 o = make_float4(
-                      __uint_as_float(r[4 * k]) * scale, __uint_as_float(r[4 * k + 1]) * scale,
-                      __uint_as_float(r[4 * k + 2]) * scale, __uint_as_float(r[4 * k + 3]) * scale);
-                  if (go_.accumulate) {
-                    const float4 old = dst[k];
-                    o.x += old.x, o.y += old.y, o.z += old.z, o.w += old.w;
-                  }
-                  dst[k] = o;
-                }
-              },
-              release);
+            for (int k = 0; k < 8; ++k) {
+              if (k * 4 >= nv) break;
+              float4 o = make_float4(
+                  __uint_as_float(r[4 * k]) * scale, __uint_as_float(r[4 * k + 1]) * scale,
+                  __uint_as_float(r[4 * k + 2]) * scale, __uint_as_float(r[4 * k + 3]) * scale);
+              if (go_.accumulate) {
+                const float4 old = dst[k];
+                o.x += old.x, o.y += old.y, o.z += old.z, o.w += old.w;
+              }
+              dst[k] = o;
+            }
+          });
         else
-          for_tmem_chunks<4>(
-              acc, cg * 4,
-              [&](const uint32_t(&r)[32], int i) {
-                const int nv = min(32, ncols - i * 32);
-                if (nv <= 0 || !valid) return;
-                uint16_t* dst = static_cast<uint16_t*>(go_.out) + base + i * 32;
-                uint32_t w[16] = {};
-                if (go_.accumulate) {
+          for_chunks([&](const uint32_t(&r)[32], int i) {
+            const int nv = min(32, ncols - i * 32);
+            if (nv <= 0 || !valid) return;
+            uint16_t* dst = static_cast<uint16_t*>(go_.out) + base + i * 32;
+            uint32_t w[16] = {};
+            if (go_.accumulate) {
 #pragma unroll
-                  for (int v = 0; v < 4; ++v)
-                    if (v * 8 < nv) {
-                      const uint4 x = reinterpret_cast<const uint4*>(dst)[v];
-                      w[4 * v] = x.x, w[4 * v + 1] = x.y, w[4 * v + 2] = x.z, w[4 * v + 3] = x.w;
-                    }
+              for (int v = 0; v < 4; ++v)
+                if (v * 8 < nv) {
+                  const uint4 x = reinterpret_cast<const uint4*>(dst)[v];
+                  w[4 * v] = x.x, w[4 * v + 1] = x.y, w[4 * v + 2] = x.z, w[4 * v + 3] = x.w;
                 }
+            }
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                  w[k] = pack_bf16x2(fmaf(__uint_as_float(r[2 * k]), scale, bf16_lo(w[k])),
-                                     fmaf(__uint_as_float(r[2 * k + 1]), scale, bf16_hi(w[k])));
-                store_row32(dst, w, nv, go_.wide);
-              },
-              release);
+            for (int k = 0; k < 16; ++k)
+              w[k] = pack_bf16x2(fmaf(__uint_as_float(r[2 * k]), scale, bf16_lo(w[k])),
+                                 fmaf(__uint_as_float(r[2 * k + 1]), scale, bf16_hi(w[k])));
+            store_row32(dst, w, nv, go_.wide);
+          });
       }
       if (++b == 2) {
         b = 0;
@@ -840,6 +849,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if constexpr (KIND == kUp || KIND == kGradAct) {
       if (leader) bulk_wait<0>();
     }
+    __syncwarp();
   }
   __syncthreads();
   cluster_sync_all();  // the leader's MMAs are drained before either CTA frees TMEM
