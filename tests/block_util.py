@@ -55,9 +55,9 @@ def act64(g, act):
         cdf = 0.5 * torch.erfc(-g * math.sqrt(0.5))
         return g * cdf, cdf + g * torch.exp(-g * g / 2) / math.sqrt(2 * math.pi)
     if act == "gelu_tanh":
-        c = math.sqrt(2 / math.pi)
-        t = torch.tanh(c * (g + 0.044715 * g ** 3))
-        return 0.5 * g * (1 + t), 0.5 * (1 + t) + 0.5 * g * (1 - t * t) * c * (1 + 0.134145 * g * g)
+        c = 2 * math.sqrt(2 / math.pi)
+        s = torch.sigmoid(c * (g + 0.044715 * g ** 3))  # (1 + tanh(v)) / 2 is sigmoid(2 v)
+        return g * s, s + g * s * (1 - s) * c * (1 + 0.134145 * g * g)
     on = (g > 0).to(F64)
     return g * on, on
 

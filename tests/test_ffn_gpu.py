@@ -8,7 +8,8 @@ import pytest
 import torch
 
 import sampled_softmax_output_gb300 as ss
-from block_util import BF, assert_within, backward64, forward64, keep_factor, keep_mask, refined
+from block_util import (ACT, BF, F32, act64, assert_within, backward64, forward64, keep_factor,
+                        keep_mask, refined)
 
 pytestmark = pytest.mark.gpu
 BF16 = torch.bfloat16
@@ -143,6 +144,32 @@ def test_activations(act, size):
     x["Wg"] *= 4  # gates far out on both sides
     _, saved = _forward_check(x, act)
     _backward_check(x, saved, act)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh", "relu"])
+@pytest.mark.parametrize("T", [1, 300])
+def test_tails(act, T):
+    """act(g) to its own digits where it is tiny. With X, Wd and one column of dY of
+    ones in row 0, dWu is act(G) and dWg act'(G), rounded to bf16 once. An
+    exponential's argument of size E has three roundings: 3 F32 E of the value."""
+    D, F = 8, 2048
+    G = torch.zeros(T, F, dtype=BF16, device="cuda")
+    G[0] = torch.linspace(-13, 13, F, device="cuda").to(BF16)
+    X, dY = torch.ones(T, D, dtype=BF16, device="cuda"), torch.zeros(T, D, device="cuda")
+    dY[0, 3] = 1
+    W, Wd = torch.ones(F, D, dtype=BF16, device="cuda"), torch.ones(D, F, dtype=BF16, device="cuda")
+    g = ss.ffn_backward(dY.to(BF16), X, W, W, Wd, (G, torch.ones_like(G), G),
+                        ss.ffn_workspace(T, D, F), act=act)
+    x = G[0].double()
+    a, d = act64(x, act)
+    E = {"silu": x.abs(), "gelu": x * x / 2, "relu": 0 * x,
+         "gelu_tanh": 1.6 * (x + 0.044715 * x ** 3).abs()}[act]
+    rel = ACT + 3 * F32 * E
+    for k in range(D):
+        assert_within(g["dWu"][:, k], (a, (BF + 1.01 * rel) * a.abs()), "act")
+        # the slope: two terms of at most 1 + |g|
+        fine = 2 * ACT * (1 + x.abs())
+        assert_within(g["dWg"][:, k], (d, BF * d.abs() + 1.01 * fine), "slope")
 
 
 @pytest.mark.parametrize("size", [(3, 64, 72), (130, 264, 392), (1500, 768, 1288)])
