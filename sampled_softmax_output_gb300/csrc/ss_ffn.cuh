@@ -220,14 +220,32 @@ struct SplitPlan {
   float us;
 };
 
-// A CTA pair's time per k-block; launch, first loads, the last tile's epilogue
-// and the exit together.
+// A CTA pair's time per k-block of a tile of 256 columns; launch, first loads,
+// the last tile's epilogue and the exit together.
 constexpr float kPairUsPerKb = 0.35f, kPairUsFixed = 5.7f;
 // out_us: what the outputs of the epilogue cost beyond one bf16 value (gate/up
 // and dA: two to four values read or written for each sum).
 inline float pair_us(int64_t units, int64_t kb, float out_us, int num_sms) {
   const int64_t pairs = num_sms / 2, waves = (units + pairs - 1) / pairs;
   return kPairUsFixed + out_us + kPairUsPerKb * static_cast<float>(waves * kb);
+}
+
+// gate/up and dA also have tiles of 192 columns, for sizes whose last round of
+// pairs they fill better: a k-block of theirs takes 0.87 of the time for 0.75 of
+// the products. Gate/up and down of T 1003, D 1096, F 2952: 33.8 us against 35.8
+// (2 rounds either way); backward of T 3001, D 1352, F 3640: 167.7 against 170.4.
+// cols: of the product (gate/up: both matrices).
+struct PairPlan {
+  int bn;
+  float us;
+};
+inline PairPlan pair_plan(int64_t rows, int64_t cols, int64_t kb, float out_us, int num_sms) {
+  auto at = [&](int bn, float cost) {
+    const int64_t units = ((rows + 255) / 256) * ((cols + bn - 1) / bn);
+    return PairPlan{bn, kPairUsFixed + cost * (pair_us(units, kb, out_us, num_sms) - kPairUsFixed)};
+  };
+  const PairPlan whole = at(256, 1.f), narrow = at(192, 0.87f);
+  return narrow.us < whole.us ? narrow : whole;
 }
 
 // 128 x bn tiles (m_tile = 64 features of two matrices for gate/up), bn the
@@ -243,9 +261,9 @@ cudaError_t launch_drop_mask(const uint16_t* x, int64_t n, const DropArgs& drop,
 
 // CTA pairs, 256 x 256 tiles (ss_ffn_pair.cu)
 enum GradWhich { kDoX = 1, kDoW = 2 };  // the products of one pair_grads launch
-cudaError_t pair_gate_up(const FfnForward& p, cudaStream_t s);
+cudaError_t pair_gate_up(const FfnForward& p, int bn, cudaStream_t s);
 cudaError_t pair_down(const FfnForward& p, cudaStream_t s);
-cudaError_t pair_grad_act(const FfnBackward& p, cudaStream_t s);  // dG, dU
+cudaError_t pair_grad_act(const FfnBackward& p, int bn, cudaStream_t s);  // dG, dU
 cudaError_t pair_grads(const FfnBackward& p, int which, cudaStream_t s);
 
 // 128 x (16 to 128) tiles, K split over a cluster (ss_ffn_split.cu)

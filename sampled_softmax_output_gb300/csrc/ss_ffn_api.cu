@@ -47,8 +47,8 @@ bool usable(std::initializer_list<const void*> ps) {
 }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int64_t units(int64_t rows, int64_t cols, int col_tile = 256) {
-  return cdiv(rows, 256) * cdiv(cols, col_tile);
+int64_t units(int64_t rows, int64_t cols) {
+  return cdiv(rows, 256) * cdiv(cols, 256);
 }
 
 // What an epilogue's further outputs cost on either family, in us (on split
@@ -105,8 +105,8 @@ ss_status ss_ffn_forward(const uint16_t* X, const uint16_t* Wg, const uint16_t* 
   {
     StageTrace trace(s, "ffn_gate_up");
     const SplitPlan plan = split_plan(T, F, 64, cdiv(D, 64), kSplitUpUs, false, f.num_sms);
-    e = pair_us(units(T, F, 128), cdiv(D, 64), kPairUpUs, f.num_sms) < plan.us ? pair_gate_up(f, s)
-                                                                      : split_gate_up(f, plan, s);
+    const PairPlan pair = pair_plan(T, 2 * F, cdiv(D, 64), kPairUpUs, f.num_sms);
+    e = pair.us < plan.us ? pair_gate_up(f, pair.bn, s) : split_gate_up(f, plan, s);
   }
   if (e != cudaSuccess) return record_failure("ss_ffn_forward (gate/up)", e);
   {
@@ -172,8 +172,8 @@ ss_status ss_ffn_backward(const uint16_t* dY, const uint16_t* X, const uint16_t*
   {
     StageTrace trace(s, "ffn_grad_act");
     const SplitPlan plan = split_plan(T, F, 128, cdiv(D, 64), kSplitActUs, false, b.num_sms);
-    e = pair_us(units(T, F), cdiv(D, 64), kPairActUs, b.num_sms) < plan.us ? pair_grad_act(b, s)
-                                                                    : split_grad_act(b, plan, s);
+    const PairPlan pair = pair_plan(T, F, cdiv(D, 64), kPairActUs, b.num_sms);
+    e = pair.us < plan.us ? pair_grad_act(b, pair.bn, s) : split_grad_act(b, plan, s);
   }
   if (e != cudaSuccess) return record_failure("ss_ffn_backward (dG, dU)", e);
   {

@@ -47,7 +47,9 @@ namespace {
 // kUp, kGradAct: outputs staged in shared memory; ...Wide: stored from registers
 enum Kind { kUp, kUpWide, kDown, kGradAct, kGradActWide, kGrads };
 
-constexpr int kBN = 256;
+constexpr int kBN = 256, kNarrowBN = 192;
+template <int KIND>
+constexpr bool kIsUp = KIND == kUp || KIND == kUpWide;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kMaxJobs = 4;
@@ -211,7 +213,8 @@ __device__ __forceinline__ Unit find_unit(const PairArgs<KIND>& p, int u) {
   return r;
 }
 
-template <int KIND>
+// BN: columns of a tile, 256, or 192 for gate/up and dA
+template <int KIND, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_ffn_pair(const __grid_constant__ PairArgs<KIND> p) {
   pdl_enter();
@@ -230,6 +233,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
   int* status = p.status;
+  constexpr int n_chunks = BN / 64;  // of 32 columns, to a column group (dA)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -281,17 +285,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int m0 = un.mt * 2 * BM + static_cast<int>(rank) * BM;
         // this CTA's half of the tile's N; gate/up: the same 128 features of
         // the CTA's own matrix
-        const int n0 = KIND == kUp || KIND == kUpWide ? un.nt * (kBN / 2)
-                                   : un.nt * kBN + static_cast<int>(rank) * (kBN / 2);
+        const int n0 = kIsUp<KIND> ? un.nt * (BN / 2)
+                                   : un.nt * BN + static_cast<int>(rank) * (BN / 2);
         // one k-loop per form of the operands, chosen once per unit: this thread
         // issues every copy, and branches between them cost 8% of dX and dW
         auto load_unit = [&](auto a_form, auto b_form) {
           constexpr bool A_MN = decltype(a_form)::value, B_MN = decltype(b_form)::value;
+          // half a tile's columns: two boxes of 64 (BN 192: the last 32 of them for
+          // nothing), or one of BN / 2 rows
+          constexpr uint32_t b_bytes = B_MN ? 16384u : BN * BK;
 #pragma unroll 1
           for (int seg = 0; ok && seg < 2; ++seg) {
             const CUtensorMap* ma = &job.a[seg];
             const CUtensorMap* mb =
-                &job.b[KIND == kUp || KIND == kUpWide ? static_cast<int>(rank) : seg];
+                &job.b[kIsUp<KIND> ? static_cast<int>(rank) : seg];
             const int k_end = job.kb[seg] * BK;
 #pragma unroll 1
             for (int k = 0; k < k_end; k += BK) {
@@ -299,7 +306,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 ok = false;
                 break;
               }
-              if (rank == 0) mbar_arrive_expect_tx(&ctrl->full[s], 2 * L::STAGE_BYTES);
+              if (rank == 0) mbar_arrive_expect_tx(&ctrl->full[s], 2 * (L::A_BYTES + b_bytes));
               const uint32_t fb = full0 + s * 8;
               const uint32_t a_dst = tiles + s * L::STAGE_BYTES;
               const uint32_t b_dst = a_dst + L::A_BYTES;
@@ -356,9 +363,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const PairJob& job = p.job[un.job];
         const int kbs = job.kb[0] + job.kb[1];
         const bool a_mn = job.a_mn != 0, b_mn = job.b_mn != 0;
-        const uint32_t idesc = a_mn   ? idesc_bf16_f32(2 * BM, kBN, true, true)
-                               : b_mn ? idesc_bf16_f32(2 * BM, kBN, false, true)
-                                      : idesc_bf16_f32(2 * BM, kBN, false, false);
+        const uint32_t idesc = a_mn   ? idesc_bf16_f32(2 * BM, BN, true, true)
+                               : b_mn ? idesc_bf16_f32(2 * BM, BN, false, true)
+                                      : idesc_bf16_f32(2 * BM, BN, false, false);
         if (!mbar_wait(&ctrl->tempty[b], aph ^ 1u, abort_flag, status)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(b * kBN);
@@ -415,14 +422,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     [[maybe_unused]] auto row_of = [&](const Unit& x) {
       return (x.mt * 2 + static_cast<int>(rank)) * BM + row;
     };
-    // dA: round r of this group is chunk r % 4 of its tile r / 4; the G and U
-    // chunks of round r are loaded ahead into buffer r % kBufs. kGradAct: two
-    // rounds ahead, replaced there by dG and dU and stored from there;
+    // dA: round r of this group is chunk r % n_chunks of its tile r / n_chunks; the
+    // G and U chunks of round r are loaded ahead into buffer r % kBufs. kGradAct:
+    // two rounds ahead, replaced there by dG and dU and stored from there;
     // kGradActWide: read into registers, and the buffer is loaded again at once.
     [[maybe_unused]] int round = 0, n_rounds = 0;
     [[maybe_unused]] auto chunk_at = [&](int r, int& col, int& mrow) {
-      const Unit un = find_unit(p, pair + (r >> 2) * npairs);
-      col = un.nt * kBN + cg * 128 + (r & 3) * 32;
+      const int turn = r / n_chunks;
+      const Unit un = find_unit(p, pair + turn * npairs);
+      col = un.nt * BN + cg * (BN / 2) + (r - turn * n_chunks) * 32;
       mrow = (un.mt * 2 + static_cast<int>(rank)) * BM;
     };
     [[maybe_unused]] auto load_round = [&](int r) {  // by the group's leader
@@ -439,7 +447,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       constexpr int kAhead = KIND == kGradAct ? 2 : C::kBufs;
       const int num_units = p.job[0].units_end;
       const int my_units = pair < num_units ? (num_units - pair + npairs - 1) / npairs : 0;
-      n_rounds = my_units * 4;
+      n_rounds = my_units * n_chunks;
       if (leader)
         for (int r = 0; r < min(kAhead, n_rounds); ++r) load_round(r);
     }
@@ -447,7 +455,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // dA: the low bits of the next chunk's G and U, loaded one chunk ahead
     [[maybe_unused]] uint32_t low_next[8] = {};
     [[maybe_unused]] auto load_low = [&](const Unit& x, int i) {
-      const int tt = row_of(x), f = x.nt * kBN + cg * 128 + i * 32;
+      const int tt = row_of(x), f = x.nt * BN + cg * (BN / 2) + i * 32;
       if (p.R && tt < p.T && f < p.F)
         ld_global_v8(p.R + static_cast<size_t>(tt) * p.ldr + f, low_next);
     };
@@ -455,7 +463,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                          int i) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) low[k] = low_next[k];
-      if (i < 3) {
+      if (i + 1 < n_chunks) {
         load_low(x, i + 1);
       } else {
         w.next();
@@ -512,16 +520,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         dispatch_act(p.act, [&](auto act) {
           constexpr int ACT = decltype(act)::value;
 #pragma unroll 1
-          for (int i = 0; i < 2; ++i) {
-            const int c0 = cg * 64 + i * 32;  // within the tile's 128 features
-            const int f0 = un.nt * (kBN / 2) + c0;
+          for (int c0 = cg * 32; c0 < BN / 2; c0 += 64) {  // within the tile's features
+            const int f0 = un.nt * (BN / 2) + c0;
             uint32_t rg[32], ru[32];
             __syncwarp();
             tmem_ld32(acc + c0, rg);
-            tmem_ld32(acc + kBN / 2 + c0, ru);
+            tmem_ld32(acc + BN / 2 + c0, ru);
             tmem_ld_wait(rg);
             tmem_ld_wait(ru);
-            if (i == 1) release();
+            if (c0 + 64 >= BN / 2) release();
             const size_t at = static_cast<size_t>(valid ? t : 0) * p.ldo + f0;
             const int nv = valid ? min(32, p.F - f0) : 0;
             uint32_t low[8] = {};
@@ -561,9 +568,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           constexpr int ACT = decltype(act)::value;
           constexpr bool LOW = decltype(with_low)::value;
 #pragma unroll 1
-          for (int i = 0; i < 4; ++i, ++round) {
-            const int c0 = cg * 128 + i * 32;
-            const int f0 = un.nt * kBN + c0;
+          for (int i = 0; i < n_chunks; ++i, ++round) {
+            const int c0 = cg * (BN / 2) + i * 32;
+            const int f0 = un.nt * BN + c0;
             const int buf = round % C::kBufs;
             const uint32_t sg = stage + static_cast<uint32_t>(buf) * kBufBytes;
             [[maybe_unused]] uint32_t low[8];
@@ -584,7 +591,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               v[4 * c] = x[0], v[4 * c + 1] = x[1], v[4 * c + 2] = x[2], v[4 * c + 3] = x[3];
             }
             tmem_ld_wait(r);
-            if (i == 3) release();
+            if (i + 1 == n_chunks) release();
             // The group has read the buffer. Without the fence a read may still be on
             // its way behind the MMAs' own when the next copy lands.
             fence_proxy_async_smem();
@@ -623,16 +630,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         dispatch_act(p.act, [&](auto act) {
           constexpr int ACT = decltype(act)::value;
 #pragma unroll 1
-          for (int i = 0; i < 2; ++i) {
-            const int c0 = cg * 64 + i * 32;  // within the tile's 128 features
-            const int f0 = un.nt * (kBN / 2) + c0;
+          for (int c0 = cg * 32; c0 < BN / 2; c0 += 64) {  // within the tile's features
+            const int f0 = un.nt * (BN / 2) + c0;
             uint32_t rg[32], ru[32];
             __syncwarp();
             tmem_ld32(acc + c0, rg);
-            tmem_ld32(acc + kBN / 2 + c0, ru);
+            tmem_ld32(acc + BN / 2 + c0, ru);
             tmem_ld_wait(rg);
             tmem_ld_wait(ru);
-            if (i == 1) release();
+            if (c0 + 64 >= BN / 2) release();
             // the last store from the staging buffer has read it
             if (leader) bulk_wait_read<0>();
             group_sync(bar, 128);
@@ -684,9 +690,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           constexpr int ACT = decltype(act)::value;
           constexpr bool LOW = decltype(with_low)::value;
 #pragma unroll 1
-          for (int i = 0; i < 4; ++i, ++round) {
-            const int c0 = cg * 128 + i * 32;
-            const int f0 = un.nt * kBN + c0;
+          for (int i = 0; i < n_chunks; ++i, ++round) {
+            const int c0 = cg * (BN / 2) + i * 32;
+            const int f0 = un.nt * BN + c0;
             const int buf = round % 3;
             const uint32_t sg = stage + static_cast<uint32_t>(buf) * kBufBytes;
             [[maybe_unused]] uint32_t low[8];
@@ -697,7 +703,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_wait(&s_load[cg][buf], (round / 3) & 1, abort_flag, status);
             __syncwarp();
             tmem_ld_wait(r);
-            if (i == 3) release();
+            if (i + 1 == n_chunks) release();
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const uint32_t at = chunk_addr(sg, row, c);
@@ -881,10 +887,11 @@ bool rows_on_sectors(int64_t cols, std::initializer_list<const void*> ps) {
 
 int tiles_of(int64_t n, int tile) { return static_cast<int>((n + tile - 1) / tile); }
 
-// K-major operand [rows, k]: boxes of 128 rows x 64 of k. MN-major operand
+// K-major operand [rows, k]: boxes of box_rows rows x 64 of k. MN-major operand
 // [k, cols]: boxes of 64 columns x 64 of k. ld: elements between rows.
-bool map_kmajor(CUtensorMap* m, const uint16_t* p, int64_t rows, int64_t k, int64_t ld) {
-  return make_bf16_map(m, p, k, rows, ld * 2, BK, 128);
+bool map_kmajor(CUtensorMap* m, const uint16_t* p, int64_t rows, int64_t k, int64_t ld,
+                int box_rows = 128) {
+  return make_bf16_map(m, p, k, rows, ld * 2, BK, box_rows);
 }
 bool map_mnmajor(CUtensorMap* m, const uint16_t* p, int64_t k, int64_t cols, int64_t ld) {
   return make_bf16_map(m, p, cols, k, ld * 2, 64, BK);
@@ -926,7 +933,7 @@ bool balance(int n_a, int64_t kb_a, int n_b, int64_t kb_b, int pairs, PairSchedu
   return true;
 }
 
-template <int KIND>
+template <int KIND, int BN = kBN>
 cudaError_t launch_pair(PairArgs<KIND>& p, int num_sms, cudaStream_t s) {
   int end = 0;
   for (int j = 0; j < p.n_jobs; ++j) {
@@ -943,20 +950,20 @@ cudaError_t launch_pair(PairArgs<KIND>& p, int num_sms, cudaStream_t s) {
     }
   }
   constexpr int smem = Gemm2Smem<kBN, PairCfg<KIND>::kStages, epi_bytes<KIND>()>::TOTAL;
-  return launch_pdl(k_ffn_pair<KIND>, dim3(2 * pairs), dim3(kThreads), smem, s, p);
+  return launch_pdl(k_ffn_pair<KIND, BN>, dim3(2 * pairs), dim3(kThreads), smem, s, p);
 }
 
 }  // namespace
 
 namespace {
 
-template <int KIND>
+template <int KIND, int BN>
 cudaError_t gate_up(const FfnForward& f, cudaStream_t s) {
   PairArgs<KIND> p = {};
   PairJob& j = p.job[0];
   const bool save = f.G != nullptr;
-  if (!map_kmajor(&j.a[0], f.X, f.T, f.D, f.D) || !map_kmajor(&j.b[0], f.Wg, f.F, f.D, f.D) ||
-      !map_kmajor(&j.b[1], f.Wu, f.F, f.D, f.D))
+  if (!map_kmajor(&j.a[0], f.X, f.T, f.D, f.D) || !map_kmajor(&j.b[0], f.Wg, f.F, f.D, f.D, BN / 2) ||
+      !map_kmajor(&j.b[1], f.Wu, f.F, f.D, f.D, BN / 2))
     return cudaErrorInvalidValue;
   if (KIND == kUp &&
       (!map_chunk(&p.m[2], f.A, f.T, f.F, f.ldo) ||
@@ -964,16 +971,16 @@ cudaError_t gate_up(const FfnForward& f, cudaStream_t s) {
     return cudaErrorInvalidValue;
   j.kb[0] = tiles_of(f.D, BK);
   j.m_tiles = tiles_of(f.T, 2 * BM);
-  j.n_tiles = tiles_of(f.F, kBN / 2);
+  j.n_tiles = tiles_of(f.F, BN / 2);
   p.n_jobs = 1;
   p.T = f.T, p.D = f.D, p.F = f.F, p.act = f.act, p.save = save;
   p.ldo = f.ldo, p.G = f.G, p.U = f.U, p.A = f.A;
   p.R = f.R, p.ldr = f.ldr;
   p.status = f.status;
-  return launch_pair(p, f.num_sms, s);
+  return launch_pair<KIND, BN>(p, f.num_sms, s);
 }
 
-template <int KIND>
+template <int KIND, int BN>
 cudaError_t grad_act(const FfnBackward& f, cudaStream_t s) {
   PairArgs<KIND> p = {};
   PairJob& j = p.job[0];
@@ -985,25 +992,27 @@ cudaError_t grad_act(const FfnBackward& f, cudaStream_t s) {
     return cudaErrorInvalidValue;
   j.kb[0] = tiles_of(f.D, BK);
   j.m_tiles = tiles_of(f.T, 2 * BM);
-  j.n_tiles = tiles_of(f.F, kBN);
+  j.n_tiles = tiles_of(f.F, BN);
   p.n_jobs = 1;
   p.T = f.T, p.D = f.D, p.F = f.F, p.act = f.act, p.scale = f.scale;
   p.G_in = f.G, p.U_in = f.U, p.ldo = f.ldg, p.G = f.dG, p.U = f.dU;
   p.R = const_cast<uint8_t*>(f.R), p.ldr = f.ldr;
   p.status = f.status;
-  return launch_pair(p, f.num_sms, s);
+  return launch_pair<KIND, BN>(p, f.num_sms, s);
 }
 
 }  // namespace
 
-cudaError_t pair_gate_up(const FfnForward& f, cudaStream_t s) {
-  return rows_on_sectors(f.ldo, {f.G, f.U, f.A}) ? gate_up<kUpWide>(f, s) : gate_up<kUp>(f, s);
+cudaError_t pair_gate_up(const FfnForward& f, int bn, cudaStream_t s) {
+  if (rows_on_sectors(f.ldo, {f.G, f.U, f.A}))
+    return bn == kBN ? gate_up<kUpWide, kBN>(f, s) : gate_up<kUpWide, kNarrowBN>(f, s);
+  return bn == kBN ? gate_up<kUp, kBN>(f, s) : gate_up<kUp, kNarrowBN>(f, s);
 }
 
-cudaError_t pair_grad_act(const FfnBackward& f, cudaStream_t s) {
-  return tiles_of(f.D, BK) >= kActWideKb && rows_on_sectors(f.ldg, {f.dG, f.dU})
-             ? grad_act<kGradActWide>(f, s)
-             : grad_act<kGradAct>(f, s);
+cudaError_t pair_grad_act(const FfnBackward& f, int bn, cudaStream_t s) {
+  if (tiles_of(f.D, BK) >= kActWideKb && rows_on_sectors(f.ldg, {f.dG, f.dU}))
+    return bn == kBN ? grad_act<kGradActWide, kBN>(f, s) : grad_act<kGradActWide, kNarrowBN>(f, s);
+  return bn == kBN ? grad_act<kGradAct, kBN>(f, s) : grad_act<kGradAct, kNarrowBN>(f, s);
 }
 
 cudaError_t pair_down(const FfnForward& f, cudaStream_t s) {
