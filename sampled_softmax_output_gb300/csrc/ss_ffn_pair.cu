@@ -25,7 +25,9 @@
 //   in-kernel time, rate      gate/up       down          dA            dX and dW
 //   T 65536, D 768, F 2048    249 us 1.66   133 us 1.55   206 us 1.00   567 us 1.82 PFLOP/s
 //   T 8192, D 2048, F 5504    205    1.80   112    1.65   143    1.29   508    1.82
-// (K-blocks lost to the last, partly filled round of tiles included.)
+// (K-blocks lost to the last, partly filled round of tiles included; without the
+// low bits of G and U, which add 20 and 28 us to the first and third column at
+// T 65536, 7 and 6 us at T 8192.)
 //
 // Roles per CTA: warp 0 TMA producer, warp 1 MMA issuer (the leader's), warps
 // 2-9 epilogue: two column groups of four warps, one accumulator row per
