@@ -611,8 +611,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                   float gv = h ? bf16_hi(g[k]) : bf16_lo(g[k]);
                   float uv = h ? bf16_hi(v[k]) : bf16_lo(v[k]);
                   if constexpr (LOW) {
-                    gv = refine_g(gv, low[e >> 2], e & 3);
-                    uv = refine_u(uv, low[e >> 2], e & 3);
+                    gv = refine(g[k], halves_g(low[e >> 2]), e & 3);
+                    uv = refine(v[k], halves_u(low[e >> 2]), e & 3);
                   }
                   float a, d;
                   act_eval<ACT, true>(gv, a, d);
@@ -722,8 +722,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                   float g = h ? bf16_hi(wg[k]) : bf16_lo(wg[k]);
                   float uu = h ? bf16_hi(wu[k]) : bf16_lo(wu[k]);
                   if constexpr (LOW) {
-                    g = refine_g(g, low[e >> 2], e & 3);
-                    uu = refine_u(uu, low[e >> 2], e & 3);
+                    g = refine(wg[k], halves_g(low[e >> 2]), e & 3);
+                    uu = refine(wu[k], halves_u(low[e >> 2]), e & 3);
                   }
                   float a, d;
                   act_eval<ACT, true>(g, a, d);

@@ -335,6 +335,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         const int row0 = nt * BN + n_first + n0;
         F4 v[kBatch];
         [[maybe_unused]] F4 w[kBatch];
+        [[maybe_unused]] uint2 g_in[kBatch], u_in[kBatch];
         [[maybe_unused]] uint32_t low[kBatch];
         // what else the epilogue reads, all of it on its way before the first use
         // (Y may be the residual: a load after a store would have to wait for it)
@@ -350,11 +351,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
           for (int i = 0; i < kBatch; ++i)
             if (row0 + i * kStep < p.T && m < p.F) {
               const size_t o = static_cast<size_t>(row0 + i * kStep) * p.F + m;
-              w[i] = load_bf16x4(p.U_in + o);
-              v[i] = load_bf16x4(p.G_in + o);
+              u_in[i] = *reinterpret_cast<const uint2*>(p.U_in + o);
+              g_in[i] = *reinterpret_cast<const uint2*>(p.G_in + o);
               low[i] = p.R ? *reinterpret_cast<const uint32_t*>(
                                  p.R + static_cast<size_t>(row0 + i * kStep) * p.ldr + m)
-                           : 0u;
+                           : 0x88888888u;  // as they are
             }
         }
         [[maybe_unused]] F4 x[kBatch];
@@ -413,9 +414,10 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 float a, d;
-                act_eval<ACT, true>(refine_g(v[i].v[k], low[i], k), a, d);
+                act_eval<ACT, true>(refine(k < 2 ? g_in[i].x : g_in[i].y, halves_g(low[i]), k), a, d);
+                const float u = refine(k < 2 ? u_in[i].x : u_in[i].y, halves_u(low[i]), k);
                 const float dA = x[i].v[k] * p.scale;
-                v[i].v[k] = dA * refine_u(w[i].v[k], low[i], k) * d;
+                v[i].v[k] = dA * u * d;
                 w[i].v[k] = dA * a;
               }
             });

@@ -83,13 +83,13 @@ def forward64(X, Wg, Wu, Wd, act, residual=None, factor=None):
 
 
 def refined(saved, low=None):
-    """G, U (with their low bits: 16ths of a bf16 step of their bit patterns) and
-    A of an FfnSaved, or of some rows of one and of its low bits, as fp32 tensors."""
+    """G, U (with their low bits: 8 plus 16ths of a bf16 step of their bit patterns,
+    a 256th more each) and A of an FfnSaved, or of some rows of one and of its low
+    bits, as fp32 tensors."""
     low = (saved.low_bits() if low is None else low).to(torch.int32)
 
     def add(t, nibble):
-        q = torch.where(nibble > 7, nibble - 16, nibble)
-        bits = (t.contiguous().view(torch.int16).to(torch.int32) << 16) + (q << 12)
+        bits = (t.contiguous().view(torch.int16).to(torch.int32) << 16) + (nibble - 8) * 0x1010
         return bits.view(torch.float32)
 
     return add(saved[0], low & 15), add(saved[1], low >> 4), saved[2]
