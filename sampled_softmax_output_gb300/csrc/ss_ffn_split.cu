@@ -288,12 +288,19 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     mma_commit(&ctrl.done);
   }
   __syncwarp();
-  if (p.wait == kWaitLoadA) pdl_wait();
+  // (kWaitLoadA) `go` is older than the end of the kernel before, which may have
+  // recorded an error since: then what it wrote is not to be used. A thread
+  // without a role asks, beside the MMAs.
+  bool clean = true;
+  if (p.wait == kWaitLoadA) {
+    pdl_wait();
+    if (threadIdx.x == kSplitThreads - 1) clean = read_status(p.status) == 0;
+  }
 
   // ------------------------------------------------- accumulator -> P[n][m]
   // Every block's loads have landed when its MMAs are done, so the ring is free.
   bool ok = go && mbar_wait(&ctrl.done, 0, abort_flag, p.status);
-  ok = __syncthreads_and(ok && !*abort_flag) != 0;
+  ok = __syncthreads_and(ok && clean && !*abort_flag) != 0;
   if (ok) {
     tc_fence_after();
     const int q = warp & 3, half = warp >> 2;
