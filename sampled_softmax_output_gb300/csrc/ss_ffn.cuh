@@ -19,6 +19,7 @@
 #include <type_traits>
 
 #include "ss_dropout.cuh"
+#include "ss_ffn_plan.h"
 #include "ss_internal.h"
 #include "ss_ptx.cuh"
 #include "ss_shared.h"
@@ -206,53 +207,6 @@ struct FfnBackward {
 // y = x with the dropped elements zeroed, not scaled (ss_dropout.cu)
 cudaError_t launch_drop_mask(const uint16_t* x, int64_t n, const DropArgs& drop, uint16_t* y,
                              int num_sms, cudaStream_t stream);
-
-// ------------------------------------------------- which family, which tile
-//
-// A problem is N rows of output (tokens, or rows of a weight gradient) by M
-// columns, K = 64 kb. The two families' times are estimated in microseconds
-// with constants fitted on one GB300 to 110 problem sizes (T 65 to 16000, D 64
-// to 4096, F 64 to 12288), every product in every form: what the estimates pick
-// takes 2.4% longer than the best form on average.
-
-// The choice for one problem on the split family.
-struct SplitPlan {
-  int bn, cluster;
-  float us;
-};
-
-// A CTA pair's time per k-block of a tile of 256 columns; launch, first loads,
-// the last tile's epilogue and the exit together.
-constexpr float kPairUsPerKb = 0.35f, kPairUsFixed = 5.7f;
-// out_us: what the outputs of the epilogue cost beyond one bf16 value (gate/up
-// and dA: two to four values read or written for each sum).
-inline float pair_us(int64_t units, int64_t kb, float out_us, int num_sms) {
-  const int64_t pairs = num_sms / 2, waves = (units + pairs - 1) / pairs;
-  return kPairUsFixed + out_us + kPairUsPerKb * static_cast<float>(waves * kb);
-}
-
-// gate/up and dA also have tiles of 192 columns, for sizes whose last round of
-// pairs they fill better: a k-block of theirs takes 0.87 of the time for 0.75 of
-// the products. Gate/up and down of T 1003, D 1096, F 2952: 33.8 us against 35.8
-// (2 rounds either way); backward of T 3001, D 1352, F 3640: 167.7 against 170.4.
-// cols: of the product (gate/up: both matrices).
-struct PairPlan {
-  int bn;
-  float us;
-};
-inline PairPlan pair_plan(int64_t rows, int64_t cols, int64_t kb, float out_us, int num_sms) {
-  auto at = [&](int bn, float cost) {
-    const int64_t units = ((rows + 255) / 256) * ((cols + bn - 1) / bn);
-    return PairPlan{bn, kPairUsFixed + cost * (pair_us(units, kb, out_us, num_sms) - kPairUsFixed)};
-  };
-  const PairPlan whole = at(256, 1.f), narrow = at(192, 0.87f);
-  return narrow.us < whole.us ? narrow : whole;
-}
-
-// 128 x bn tiles (m_tile = 64 features of two matrices for gate/up), bn the
-// narrowest that takes all tokens, up to 64, or 128; K over up to 8 CTAs.
-SplitPlan split_plan(int64_t n, int64_t m, int m_tile, int64_t kb, float out_us, bool wide_only,
-                     int num_sms);
 
 // ------------------------------------------------------------- the kernels
 

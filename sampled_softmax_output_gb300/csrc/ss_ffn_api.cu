@@ -46,16 +46,6 @@ bool usable(std::initializer_list<const void*> ps) {
   });
 }
 
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int64_t units(int64_t rows, int64_t cols) {
-  return cdiv(rows, 256) * cdiv(cols, 256);
-}
-
-// What an epilogue's further outputs cost on either family, in us (on split
-// tiles, per 64 tokens): gate/up writes G, U and A, dA reads G and U and writes
-// dG and dU.
-constexpr float kPairUpUs = 0.6f, kPairActUs = 0.45f, kSplitUpUs = 2.9f, kSplitActUs = 2.f;
-
 bool low_bits_usable(const void* p) { return reinterpret_cast<uintptr_t>(p) % 32 == 0; }
 
 bool known_act(int act) { return act >= SS_ACT_SILU && act <= SS_ACT_RELU; }
@@ -100,20 +90,17 @@ ss_status ss_ffn_forward(const uint16_t* X, const uint16_t* Wg, const uint16_t* 
   f.ldo = static_cast<int>(save ? F : workspace_pitch(F));
   f.R = R, f.ldr = static_cast<int>(ss_ffn_low_bits_pitch(F));
   f.status = reinterpret_cast<int*>(ws);
+  const ForwardPlan plan = forward_plan(T, D, F, f.num_sms);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   {
     StageTrace trace(s, "ffn_gate_up");
-    const SplitPlan plan = split_plan(T, F, 64, cdiv(D, 64), kSplitUpUs, false, f.num_sms);
-    const PairPlan pair = pair_plan(T, 2 * F, cdiv(D, 64), kPairUpUs, f.num_sms);
-    e = pair.us < plan.us ? pair_gate_up(f, pair.bn, s) : split_gate_up(f, plan, s);
+    e = plan.up_on_pairs ? pair_gate_up(f, plan.up_pair.bn, s) : split_gate_up(f, plan.up, s);
   }
   if (e != cudaSuccess) return record_failure("ss_ffn_forward (gate/up)", e);
   {
     StageTrace trace(s, "ffn_down");
-    const SplitPlan plan = split_plan(T, D, 128, cdiv(F, 64), 0.f, false, f.num_sms);
-    e = pair_us(units(T, D), cdiv(F, 64), 0.f, f.num_sms) < plan.us ? pair_down(f, s)
-                                                                    : split_down(f, plan, s);
+    e = plan.down_on_pairs ? pair_down(f, s) : split_down(f, plan.down, s);
   }
   return e == cudaSuccess ? SS_OK : record_failure("ss_ffn_forward (down)", e);
 }
@@ -161,6 +148,7 @@ ss_status ss_ffn_backward(const uint16_t* dY, const uint16_t* X, const uint16_t*
   b.ldg = static_cast<int>(workspace_pitch(F));
   b.R = R, b.ldr = static_cast<int>(ss_ffn_low_bits_pitch(F));
   b.status = reinterpret_cast<int*>(ws);
+  const BackwardPlan plan = backward_plan(T, D, F, b.num_sms);
   cudaError_t e = cudaSuccess;
   if (d.mode != kDropNone) {
     // zeroes only: the factor 1 / (1 - p) goes into the products' epilogues, so
@@ -171,29 +159,17 @@ ss_status ss_ffn_backward(const uint16_t* dY, const uint16_t* X, const uint16_t*
   if (e != cudaSuccess) return record_failure("ss_ffn_backward (mask)", e);
   {
     StageTrace trace(s, "ffn_grad_act");
-    const SplitPlan plan = split_plan(T, F, 128, cdiv(D, 64), kSplitActUs, false, b.num_sms);
-    const PairPlan pair = pair_plan(T, F, cdiv(D, 64), kPairActUs, b.num_sms);
-    e = pair.us < plan.us ? pair_grad_act(b, pair.bn, s) : split_grad_act(b, plan, s);
+    e = plan.act_on_pairs ? pair_grad_act(b, plan.act_pair.bn, s) : split_grad_act(b, plan.act, s);
   }
   if (e != cudaSuccess) return record_failure("ss_ffn_backward (dG, dU)", e);
   {
     StageTrace trace(s, "ffn_grads");
-    // dX (K = 2 F) and the three dW (K = T): each on either family, or all in
-    // one launch of pairs, as long as its busiest pair
-    const int64_t kx = 2 * cdiv(F, 64), kw = cdiv(T, 64);
-    const int64_t ux = units(T, D), uw = 3 * units(F, D);
-    const SplitPlan px = split_plan(T, D, 128, kx, 0.f, false, b.num_sms);
-    // three gradients of F x D, as one of 3 F rows
-    const SplitPlan pw = split_plan(3 * cdiv(F, 128) * 128, D, 128, kw, 0.f, true, b.num_sms);
-    const float x_us = pair_us(ux, kx, 0.f, b.num_sms), w_us = pair_us(uw, kw, 0.f, b.num_sms);
-    const int64_t share = cdiv(ux * kx + uw * kw, b.num_sms / 2);
-    const float both_us =
-        kPairUsFixed + kPairUsPerKb * static_cast<float>(std::max(share, std::max(kx, kw)));
-    if (both_us <= std::min(x_us, px.us) + std::min(w_us, pw.us)) {
+    if (plan.grads_together) {
       e = pair_grads(b, kDoX | kDoW, s);
     } else {
-      e = x_us < px.us ? pair_grads(b, kDoX, s) : split_grad_x(b, px, s);
-      if (e == cudaSuccess) e = w_us < pw.us ? pair_grads(b, kDoW, s) : split_grad_w(b, pw, s);
+      e = plan.x_on_pairs ? pair_grads(b, kDoX, s) : split_grad_x(b, plan.x, s);
+      if (e == cudaSuccess)
+        e = plan.w_on_pairs ? pair_grads(b, kDoW, s) : split_grad_w(b, plan.w, s);
     }
   }
   return e == cudaSuccess ? SS_OK : record_failure("ss_ffn_backward (dX, dW)", e);

@@ -29,7 +29,6 @@ namespace {
 enum SplitKind { kSUp, kSDown, kSGradAct, kSGradX, kSGradW };
 
 constexpr int kSplitThreads = 256;
-constexpr int kSplitMaxCluster = 8;
 constexpr int kSplitMaxJobs = 3;
 
 // When a kernel of this file waits for the one before it in the stream:
@@ -522,34 +521,6 @@ bool map_mnmajor(CUtensorMap* m, const uint16_t* p, int64_t k, int64_t cols, int
 }
 
 }  // namespace
-
-// A CTA alone on its SM takes 0.28 to 0.59 us a k-block (16 to 128 tokens, the
-// rate at which one CTA takes operands in); two on an SM share that rate and
-// hide each other's gaps, so that they hardly slow one another; a third waits
-// for a place. A cluster's join costs a barrier; the outputs' cost goes with the
-// tokens of a tile.
-SplitPlan split_plan(int64_t n, int64_t m, int m_tile, int64_t kb, float out_us, bool wide_only,
-                     int num_sms) {
-  constexpr float kFixed = 2.2f, kJoin = 0.1f, kTile = 1.15f;
-  SplitPlan best{0, 0, 0.f};
-  for (int bn = wide_only ? 128 : 16; bn <= 128; bn *= 2) {
-    if (bn < 64 && n > bn) continue;  // narrower tiles only re-read the weights
-    const float per_kb = bn == 16 ? 0.28f : bn == 32 ? 0.3f : bn == 64 ? 0.364f : 0.59f;
-    const int64_t tiles = ((n + bn - 1) / bn) * ((m + m_tile - 1) / m_tile);
-    for (int S = 1; S <= kSplitMaxCluster && (S == 1 || kb / S >= 2); S *= 2) {
-      const float share = static_cast<float>(tiles * S) / num_sms;
-      const float load = share <= 1.f ? 1.f : share <= 2.f ? 1.f + 0.18f * (share - 1.f) : 1.09f * share;
-      const float us = kFixed + (S > 1 ? kJoin : 0.f) +
-                       load * (per_kb * kb / S + (kTile + out_us) * bn / 64);
-      // few tokens: the weights' bytes bound the kernel; every CTA has a place
-      // from the start, so that all of K streams at once
-      if (n <= 64 && S > 1 && share > 2.f) continue;
-      if (best.bn == 0 || us < best.us) best = SplitPlan{bn, S, us};
-    }
-    if (n <= bn) break;
-  }
-  return best;
-}
 
 cudaError_t split_gate_up(const FfnForward& f, const SplitPlan& plan, cudaStream_t s) {
   SplitArgs<kSUp> p = {};

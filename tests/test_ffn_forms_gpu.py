@@ -1,0 +1,70 @@
+"""The feed-forward block in every form that its choice of kernels has, against 64
+bits (test_ffn_plan_host.py: that these sizes reach them all)."""
+import pytest
+import torch
+
+import sampled_softmax_output_gb300 as ss
+from block_util import BF, keep_mask
+from ffn_plan import ACT_SIZES, FORM_SIZES
+from test_ffn_gpu import _backward_check, _forward_check, _inputs, _weights
+
+pytestmark = pytest.mark.gpu
+ACTS = sorted(ss.ACTS)
+
+
+@pytest.mark.parametrize("k,size", list(enumerate(FORM_SIZES)))
+def test_forms(k, size):
+    x = _inputs(*size, seed=40 + k)
+    act = ACTS[k % 4]
+    ws = ss.ffn_workspace(*size)
+    Y, saved = _forward_check(x, act, p=0.1, seed=k, ws=ws)
+    only, _ = _forward_check(x, act, p=0.1, seed=k, save=False, ws=ws)
+    assert torch.equal(only, Y)
+    _backward_check(x, saved, act, p=0.1, seed=k, ws=ws)
+
+
+@pytest.mark.parametrize("T", [17, 24, 31, 32])
+@pytest.mark.parametrize("D,F", [(264, 520), (1096, 392), (768, 2048)])
+@pytest.mark.parametrize("dw_dtype", [torch.float32, torch.bfloat16])
+def test_17_to_32_tokens(T, D, F, dw_dtype):
+    """With and without low bits, with and without dropout."""
+    x = _inputs(T, D, F, seed=T)
+    ws = ss.ffn_workspace(T, D, F)
+    _, saved = _forward_check(x, "silu", ws=ws)
+    _backward_check(x, saved, "silu", dw_dtype=dw_dtype, ws=ws)
+    _backward_check(x, tuple(t.clone() for t in saved), "silu", p=0.3, seed=2, offset=5,
+                    dw_dtype=dw_dtype, ws=ws)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("size", ACT_SIZES)
+def test_activations_on_pairs(act, size):
+    x = _inputs(*size, seed=3)
+    x["Wg"] *= 4  # gates far out on both sides
+    ws = ss.ffn_workspace(*size)
+    _, saved = _forward_check(x, act, ws=ws)
+    _backward_check(x, saved, act, ws=ws)
+    _backward_check(x, tuple(t.clone() for t in saved), act, ws=ws)
+
+
+@pytest.mark.parametrize("size", [(2, 16384, 8), (2, 8, 65536), (300, 16384, 8), (300, 8, 65536)])
+def test_widest(size):
+    """SS_MAX_D and SS_MAX_F."""
+    x = _inputs(*size, seed=41)
+    _, saved = _forward_check(x, "gelu", p=0.1, seed=1)
+    _backward_check(x, saved, "gelu", p=0.1, seed=1)
+
+
+@pytest.mark.parametrize("T", [5, 300, 2100])
+def test_kept_values_are_those_of_dropout(T):
+    """The block's dropout against ss.dropout over the undropped output, value by
+    value. The sums are the same; Z is rounded, its dropout once more, and Y once:
+    three half steps."""
+    x = _inputs(T, 264, 392, seed=5, residual=False)
+    ws = ss.ffn_workspace(T, 264, 392)
+    Z = ss.ffn_forward(*_weights(x), ws)
+    Y = ss.ffn_forward(*_weights(x), ws, p=0.3, seed=6).double()
+    want = ss.dropout(Z, 0.3, 6).double()
+    kept = torch.from_numpy(keep_mask(Z.numel(), 0.3, 6)).cuda().view(Z.shape)
+    assert torch.equal(Y[~kept], want[~kept])
+    assert ((Y - want).abs() <= 3.1 * BF * torch.maximum(Y.abs(), want.abs()) + 1e-37).all()
