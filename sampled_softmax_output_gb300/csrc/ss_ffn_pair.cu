@@ -5,7 +5,7 @@
 // A job is one product with up to two segments of K (dX = dG Wg + dU Wu is one
 // accumulation over 2 F), its operands' tensor maps and majors, and its tiles.
 // A launch runs one or more jobs; pair p runs the units p, p + pairs, ... of
-// all jobs' tiles in a row.
+// all jobs' tiles in a row, or those that ss_ffn_plan.h deals it (dX and dW).
 //
 // gate/up: the two CTAs of a pair hold the two halves of the MMA's N, and here
 // the leader's half is 128 rows of Wg and the peer's 128 rows of Wu. Columns
@@ -34,9 +34,7 @@
 // thread, two TMEM accumulators so that the epilogue of a tile runs beside the
 // MMAs of the next.
 #include <algorithm>
-#include <functional>
 #include <type_traits>
-#include <utility>
 
 #include "ss_ffn.cuh"
 #include "ss_gemm.cuh"
@@ -148,15 +146,6 @@ constexpr int epi_bytes() {
   return 2 * PairCfg<KIND>::kBufs * PairCfg<KIND>::kTensors * static_cast<int>(kChunkBytes);
 }
 
-// kGrads with both K lengths: which units each pair runs, in order (else pair p
-// runs p, p + pairs, ...).
-constexpr int kSchedPairs = 128, kSchedUnits = 2048;
-struct PairSchedule {
-  uint16_t first[kSchedPairs + 1];  // pair p runs unit[first[p] .. first[p + 1])
-  uint16_t unit[kSchedUnits];
-};
-struct NoSchedule {};
-
 template <int KIND>
 struct PairArgs {
   PairJob job[KIND == kGrads ? kMaxJobs : 1];
@@ -178,26 +167,29 @@ struct PairArgs {
   float scale;  // kGradAct, kGradActWide
   GradOut grad[KIND == kGrads ? kMaxJobs : 1];
   int* status;
-  int listed;  // kGrads: 1 if sched holds the units
-  std::conditional_t<KIND == kGrads, PairSchedule, NoSchedule> sched;
+  UnitDeal deal;  // kGrads
 };
 
-// The units of one pair, one after the other.
+// The units of one pair, one after the other: p, p + pairs, ..., or (kGrads) as
+// they are dealt.
 template <int KIND>
 struct UnitWalk {
   int at, end, step;
   __device__ __forceinline__ UnitWalk(const PairArgs<KIND>& p, int pair, int npairs)
-      : at(pair), end(p.job[p.n_jobs - 1].units_end), step(npairs) {
-    if constexpr (KIND == kGrads)
-      if (p.listed) at = p.sched.first[pair], end = p.sched.first[pair + 1], step = 1;
-  }
+      : at(pair), end(p.job[0].units_end), step(npairs) {}
   __device__ __forceinline__ bool more() const { return at < end; }
   __device__ __forceinline__ void next() { at += step; }
-  __device__ __forceinline__ int unit(const PairArgs<KIND>& p) const {
-    if constexpr (KIND == kGrads)
-      if (p.listed) return p.sched.unit[at];
-    return at;
-  }
+  __device__ __forceinline__ int unit() const { return at; }
+};
+template <>
+struct UnitWalk<kGrads> {
+  PairShare share;
+  int at = 0;
+  __device__ __forceinline__ UnitWalk(const PairArgs<kGrads>& p, int pair, int npairs)
+      : share(share_of(p.deal, pair, npairs)) {}
+  __device__ __forceinline__ bool more() const { return at < share.count(); }
+  __device__ __forceinline__ void next() { ++at; }
+  __device__ __forceinline__ int unit() const { return share.unit(at); }
 };
 
 struct Unit {
@@ -282,7 +274,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t ph = 0, issued = 0;  // k-blocks issued
       bool ok = true;
       for (UnitWalk<KIND> w(p, pair, npairs); ok && w.more(); w.next()) {
-        const Unit un = find_unit(p, w.unit(p));
+        const Unit un = find_unit(p, w.unit());
         const PairJob& job = p.job[un.job];
         const int m0 = un.mt * 2 * BM + static_cast<int>(rank) * BM;
         // this CTA's half of the tile's N; gate/up: the same 128 features of
@@ -361,7 +353,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t ph = 0, aph = 0;
       bool ok = true;
       for (UnitWalk<KIND> w(p, pair, npairs); ok && w.more(); w.next()) {
-        const Unit un = find_unit(p, w.unit(p));
+        const Unit un = find_unit(p, w.unit());
         const PairJob& job = p.job[un.job];
         const int kbs = job.kb[0] + job.kb[1];
         const bool a_mn = job.a_mn != 0, b_mn = job.b_mn != 0;
@@ -469,12 +461,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         load_low(x, i + 1);
       } else {
         w.next();
-        if (w.more()) load_low(find_unit(p, w.unit(p)), 0);
+        if (w.more()) load_low(find_unit(p, w.unit()), 0);
       }
     };
     if constexpr (KIND == kGradAct || KIND == kGradActWide) {
       UnitWalk<KIND> w(p, pair, npairs);
-      if (w.more()) load_low(find_unit(p, w.unit(p)), 0);
+      if (w.more()) load_low(find_unit(p, w.unit()), 0);
     }
     int turn = 0;
     for (UnitWalk<KIND> w(p, pair, npairs); w.more(); w.next(), ++turn) {
@@ -491,7 +483,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (!go) break;
       tc_fence_after();
-      const Unit un = find_unit(p, w.unit(p));
+      const Unit un = find_unit(p, w.unit());
       const int mrow = (un.mt * 2 + static_cast<int>(rank)) * BM;  // first row of this CTA
       const int t = mrow + row;
       const uint32_t acc = lane_addr + static_cast<uint32_t>(b * kBN);
@@ -902,39 +894,6 @@ bool map_chunk(CUtensorMap* m, const uint16_t* p, int64_t rows, int64_t cols, in
   return make_bf16_map(m, p, cols, rows, ld * 2, 32, 128);
 }
 
-// The units of two groups with different K, 0 .. n_a - 1 of kb_a k-blocks and
-// the n_b after them of kb_b, handed to the pair that is free first, the longer
-// group first: units that run at the same time are neighbours, which share
-// operands in L2, and the pairs finish within one short unit of each other.
-// Walked round-robin instead, T 8192, D 2048, F 5504 loses 7%. False: too many
-// units for the kernel's parameters (which 32 or more to a pair balance alone).
-bool balance(int n_a, int64_t kb_a, int n_b, int64_t kb_b, int pairs, PairSchedule* out) {
-  if (n_a + n_b > kSchedUnits || pairs > kSchedPairs) return false;
-  using Slot = std::pair<int64_t, int>;  // (time the pair becomes free, pair), earliest on top
-  Slot heap[kSchedPairs];
-  for (int p = 0; p < pairs; ++p) heap[p] = Slot(0, p);
-  uint8_t owner[kSchedUnits];
-  int count[kSchedPairs] = {};
-  const bool a_first = kb_a >= kb_b;
-  for (int i = 0; i < n_a + n_b; ++i) {
-    const bool is_a = a_first ? i < n_a : i >= n_b;
-    std::pop_heap(heap, heap + pairs, std::greater<Slot>());
-    Slot& slot = heap[pairs - 1];
-    slot.first += is_a ? kb_a : kb_b;
-    owner[i] = static_cast<uint8_t>(slot.second);
-    ++count[slot.second];
-    std::push_heap(heap, heap + pairs, std::greater<Slot>());
-  }
-  out->first[0] = 0;
-  for (int p = 0; p < pairs; ++p) out->first[p + 1] = static_cast<uint16_t>(out->first[p] + count[p]);
-  std::fill(count, count + pairs, 0);
-  for (int i = 0; i < n_a + n_b; ++i) {
-    const int unit = a_first ? i : i < n_b ? n_a + i : i - n_b;
-    out->unit[out->first[owner[i]] + count[owner[i]]++] = static_cast<uint16_t>(unit);
-  }
-  return true;
-}
-
 template <int KIND, int BN = kBN>
 cudaError_t launch_pair(PairArgs<KIND>& p, int num_sms, cudaStream_t s) {
   int end = 0;
@@ -945,11 +904,10 @@ cudaError_t launch_pair(PairArgs<KIND>& p, int num_sms, cudaStream_t s) {
   p.group_m = kGroupM;
   const int pairs = end < num_sms / 2 ? end : num_sms / 2;
   if constexpr (KIND == kGrads) {
-    if (p.n_jobs == kMaxJobs) {  // the three dW, then dX
-      const int n_dw = p.job[2].units_end;
-      p.listed = balance(n_dw, p.job[0].kb[0], end - n_dw, p.job[3].kb[0] + p.job[3].kb[1], pairs,
-                         &p.sched);
-    }
+    // the three dW, then dX; or only either
+    const int n_a = p.n_jobs == kMaxJobs ? p.job[2].units_end : end;
+    auto kb = [&](int j) { return p.job[j].kb[0] + p.job[j].kb[1]; };
+    p.deal = deal_units(n_a, kb(0), end - n_a, kb(p.n_jobs - 1));
   }
   constexpr int smem = Gemm2Smem<kBN, PairCfg<KIND>::kStages, epi_bytes<KIND>()>::TOTAL;
   return launch_pdl(k_ffn_pair<KIND, BN>, dim3(2 * pairs), dim3(kThreads), smem, s, p);

@@ -36,6 +36,17 @@ extern "C" void backward(long T, long D, long F, int sms, int* o) {
                    p.x_on_pairs, p.x.bn, p.x.cluster, p.w_on_pairs, p.w.bn, p.w.cluster};
   for (int x : v) *o++ = x;
 }
+// the units of all pairs, one pair after the other; ends[p]: where pair p's end
+extern "C" long deal(int n_a, long kb_a, int n_b, long kb_b, int pairs, int* units, int* ends) {
+  const UnitDeal d = deal_units(n_a, kb_a, n_b, kb_b);
+  int n = 0;
+  for (int p = 0; p < pairs; ++p) {
+    const PairShare s = share_of(d, p, pairs);
+    for (int k = 0; k < s.count(); ++k) units[n++] = s.unit(k);
+    ends[p] = n;
+  }
+  return busiest_pair(d, std::max(kb_a, kb_b), std::min(kb_a, kb_b), pairs);
+}
 """
 
 
@@ -49,7 +60,21 @@ def compile_plan(folder: str) -> ctypes.CDLL:
     for f in (L.forward, L.backward):
         f.restype = None
         f.argtypes = [ctypes.c_long] * 3 + [ctypes.c_int, ctypes.POINTER(ctypes.c_int)]
+    L.deal.restype = ctypes.c_long
+    L.deal.argtypes = [ctypes.c_int, ctypes.c_long, ctypes.c_int, ctypes.c_long, ctypes.c_int,
+                       ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int)]
     return L
+
+
+def deal(L: ctypes.CDLL, n_a: int, kb_a: int, n_b: int, kb_b: int, pairs: int):
+    """(units of each pair, the busiest pair's k-blocks)."""
+    units, ends = (ctypes.c_int * (n_a + n_b))(), (ctypes.c_int * pairs)()
+    most = L.deal(n_a, kb_a, n_b, kb_b, pairs, units, ends)
+    out, at = [], 0
+    for p in range(pairs):
+        out.append(list(units[at:ends[p]]))
+        at = ends[p]
+    return out, most
 
 
 def forms(L: ctypes.CDLL, T: int, D: int, F: int) -> set:

@@ -68,3 +68,16 @@ def test_kept_values_are_those_of_dropout(T):
     kept = torch.from_numpy(keep_mask(Z.numel(), 0.3, 6)).cuda().view(Z.shape)
     assert torch.equal(Y[~kept], want[~kept])
     assert ((Y - want).abs() <= 3.1 * BF * torch.maximum(Y.abs(), want.abs()) + 1e-37).all()
+
+
+@pytest.mark.parametrize("size", [(512, 2048, 24320), (339, 4040, 11680)])
+def test_more_than_2048_units(size):
+    """dX and dW in one launch of CTA pairs: few long units beside thousands of
+    short ones."""
+    x = _inputs(*size, seed=42)
+    ws = ss.ffn_workspace(*size)
+    _, saved = ss.ffn_forward(*_weights(x), ws, save=True)
+    want = _backward_check(x, saved, "silu", ws=ws)
+    for _ in range(3):
+        g = ss.ffn_backward(x["dY"], *_weights(x), saved, ws)
+        assert all(torch.equal(g[k], want[k]) for k in want)
