@@ -369,6 +369,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
+          tc_fence_after();
           const uint32_t a_addr = tiles + s * L::STAGE_BYTES;
           const uint32_t b_addr = a_addr + L::A_BYTES;
           const int sn = s + 1 == STAGES ? 0 : s + 1;
