@@ -12,6 +12,7 @@ tensors, results on the current stream of the tensors' device.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 import torch
@@ -66,7 +67,8 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.curre
 # asks the cheap questions first and goes through _need, which says what is
 # wrong, only where one of them fails.
 
-_BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
+_BF16, _U8 = torch.bfloat16, torch.uint8
+_U64 = 0xFFFFFFFFFFFFFFFF
 
 
 def _fits(t, dtype, index, shape) -> bool:
@@ -90,16 +92,20 @@ def _call(fn, index, *args):
 
 
 def _dropout_spec(p, seed, offset, device):
-    if offset < 0:
-        raise ValueError(f"offset must not be negative, got {offset}")
+    if not 0 <= offset <= _U64:
+        raise ValueError(f"offset must be in [0, 2^64), got {offset}")
     if seed.__class__ is int:
-        return DropoutSpec(p, seed & 0xFFFFFFFFFFFFFFFF, None, offset)
+        return DropoutSpec(p, seed & _U64, None, offset)
     if isinstance(seed, torch.Tensor):
         _need(seed, "seed", torch.int64, device)
         if seed.numel() != 1:
             raise ValueError(f"seed must hold one value, got {seed.numel()}")
         return DropoutSpec(p, 0, seed.data_ptr(), offset)
-    return DropoutSpec(p, int(seed) & 0xFFFFFFFFFFFFFFFF, None, offset)
+    try:
+        seed = operator.index(seed)
+    except TypeError:
+        raise TypeError(f"seed must be an int or an int64 CUDA tensor, got {seed!r}") from None
+    return DropoutSpec(p, seed & _U64, None, offset)
 
 
 def _dropout_args(x, name, out, p, seed, offset):

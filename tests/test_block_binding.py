@@ -3,6 +3,7 @@ import os
 import subprocess
 import sys
 
+import numpy as np
 import pytest
 import torch
 
@@ -47,3 +48,25 @@ def test_current_stream_by_the_public_calls(monkeypatch):
         y = ss.dropout(x, 0.1, 3)
     side.synchronize()
     assert torch.equal(y, want)
+
+
+def _spec(seed, offset=0):
+    s = block._dropout_spec(0.1, seed, offset, None)
+    return s.seed, s.offset
+
+
+def test_seeds_and_offsets():
+    """Whole numbers of any kind, taken modulo 2^64 (seed) or as they are (offset);
+    nothing is cut off in silence."""
+    for one in (1, True, np.int32(1), np.uint64(1)):
+        assert _spec(one, 5) == (1, 5)
+    assert _spec(-1)[0] == 2 ** 64 - 1 and _spec(2 ** 64 + 3)[0] == 3
+    assert _spec(0, 2 ** 64 - 1)[1] == 2 ** 64 - 1
+    for seed in (0.5, 1.0, "1", None, np.float64(2)):
+        with pytest.raises(TypeError):
+            _spec(seed)
+    for offset in (-1, 2 ** 64, 2 ** 64 + 5):
+        with pytest.raises(ValueError):
+            _spec(0, offset)
+    with pytest.raises(TypeError):
+        _spec(0, 3.0)
