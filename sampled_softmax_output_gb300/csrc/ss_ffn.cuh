@@ -149,7 +149,7 @@ __device__ __forceinline__ void dispatch_act_low(int act, bool low, F&& fn) {
 // 16ths: bits 12 to 15 are the half byte, rounded to nearest. 15 is the largest.
 __device__ __forceinline__ uint32_t low_bits(float x, uint32_t hi) {
   return static_cast<uint32_t>(
-      __viaddmin_s32(__float_as_int(x), 0x8800 - static_cast<int>(hi), 0xffff));
+      __viaddmin_s32(static_cast<int>(__float_as_uint(x) - hi), 0x8800, 0xffff));
 }
 // byte 1 of each of four words
 __device__ __forceinline__ uint32_t second_bytes(const uint32_t (&d)[4]) {

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import sampled_softmax_output_gb300 as ss
-from block_util import BF, keep_mask
+from block_util import BF, keep_mask, refined
 from ffn_plan import ACT_SIZES, FORM_SIZES
 from test_ffn_gpu import _backward_check, _forward_check, _inputs, _weights
 
@@ -81,3 +81,29 @@ def test_more_than_2048_units(size):
     for _ in range(3):
         g = ss.ffn_backward(x["dY"], *_weights(x), saved, ws)
         assert all(torch.equal(g[k], want[k]) for k in want)
+
+
+@pytest.mark.parametrize("T", [3, 2100])
+def test_low_bits_around_zero(T):
+    """Sums of either sign that round to a zero or to bf16's smallest values: with
+    their low bits they are off by half a 16th of a step of 2^-133, but half a step
+    above an even bf16 (a tie, rounded down) is 16 16ths' place in a half byte that
+    ends at 15: there by a whole 16th, 2^-137. (The 256th more of (n - 8) 16ths
+    that the second half byte adds is below 2^-141: 1.01 covers it.) Or nothing is
+    left out where the products themselves were flushed to zero."""
+    D, F = 8, 256
+    X, W = torch.zeros(T, D, device="cuda"), torch.zeros(F, D, device="cuda")
+    X[:, 0] = 2.0 ** -60
+    # sums k 2^-137, k = -128 .. 127: up to four steps
+    k = torch.arange(F, device="cuda") - F // 2
+    W[:, 0] = k * 2.0 ** -77
+    W = W.to(torch.bfloat16)
+    _, saved = ss.ffn_forward(X.to(torch.bfloat16), W, W, torch.ones(D, F, device="cuda").to(
+        torch.bfloat16), ss.ffn_workspace(T, D, F), save=True)
+    exact = k.double() * 2.0 ** -137
+    bound = torch.where(k.abs() % 32 == 8, 2.0 ** -137, 2.0 ** -138)
+    G, U, _ = refined(saved)
+    for fine, bf in ((G, saved[0]), (U, saved[1])):
+        off = (fine.double() - exact).abs()
+        flushed = (bf == 0) & (fine == 0)
+        assert ((off <= 1.01 * bound) | flushed).all()
