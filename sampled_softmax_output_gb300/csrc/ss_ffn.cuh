@@ -204,9 +204,19 @@ struct FfnBackward {
   int num_sms;
 };
 
-// y = x with the dropped elements zeroed, not scaled (ss_dropout.cu)
-cudaError_t launch_drop_mask(const uint16_t* x, int64_t n, const DropArgs& drop, uint16_t* y,
-                             int num_sms, cudaStream_t stream);
+// ---------------------------------------------------------- tiles and maps
+
+inline int tiles_of(int64_t n, int tile) { return static_cast<int>(cdiv(n, tile)); }
+
+// K-major operand [rows, k]: boxes of box_rows rows x 64 of k. MN-major operand
+// [k, cols]: boxes of 64 columns x 64 of k. ld: elements between rows.
+inline bool map_kmajor(CUtensorMap* m, const uint16_t* p, int64_t rows, int64_t k, int64_t ld,
+                       int box_rows = 128) {
+  return make_bf16_map(m, p, k, rows, ld * 2, 64, box_rows);
+}
+inline bool map_mnmajor(CUtensorMap* m, const uint16_t* p, int64_t k, int64_t cols, int64_t ld) {
+  return make_bf16_map(m, p, cols, k, ld * 2, 64, 64);
+}
 
 // ------------------------------------------------------------- the kernels
 

@@ -152,7 +152,6 @@ struct PairArgs {
   int n_jobs, group_m;
   int T, D, F, act;
   int ldo;  // elements between the rows of G, U, A (gate/up) or dG, dU (dA)
-  const uint16_t *G_in, *U_in;
   uint16_t *G, *U, *A;
   // kUp: G, U, A (stores); kGradAct: G, U (loads), dG, dU (stores)
   CUtensorMap m[4];
@@ -880,17 +879,6 @@ bool rows_on_sectors(int64_t cols, std::initializer_list<const void*> ps) {
          });
 }
 
-int tiles_of(int64_t n, int tile) { return static_cast<int>((n + tile - 1) / tile); }
-
-// K-major operand [rows, k]: boxes of box_rows rows x 64 of k. MN-major operand
-// [k, cols]: boxes of 64 columns x 64 of k. ld: elements between rows.
-bool map_kmajor(CUtensorMap* m, const uint16_t* p, int64_t rows, int64_t k, int64_t ld,
-                int box_rows = 128) {
-  return make_bf16_map(m, p, k, rows, ld * 2, BK, box_rows);
-}
-bool map_mnmajor(CUtensorMap* m, const uint16_t* p, int64_t k, int64_t cols, int64_t ld) {
-  return make_bf16_map(m, p, cols, k, ld * 2, 64, BK);
-}
 bool map_chunk(CUtensorMap* m, const uint16_t* p, int64_t rows, int64_t cols, int64_t ld) {
   return make_bf16_map(m, p, cols, rows, ld * 2, 32, 128);
 }
@@ -913,10 +901,6 @@ cudaError_t launch_pair(PairArgs<KIND>& p, int num_sms, cudaStream_t s) {
   constexpr int smem = Gemm2Smem<kBN, PairCfg<KIND>::kStages, epi_bytes<KIND>()>::TOTAL;
   return launch_pdl(k_ffn_pair<KIND, BN>, dim3(2 * pairs), dim3(kThreads), smem, s, p);
 }
-
-}  // namespace
-
-namespace {
 
 template <int KIND, int BN>
 cudaError_t gate_up(const FfnForward& f, cudaStream_t s) {
@@ -956,7 +940,7 @@ cudaError_t grad_act(const FfnBackward& f, cudaStream_t s) {
   j.n_tiles = tiles_of(f.F, BN);
   p.n_jobs = 1;
   p.T = f.T, p.D = f.D, p.F = f.F, p.act = f.act, p.scale = f.scale;
-  p.G_in = f.G, p.U_in = f.U, p.ldo = f.ldg, p.G = f.dG, p.U = f.dU;
+  p.ldo = f.ldg, p.G = f.dG, p.U = f.dU;
   p.R = const_cast<uint8_t*>(f.R), p.ldr = f.ldr;
   p.status = f.status;
   return launch_pair<KIND, BN>(p, f.num_sms, s);

@@ -471,8 +471,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
 
 // ------------------------------------------------------------- host side
 
-int tiles_of(int64_t n, int tile) { return static_cast<int>((n + tile - 1) / tile); }
-
+// launch_pdl with the cluster's size beside it
 template <int KIND, int BN>
 cudaError_t launch_split_bn(const SplitArgs<KIND>& p, int S, cudaStream_t s) {
   auto kern = k_ffn_split<KIND, BN>;
@@ -508,16 +507,6 @@ cudaError_t launch_split(SplitArgs<KIND>& p, const SplitPlan& plan, cudaStream_t
     if (plan.bn == 64) return launch_split_bn<KIND, 64>(p, plan.cluster, s);
   }
   return launch_split_bn<KIND, 128>(p, plan.cluster, s);
-}
-
-// K-major operand [rows, k]: boxes of box_rows x 64 of k
-bool map_kmajor(CUtensorMap* m, const uint16_t* p, int64_t rows, int64_t k, int64_t ld,
-                int box_rows) {
-  return make_bf16_map(m, p, k, rows, ld * 2, BK, box_rows);
-}
-// MN-major operand [k, cols]: boxes of 64 columns x 64 of k
-bool map_mnmajor(CUtensorMap* m, const uint16_t* p, int64_t k, int64_t cols, int64_t ld) {
-  return make_bf16_map(m, p, cols, k, ld * 2, 64, BK);
 }
 
 }  // namespace
