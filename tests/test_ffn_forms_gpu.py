@@ -1,5 +1,7 @@
 """The feed-forward block in every form that its choice of kernels has, against 64
 bits (test_ffn_plan_host.py: that these sizes reach them all)."""
+import concurrent.futures
+
 import pytest
 import torch
 
@@ -107,3 +109,32 @@ def test_low_bits_around_zero(T):
         off = (fine.double() - exact).abs()
         flushed = (bf == 0) & (fine == 0)
         assert ((off <= 1.01 * bound) | flushed).all()
+
+
+def test_two_host_threads():
+    """Calls of two threads at once, a stream and a workspace each."""
+    sizes = [(300, 264, 392), (2100, 776, 1288)]
+    blocks = [(_inputs(*s, seed=43), ss.ffn_workspace(*s), torch.cuda.Stream()) for s in sizes]
+
+    def step(x, ws):
+        Y, saved = ss.ffn_forward(*_weights(x), ws, residual=x["residual"], p=0.1, seed=4,
+                                  save=True)
+        g = ss.ffn_backward(x["dY"], *_weights(x), saved, ws, p=0.1, seed=4)
+        return [ss.dropout(Y, 0.2, 5), *g.values()]
+
+    want = [step(x, ws) for x, ws, _ in blocks]
+    torch.cuda.synchronize()
+
+    def run(block):
+        x, ws, stream = block
+        with torch.cuda.stream(stream):
+            outs = [step(x, ws) for _ in range(30)]
+            stream.synchronize()
+        return outs
+
+    with concurrent.futures.ThreadPoolExecutor(2) as ex:
+        got = list(ex.map(run, blocks))
+    for (_, ws, _), outs, ref in zip(blocks, got, want):
+        assert ss.read_status(ws)[0] == 0
+        for out in outs:
+            assert all(torch.equal(a, b) for a, b in zip(out, ref))
