@@ -99,14 +99,16 @@ ss_status ss_dropout_backward(const void* dy, int64_t n, int dtype, const ss_dro
  * workspace serves the forward and the backward of a block, in any order, and
  * any smaller T; calls that may run at the same time need one each (two
  * captured graphs that are replayed at the same time too). A device wait that
- * timed out is recorded in the status word (ss_read_status); later calls on
- * the workspace then do nothing until its header is zeroed.
+ * timed out is recorded in the status word (ss_read_status); what that call
+ * wrote is unspecified. Later calls on the workspace then do nothing until its
+ * header is zeroed (an empty batch's zeroes are written all the same).
  */
 size_t ss_ffn_workspace_size(int64_t T, int64_t D, int64_t F); /* 0: invalid sizes */
 
 /*
  *   X [T, D], Wg, Wu [F, D], Wd [D, F] bf16; residual [T, D] bf16 or NULL.
- *   Y [T, D] bf16 out (may be `residual`).
+ *   Y [T, D] bf16 out (may be `residual`; else no output may overlap an input
+ *   or another output).
  *   G, U, A [T, F] bf16 out: what the backward needs; all three, or all NULL
  *   (no backward follows). A is rounded to bf16 before the down projection,
  *   from G and U in fp32.

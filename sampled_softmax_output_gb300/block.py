@@ -275,8 +275,9 @@ def ffn_backward(dY: torch.Tensor, X: torch.Tensor, Wg: torch.Tensor, Wu: torch.
     """The gradients of ffn_forward (ss_ffn_backward) from dY [T, D] and `saved`
     (that of ffn_forward, or three [T, F] tensors G, U, A): {"dX", "dWg",
     "dWu", "dWd"}, dX bf16 and the weight gradients of dw_dtype (fp32 or bf16),
-    zero-filled when accumulate=True and none is given. The gradient of the
-    residual is dY itself."""
+    zero-filled when accumulate=True and none is given. Outputs that are given must
+    not overlap the inputs or one another. The gradient of the residual is dY
+    itself."""
     index, T, D, F = _block_args(X, Wg, Wu, Wd, ws)
     dev = X.device
     dw = _DTYPES.get(dw_dtype)

@@ -18,15 +18,16 @@
 // what an epilogue moves through shared memory or to global memory comes on top,
 // about 9 cycles a KB. So outputs are stored from registers, 32 bytes a lane,
 // wherever rows lie on 32-byte boundaries (gate/up with G, U and A kept: 784 ->
-// 675 cycles a k-block at D 768); else (gate/up, dA) through shared memory by
+// 675 cycles a k-block at D 768, 745 with their low bits); else (gate/up, dA) through shared memory by
 // TMA, since half sectors cost more than that (T 3001, D 1352, F 3640: 56 us
 // against 68). In a steady loop the board's power does: it draws 1380 W at 1.55
 // to 1.75 GHz.
-//   in-kernel time, rate      gate/up       down          dA            dX and dW
-//   T 65536, D 768, F 2048    249 us 1.66   133 us 1.55   206 us 1.00   567 us 1.82 PFLOP/s
-//   T 8192, D 2048, F 5504    205    1.80   112    1.65   143    1.29   508    1.82
-// (K-blocks lost to the last, partly filled round of tiles included; without the
-// low bits of G and U, which add 20 and 28 us to the first and third column at
+//   one launch at a time      gate/up       down          dA            dX and dW
+//   T 65536, D 768, F 2048    285 us 1.45   154 us 1.34   240 us 0.86   555 us 1.86 PFLOP/s
+//   T 8192, D 2048, F 5504    226    1.64   129    1.43   165    1.12   507    1.82
+// (As a training step calls them: low bits of G and U written and read, dropout and
+// residual in the down projection; launch, exit and the last, partly filled round of
+// tiles included. The low bits are 20 and 28 us of the first and third column at
 // T 65536, 7 and 6 us at T 8192.)
 //
 // Roles per CTA: warp 0 TMA producer, warp 1 MMA issuer (the leader's), warps
@@ -865,7 +866,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // element of dA, bound that product: 256 x 256 elements move 512 KB, as long as
 // about 17 k-blocks. kGradActWide leaves more shared-memory bandwidth to the
 // MMAs (T 16384, D 1024, F 4096: 129 us against 135); kGradAct keeps more
-// copies in flight (T 65536, D 768, F 2048: 205 us against 225).
+// copies in flight (T 65536, D 768, F 2048: 205 us against 225; both sides without
+// the low bits).
 constexpr int kActWideKb = 16;
 
 // The units walk groups of this many row tiles column by column: a round of

@@ -6,7 +6,7 @@
 // the MMA's M (128 rows of weights) and the tokens on its N (16 to 128). One
 // token thus costs a 16-wide MMA next to the weights' bytes, which bound the
 // decoding forms: every weight is read once, by TMA, and all SMs stream (T 16,
-// D 4096, F 12288: 302 MB in 51 us, 5.9 TB/s; tiles of 56 to 128 rows, so that
+// D 4096, F 12288: 302 MB in 53 us, 5.7 TB/s; tiles of 56 to 128 rows, so that
 // the CTAs number the SMs exactly, took as long).
 // Small batches of training have too few 256 x 256 tiles for 76 CTA pairs;
 // here a tile is an eighth of that and K gives up to eight CTAs more.
