@@ -380,8 +380,8 @@ def _workspace(*size):
 
 def _own_loss(ss, s, c, logp, ws):
     if c["op"] == "policy":
-        return ss.policy_loss(logp, s["old"], s["advantage"], ref_logp=s["ref"], weight=s["weight"],
-                              clip=CLIP, kl=c["kl"])
+        return ss.policy_loss(logp, s["old"], s["advantage"], ref_logp=s["ref"],
+                              weight=s["weight"], clip=CLIP, kl=c["kl"])
     if c["op"] == "preference":
         return ss.preference_loss(logp, s["offsets"], ws, ref_logp=s["ref"], weight=s["weight"],
                                   beta=BETA, kind=c["kind"],
@@ -400,9 +400,9 @@ def _run_own(s, c):
     if c["op"] == "score":
         logp, lse = ss.logprobs(s["H"], s["W"], s["ids"], ws, **head)
         return {"logp": logp, "lse": lse}
-    logp, _, saved = ss.logprobs(s["H"], s["W"], s["ids"], ws, save=True, **head)
+    logp, lse = ss.logprobs(s["H"], s["W"], s["ids"], ws, **head)
     out = _own_loss(ss, s, c, logp, ws)
-    dH, dW = ss.logprobs_backward(out.pop("dlogp"), s["H"], s["W"], s["ids"], saved, ws,
+    dH, dW = ss.logprobs_backward(out.pop("dlogp"), s["H"], s["W"], s["ids"], logp, lse, ws,
                                   dw_dtype=BF16, **head)
     return {**out, "logp": logp, "dH": dH, "dW": dW}
 
