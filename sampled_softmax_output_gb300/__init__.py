@@ -611,3 +611,7 @@ def quantize_e4m3(x: torch.Tensor, ws: torch.Tensor):
 from .block import (  # noqa: E402
     ACTS, HEADER_BLOCK, MAX_F, DropoutSpec, FfnSaved, dropout, dropout_backward, ffn_backward,
     ffn_forward, ffn_workspace, ffn_workspace_size)
+# The log-probabilities and losses behind the head (include/ss_logprob.h).
+from .logprob import (  # noqa: E402
+    HEADER_LOGPROB, MAX_IDS, PREFERENCES, distill_loss, logprob_workspace, logprob_workspace_size,
+    logprobs, logprobs_backward, policy_loss, preference_loss)

@@ -23,7 +23,8 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libss.so")
 SOURCES = ["ss_api.cu", "ss_candidates.cu", "ss_gemm_logits.cu", "ss_gemm_logits_mtp.cu",
            "ss_gemm_grads.cu", "ss_dropout.cu", "ss_ffn_pair.cu", "ss_ffn_split.cu",
-           "ss_ffn_api.cu"]
+           "ss_ffn_api.cu", "ss_logprob_api.cu", "ss_logprob_fwd.cu",
+           "ss_logprob_gemm.cu", "ss_losses.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -46,7 +47,7 @@ def _flags(verbose: bool) -> list[str]:
 def _deps() -> list[str]:
     files = [os.path.join(CSRC, s) for s in SOURCES]
     files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    files += [os.path.join(ROOT, "include", h) for h in ("ss.h", "ss_block.h")]
+    files += [os.path.join(ROOT, "include", h) for h in ("ss.h", "ss_block.h", "ss_logprob.h")]
     files.append(os.path.abspath(__file__))
     return files
 

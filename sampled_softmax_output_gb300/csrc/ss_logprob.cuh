@@ -1,0 +1,45 @@
+// ss_logprob.cuh -- what the sources of the head's log-probabilities share: the
+// problem as the launchers take it.
+#pragma once
+
+#include "ss_internal.h"
+#include "ss_logprob.h"
+#include "ss_ptx.cuh"
+#include "ss_shared.h"
+
+namespace ss {
+
+struct LogprobArgs {
+  const uint16_t *H, *W;
+  int T, V, D;
+  HeadCap head;
+  float cap, tau;
+  int* status;
+  int num_sms;
+};
+
+// ---- ss_logprob_fwd.cu
+
+// The ids [T, K] of each 32 tokens sorted by the 128 columns they fall into, `bins`
+// = 2 ceil(V / 256) of them, for the kernel below.
+cudaError_t launch_bin_ids(const LogprobArgs& p, const int32_t* ids, int K, int bins,
+                           uint32_t* sorted, uint16_t* bin_ends, cudaStream_t s);
+// part[c][t]: the largest logit of row t among columns 128 c to 128 c + 127 and the
+// sum of the exponentials above it, c < bins; (-inf, 0) past the end. z [T, K]: the
+// ids' logits (absent ones are left alone).
+cudaError_t launch_logprob_partials(const LogprobArgs& p, int K, const uint32_t* sorted,
+                                    const uint16_t* bin_ends, float2* part, float* z,
+                                    cudaStream_t s);
+
+// ---- ss_logprob_gemm.cu
+
+// G[t, j] = bf16(coef[t] exp(z[t, j] - lse[t]) dz/ds), 0 where coef[t] = 0. G [T, ldG]
+cudaError_t launch_logprob_g(const LogprobArgs& p, const float* coef, const float* lse,
+                             uint16_t* G, int64_t ldG, cudaStream_t s);
+// dH[t] = rowfac[t] (G W)[t], dW (=|+=) *scale G^T Hs; null: a factor of 1
+cudaError_t launch_logprob_grads(const LogprobArgs& p, const uint16_t* G, int64_t ldG,
+                                 const uint16_t* Hs, const float* rowfac, const float* scale,
+                                 uint16_t* dH, void* dW, int dw_fp32, int accumulate,
+                                 cudaStream_t s);
+
+}  // namespace ss

@@ -1,0 +1,446 @@
+// ss_logprob_fwd.cu -- the softmax partials of the head's log-probabilities over
+// the whole vocabulary: logits S = H W^T tile by tile (M = T, N = V, K = D) on CTA
+// pairs, of which only (max, sum of exponentials) per row and 128 columns leave
+// the chip.
+//
+// A log-probability is the difference of two numbers near 10, so the logits want
+// more than the tensor core's accumulator gives: it truncates after every 16
+// products, and the loss grows with the sum's size and length (the log-sum-exp of
+// logits of standard deviation 3 comes out 6e-6 too small at D 768 and 1.7e-5 at
+// D 2048, the same way for every token, where fp32 sums rounded to nearest are
+// 1e-6 off either way). So K is cut into runs of kRunKb k-blocks, each in a TMEM
+// accumulator of its own; the epilogue warps add the runs in registers, rounded to
+// nearest, 128 columns of a row per thread.
+//
+// The chosen ids' logits are taken from those registers too: what truncation is
+// left then falls on both terms of the difference alike, and no row of W is read
+// again (16384 tokens of 64 ids: gathered rows took 228 us). k_bin_ids sorts the
+// ids of each 32 tokens by the 128 columns they fall into; a warp, which holds
+// those columns of those tokens, looks up the few that are its own.
+//
+// The protocol is that of ss_gemm2.cuh (pairs of CTAs on 256 x 256 tiles, warp 0
+// TMA producer, warp 1 MMA issuer, eight epilogue warps, bounded waits); the two
+// accumulators alternate between runs instead of tiles. A tile's exponentials run
+// beside the next tile's first runs, as its sums are in registers by then.
+#include <algorithm>
+
+#include "ss_gemm.cuh"
+#include "ss_gemm2.cuh"
+#include "ss_logprob.cuh"
+
+namespace ss {
+
+namespace {
+
+constexpr int kRunKb = 4;  // k-blocks of 64 in one accumulator
+constexpr int kIdRows = 32;  // tokens whose ids are sorted together: an epilogue warp's
+constexpr int kBN = kBnLogits;
+constexpr int kStages = 6;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kHalf = kBN / 2;  // columns of a row per epilogue thread
+static_assert(kHalf == 128, "seven bits of a sorted id");
+constexpr int kMostBins = SS_MAX_V / kHalf;
+using L = Gemm2Smem<kBN, kStages, 0>;
+
+struct FwdArgs {
+  int T, V, m_tiles, n_tiles, k_blocks, group_m;
+  HeadCap head;
+  float2* part;  // [2 n_tiles][T]
+  int K;
+  const uint32_t* sorted;    // [groups][32 K]: column in its bin, row and k of each id
+  const uint16_t* bin_ends;  // [groups][2 n_tiles]: where each bin's ids end
+  float* z;                  // [T, K]
+  int* status;
+};
+
+// The ids of 32 tokens by column bin, as column | row << 7 | k << 12, and where
+// each bin ends. The order within a bin is any; each id has a place of its own in
+// z. A block per 32 tokens.
+__global__ void __launch_bounds__(256) k_bin_ids(const int32_t* __restrict__ ids, int K, int T,
+                                                 int V, int bins, uint32_t* __restrict__ sorted,
+                                                 uint16_t* __restrict__ bin_ends, int* status) {
+  __shared__ int count[kMostBins];
+  __shared__ int s_warp[8];
+  __shared__ int s_go;
+  pdl_enter();
+  if (threadIdx.x == 0) s_go = read_status(status) == 0;
+  for (int i = threadIdx.x; i < bins; i += 256) count[i] = 0;
+  __syncthreads();
+  if (!s_go) return;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kIdRows;
+  const int n = (T - t0 < kIdRows ? static_cast<int>(T - t0) : kIdRows) * K;
+  const int32_t* mine = ids + t0 * K;
+  bool bad = false;
+  for (int i = threadIdx.x; i < n; i += 256) {
+    const int id = __ldg(mine + i);
+    bad |= id < -1 || id >= V;
+    if (id >= 0 && id < V) atomicAdd(&count[id / kHalf], 1);
+  }
+  if (bad) set_status(status, SS_ERR_TARGET_RANGE);
+  __syncthreads();
+  // exclusive sums: consecutive bins per thread, then over the warps
+  const int per = (bins + 255) / 256, b0 = threadIdx.x * per;
+  int sum = 0;
+  for (int b = b0; b < min(b0 + per, bins); ++b) sum += count[b];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  int upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 31) s_warp[warp] = upto;
+  __syncthreads();
+  int at = upto - sum;
+  for (int w = 0; w < warp; ++w) at += s_warp[w];
+  uint16_t* ends = bin_ends + static_cast<int64_t>(blockIdx.x) * bins;
+  for (int b = b0; b < min(b0 + per, bins); ++b) {
+    const int c = count[b];
+    count[b] = at;
+    at += c;
+    ends[b] = static_cast<uint16_t>(at);
+  }
+  __syncthreads();
+  uint32_t* out = sorted + t0 * K;
+  for (int i = threadIdx.x; i < n; i += 256) {
+    const int id = __ldg(mine + i);
+    if (id < 0 || id >= V) continue;
+    out[atomicAdd(&count[id / kHalf], 1)] =
+        static_cast<uint32_t>(id % kHalf) | static_cast<uint32_t>(i / K) << 7 |
+        static_cast<uint32_t>(i % K) << 12;
+  }
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// tcgen05.wait::ld that names the registers it waits for
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+// acc[k] (+)= the 128 columns from `taddr` on, two to a word
+template <bool FIRST>
+__device__ __forceinline__ void take_run(uint32_t taddr, uint64_t (&acc)[kHalf / 2]) {
+  uint32_t ra[16], rb[16];
+  auto add = [&](const uint32_t(&r)[16], int c) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint64_t v = f32x2_bits(r[2 * k], r[2 * k + 1]);
+      acc[c * 8 + k] = FIRST ? v : add_f32x2(acc[c * 8 + k], v);
+    }
+  };
+  tmem_ld16(taddr, ra);
+#pragma unroll
+  for (int c = 0; c < kHalf / 16; c += 2) {
+    tmem_wait16(ra);
+    tmem_ld16(taddr + (c + 1) * 16, rb);
+    add(ra, c);
+    tmem_wait16(rb);
+    if (c + 2 < kHalf / 16) tmem_ld16(taddr + (c + 2) * 16, ra);
+    add(rb, c + 1);
+  }
+}
+
+// acc[i] for an i that the warp agrees on: a tree of branches, as registers have no
+// index
+template <int LO, int N>
+__device__ __forceinline__ uint64_t pick(const uint64_t (&acc)[kHalf / 2], int i) {
+  if constexpr (N == 1) return acc[LO];
+  else return i < LO + N / 2 ? pick<LO, N / 2>(acc, i) : pick<LO + N / 2, N / 2>(acc, i);
+}
+
+template <bool CAP>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    k_logprob_forward(const __grid_constant__ CUtensorMap tmH,
+                      const __grid_constant__ CUtensorMap tmW,
+                      const __grid_constant__ FwdArgs p) {
+  pdl_enter();
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int s_go;
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  GemmCtrl* ctrl = reinterpret_cast<GemmCtrl*>(smem + L::CTRL_OFFSET);
+  const uint32_t tiles = smem_u32(smem);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+
+  // both CTAs of a pair take the same decision
+  if (threadIdx.x == 0) s_go = read_status(p.status) == 0;
+  cluster_sync_all();
+  if (threadIdx.x == 0)
+    s_go = s_go && ld_shared_cluster_u32(mapa_shared(smem_u32(&s_go), rank ^ 1u));
+  cluster_sync_all();
+  if (!s_go) return;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&ctrl->full[s], 1);
+      mbar_init(&ctrl->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&ctrl->tfull[b], 1);
+      mbar_init(&ctrl->tempty[b], 2 * kEpiWarps);
+    }
+    mbar_init(&ctrl->drain, 1);
+    ctrl->abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_map(&tmH);
+    tma_prefetch_map(&tmW);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&ctrl->tmem_base, 2 * kBN);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = ctrl->tmem_base;
+  volatile int* abort_flag = &ctrl->abort_flag;
+  const GemmShape shp{p.m_tiles, p.n_tiles, p.k_blocks, 0, 0, nullptr, p.group_m};
+  const int num_units = p.m_tiles * p.n_tiles;
+
+  if (warp == 0) {
+    // ------------------------------------------------ producer (both CTAs)
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0, issued = 0, issued_ph = 0;
+      bool ok = true;
+      // W is re-read by every row tile, H by every column tile: both stay in L2
+      const uint64_t keep = l2_evict_last();
+      for (int u = pair; ok && u < num_units; u += npairs) {
+        int mt, nt;
+        unit_tile(shp, u, mt, nt);
+        const int m0 = mt * 2 * BM + static_cast<int>(rank) * BM;
+        const int n0 = nt * kBN + static_cast<int>(rank) * kHalf;
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          if (!mbar_wait(&ctrl->empty[s], ph ^ 1u, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb_local = smem_u32(&ctrl->full[s]);
+          if (rank == 0) mbar_arrive_expect_tx(&ctrl->full[s], 2 * L::STAGE_BYTES);
+          const uint32_t fb = rank == 0 ? fb_local : mapa_shared(fb_local, 0);
+          const uint32_t dst = tiles + s * L::STAGE_BYTES;
+          tma_load_2d_pair(dst, &tmH, fb, kb * BK, m0);
+          tma_load_2d_pair_hint(dst + L::A_BYTES, &tmW, fb, kb * BK, n0, keep);
+          issued |= 1u << s;
+          issued_ph = (issued_ph & ~(1u << s)) | (ph << s);
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (rank == 0) {
+        for (int i = 0; i < kStages; ++i)
+          if ((issued >> i) & 1u) mbar_drain(&ctrl->full[i], (issued_ph >> i) & 1u, p.status);
+      } else if (!ok) {
+        // aborted: the peer cannot observe the leader's barriers; its copies in
+        // flight get a bounded moment to land before shared memory goes
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 200000ull) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMA issuer (leader)
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(2 * BM, kBN, false, false);
+      int s = 0, b = 0;
+      uint32_t ph = 0, aph = 0;
+      bool ok = true;
+      for (int u = pair; ok && u < num_units; u += npairs) {
+        for (int k0 = 0; ok && k0 < p.k_blocks; k0 += kRunKb) {
+          if (!mbar_wait(&ctrl->tempty[b], aph ^ 1u, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(b * kBN);
+          const int k1 = min(k0 + kRunKb, p.k_blocks);
+          for (int kb = k0; kb < k1; ++kb) {
+            if (!mbar_wait(&ctrl->full[s], ph, abort_flag, p.status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a_addr = tiles + s * L::STAGE_BYTES;
+            const uint32_t b_addr = a_addr + L::A_BYTES;
+#pragma unroll
+            for (int k = 0; k < BK / UMMA_K; ++k)
+              mma_bf16_pair(d_tmem, sdesc_sw128(a_addr + k * 32, 16, 1024),
+                            sdesc_sw128(b_addr + k * 32, 16, 1024), idesc,
+                            (kb > k0 || k > 0) ? 1u : 0u);
+            mma_commit_pair(&ctrl->empty[s], 0x3);
+            if (++s == kStages) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+          if (!ok) break;
+          mma_commit_pair(&ctrl->tfull[b], 0x3);
+          if (++b == 2) {
+            b = 0;
+            aph ^= 1u;
+          }
+        }
+      }
+      mma_commit_pair(&ctrl->drain, 0x1);
+      mbar_drain(&ctrl->drain, 0, p.status);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------ epilogue (both CTAs)
+    const int q = warp & 3;         // TMEM lane quarter this warp may access
+    const int cg = (warp - 2) / 4;  // its half of the tile's columns
+    const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + cg * kHalf;
+    const int runs = (p.k_blocks + kRunKb - 1) / kRunKb;
+    int b = 0;
+    uint32_t aph = 0;
+    bool ok = true;
+    for (int u = pair; ok && u < num_units; u += npairs) {
+      int mt, nt;
+      unit_tile(shp, u, mt, nt);
+      const int t0 = (mt * 2 + static_cast<int>(rank)) * BM + q * 32;
+      // this warp's ids, asked for ahead of their use behind the runs
+      int id0 = 0, id1 = 0;
+      uint32_t mine = 0u;  // lane l: the l-th
+      const uint32_t* sorted = p.sorted + static_cast<int64_t>(t0) * p.K;
+      if (t0 < p.T) {
+        const int bin = nt * 2 + cg;
+        const uint16_t* ends = p.bin_ends + static_cast<int64_t>(t0 / kIdRows) * (2 * p.n_tiles);
+        id0 = bin ? __ldg(ends + bin - 1) : 0;
+        id1 = __ldg(ends + bin);
+      }
+      uint64_t acc[kHalf / 2];
+      for (int run = 0; run < runs; ++run) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&ctrl->tfull[b], aph, abort_flag, p.status));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t at = lane_addr + static_cast<uint32_t>(b * kBN);
+        if (run == 0) take_run<true>(at, acc);
+        else take_run<false>(at, acc);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          const uint32_t te = smem_u32(&ctrl->tempty[b]);
+          if (rank == 0) mbar_arrive(&ctrl->tempty[b]);
+          else mbar_arrive_cluster(mapa_shared(te, 0));
+        }
+        if (++b == 2) {
+          b = 0;
+          aph ^= 1u;
+        }
+        if (run == 0 && id0 + lane < id1) mine = __ldg(sorted + id0 + lane);
+      }
+      if (!ok) break;
+      const int t = t0 + lane;
+      const int nv = p.V - (nt * kBN + cg * kHalf);  // valid columns, the same for the warp
+      float m = -INFINITY, s = 0.f;
+      if (nv > 0) {
+        if constexpr (CAP) {
+#pragma unroll
+          for (int k = 0; k < kHalf / 2; ++k) {
+            float x, y;
+            f32x2_split(acc[k], x, y);
+            acc[k] = f32x2(head_z(x, p.head), head_z(y, p.head));
+          }
+        }
+        if (nv < kHalf) {  // the vocabulary ends inside
+#pragma unroll
+          for (int k = 0; k < kHalf / 2; ++k) {
+            float x, y;
+            f32x2_split(acc[k], x, y);
+            acc[k] = f32x2(2 * k < nv ? x : -INFINITY, 2 * k + 1 < nv ? y : -INFINITY);
+          }
+        }
+        for (int i = id0; i < id1; ++i) {
+          const int l = (i - id0) & 31;
+          if (l == 0 && i > id0 && i + lane < id1) mine = __ldg(sorted + i + lane);
+          const uint32_t e = __shfl_sync(0xffffffffu, mine, l);
+          float x, y;
+          f32x2_split(pick<0, kHalf / 2>(acc, static_cast<int>(e & 127u) / 2), x, y);
+          if (lane == static_cast<int>((e >> 7) & 31u))
+            p.z[static_cast<int64_t>(t) * p.K + (e >> 12)] = (e & 1u) ? y : x;
+        }
+        float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kHalf / 2; ++k) {
+          float x, y;
+          f32x2_split(acc[k], x, y);
+          m0 = fmaxf(m0, x);
+          m1 = fmaxf(m1, y);
+        }
+        m = fmaxf(m0, m1);
+        // a row of -infinity alone (or a NaN) has no number to subtract
+        const float r2 = m > -INFINITY ? m * kLog2e : 0.f;
+        const uint64_t k2 = f32x2(kLog2e, kLog2e), nr2 = f32x2(-r2, -r2);
+        uint64_t s0 = f32x2(0.f, 0.f), s1 = s0;
+#pragma unroll
+        for (int k = 0; k < kHalf / 2; k += 2) {
+          float x0, y0, x1, y1;
+          f32x2_split(fma_f32x2(acc[k], k2, nr2), x0, y0);
+          f32x2_split(fma_f32x2(acc[k + 1], k2, nr2), x1, y1);
+          s0 = add_f32x2(s0, f32x2(ex2_approx(x0), ex2_approx(y0)));
+          s1 = add_f32x2(s1, f32x2(ex2_approx(x1), ex2_approx(y1)));
+        }
+        float a0, a1, a2, a3;
+        f32x2_split(s0, a0, a1);
+        f32x2_split(s1, a2, a3);
+        s = (a0 + a1) + (a2 + a3);
+      }
+      if (t < p.T) p.part[static_cast<size_t>(nt * 2 + cg) * p.T + t] = make_float2(m, s);
+    }
+  }
+  __syncthreads();
+  cluster_sync_all();  // the leader's MMAs are drained before either CTA frees TMEM
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 2 * kBN);
+  }
+}
+
+// Units walk groups of this many rows column tile by column tile, so that W is
+// read from memory once per group.
+constexpr int kGroupRows = 8192;
+
+}  // namespace
+
+cudaError_t launch_bin_ids(const LogprobArgs& p, const int32_t* ids, int K, int bins,
+                           uint32_t* sorted, uint16_t* bin_ends, cudaStream_t s) {
+  return launch_pdl(k_bin_ids, dim3(static_cast<unsigned>((p.T + kIdRows - 1) / kIdRows)),
+                    dim3(256), 0, s, ids, K, p.T, p.V, bins, sorted, bin_ends, p.status);
+}
+
+cudaError_t launch_logprob_partials(const LogprobArgs& p, int K, const uint32_t* sorted,
+                                    const uint16_t* bin_ends, float2* part, float* z,
+                                    cudaStream_t s) {
+  CUtensorMap tH, tW;
+  const uint64_t row = static_cast<uint64_t>(p.D) * 2;
+  if (!make_bf16_map(&tH, p.H, p.D, p.T, row, BK, BM) ||
+      !make_bf16_map(&tW, p.W, p.D, p.V, row, BK, kHalf))
+    return cudaErrorInvalidValue;
+  const FwdArgs a{p.T,      p.V, (p.T + 2 * BM - 1) / (2 * BM), (p.V + kBN - 1) / kBN, p.D / BK,
+                  kGroupRows / (2 * BM), p.head, part, K, sorted, bin_ends, z, p.status};
+  const int pairs = std::min(a.m_tiles * a.n_tiles, p.num_sms / 2);
+  const dim3 grid(static_cast<unsigned>(2 * pairs)), block(kThreads);
+  return p.cap > 0.f ? launch_pdl(k_logprob_forward<true>, grid, block, L::TOTAL, s, tH, tW, a)
+                     : launch_pdl(k_logprob_forward<false>, grid, block, L::TOTAL, s, tH, tW, a);
+}
+
+}  // namespace ss
