@@ -366,7 +366,8 @@ def test_distill_tail_keeps_its_digits():
     # half a step of both terms, which the division by q shows as p / q
     tol = 2.0 ** -27 * (1 / p1 + 1 / rest) + (EXP + 6 * F32) * (1 + p / (ratio * q))
     assert ((slope / ratio - 1).abs() < tol).all()
-    assert tol.median() < 1e-5
+    # 2^-27 beside 2^-10 is 7.6e-6, beside p' near 0.003 2.5e-6
+    assert tol.median() < 2e-5
 
 
 @pytest.mark.parametrize("tail", [False, True])
