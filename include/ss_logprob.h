@@ -130,8 +130,9 @@ typedef enum ss_preference {
  *   rewards are NaN and the dlogp of its tokens is left as it was.
  *   smoothing (e) in [0, 0.5], 0 but for SS_PREF_SIGMOID; beta > 0.
  *   loss [pairs], reward [2 pairs], dlogp [n] out; dlogp may be logp or ref_logp.
- * Sums are held in fp64, joined in a fixed order. 0 <= n < 2^31, 0 <= pairs <
- * 2^29; pairs = 0: dlogp is zeroed. The workspace needs only its header.
+ * Sums are held in pairs of fp32 numbers (48 bits), joined in a fixed order. 0 <= n
+ * < 2^31, 0 <= pairs < 2^29; pairs = 0: dlogp is zeroed. The workspace needs only its
+ * header, and the call runs whatever the status word holds.
  */
 ss_status ss_preference_loss(const float* logp, const float* ref_logp, const float* weight,
                              const int32_t* offsets, int64_t pairs, int64_t n, int kind,

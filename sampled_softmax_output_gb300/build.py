@@ -24,7 +24,7 @@ LIB = os.path.join(OUT_DIR, "libss.so")
 SOURCES = ["ss_api.cu", "ss_candidates.cu", "ss_gemm_logits.cu", "ss_gemm_logits_mtp.cu",
            "ss_gemm_grads.cu", "ss_dropout.cu", "ss_ffn_pair.cu", "ss_ffn_split.cu",
            "ss_ffn_api.cu", "ss_logprob_api.cu", "ss_logprob_fwd.cu",
-           "ss_logprob_gemm.cu", "ss_losses.cu"]
+           "ss_logprob_gemm.cu", "ss_logprob_grads.cu", "ss_losses.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -36,10 +36,15 @@ cudaError_t launch_logprob_partials(const LogprobArgs& p, int K, const uint32_t*
 // G[t, j] = bf16(coef[t] exp(z[t, j] - lse[t]) dz/ds), 0 where coef[t] = 0. G [T, ldG]
 cudaError_t launch_logprob_g(const LogprobArgs& p, const float* coef, const float* lse,
                              uint16_t* G, int64_t ldG, cudaStream_t s);
-// dH[t] = rowfac[t] (G W)[t], dW (=|+=) *scale G^T Hs; null: a factor of 1
+
+// ---- ss_logprob_grads.cu
+
+// dH[t] = rowfac[t] (G W)[t], dW (=|+=) *scale G^T Hs; null: a factor of 1. part:
+// logprob_part_bytes, 32-byte aligned, for partial sums of dH.
+size_t logprob_part_bytes(int64_t T, int64_t D);
 cudaError_t launch_logprob_grads(const LogprobArgs& p, const uint16_t* G, int64_t ldG,
                                  const uint16_t* Hs, const float* rowfac, const float* scale,
-                                 uint16_t* dH, void* dW, int dw_fp32, int accumulate,
+                                 float* part, uint16_t* dH, void* dW, int dw_fp32, int accumulate,
                                  cudaStream_t s);
 
 }  // namespace ss

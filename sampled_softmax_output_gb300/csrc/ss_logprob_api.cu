@@ -16,14 +16,15 @@ constexpr size_t kHdrScale = 128;  // byte offset in the header: the scale of dW
 size_t up1024(size_t x) { return (x + 1023) / 1024 * 1024; }
 
 struct LogprobLayout {
-  size_t part, sorted, bin_ends, coef, f, rowfac, hs, g, total;
+  size_t part, sorted, bin_ends, coef, f, rowfac, hs, dh_part, g, total;
   int64_t ldG;
   int n_parts;
 };
 
 // After the header, the forward's softmax partials and sorted ids, or, in the same
 // place, what the backward pass needs: the coefficients, the factors of H's and of
-// dH's rows, the scaled H, and G. The scale of dW lies in the header.
+// dH's rows, the scaled H, partial sums of dH, and G. The scale of dW lies in the
+// header.
 LogprobLayout logprob_layout(int64_t T, int64_t V, int64_t D, bool backward) {
   LogprobLayout L;
   L.ldG = (V + 63) / 64 * 64;
@@ -36,7 +37,8 @@ LogprobLayout logprob_layout(int64_t T, int64_t V, int64_t D, bool backward) {
   L.f = L.coef + up1024(static_cast<size_t>(T) * sizeof(float));
   L.rowfac = L.f + up1024(static_cast<size_t>(T) * sizeof(float));
   L.hs = L.rowfac + up1024(static_cast<size_t>(T) * sizeof(float));
-  L.g = L.hs + up1024(static_cast<size_t>(T) * D * 2);
+  L.dh_part = L.hs + up1024(static_cast<size_t>(T) * D * 2);
+  L.g = L.dh_part + up1024(logprob_part_bytes(T, D) + 32);
   const size_t both = L.g + up1024(static_cast<size_t>(T) * L.ldG * 2);
   L.total = backward ? std::max(forward, both) : forward;
   return L;
@@ -425,6 +427,9 @@ ss_status ss_logprob_backward(const float* dlogp, const uint16_t* H, const uint1
   float* scale = reinterpret_cast<float*>(ws + kHdrScale);
   uint16_t* Hs = reinterpret_cast<uint16_t*>(ws + L.hs);
   uint16_t* G = reinterpret_cast<uint16_t*>(ws + L.g);
+  // (the workspace itself may lie between two 32-byte boundaries)
+  float* part = reinterpret_cast<float*>(
+      (reinterpret_cast<uintptr_t>(ws + L.dh_part) + 31) / 32 * 32);
   const int iK = static_cast<int>(K), grid = warps_grid(T, p.num_sms);
   cudaError_t e;
   {
@@ -449,8 +454,9 @@ ss_status ss_logprob_backward(const float* dlogp, const uint16_t* H, const uint1
   {
     StageTrace trace(s, "gemm_grads");
     e = launch_logprob_grads(p, G, L.ldG, Hs, iK == 1 ? rowfac : nullptr,
-                             iK == 1 ? scale : nullptr, dH, dW, dw_dtype == SS_FP32, accumulate,
-                             s);
+                             iK == 1 ? scale : nullptr,
+                             part, dH, dW,
+                             dw_dtype == SS_FP32, accumulate, s);
   }
   return e == cudaSuccess ? SS_OK : record_failure("launch gemm_grads", e);
 }

@@ -1,8 +1,6 @@
-// ss_logprob_gemm.cu -- the products of the backward pass of the head's
-// log-probabilities, on the GEMM cores of ss_gemm.cuh and ss_gemm2.cuh:
-//   G  = (a exp(z - lse)) dz/ds   z = H W^T recomputed (M = T, N = V, K = D)
-//   dH = G W                      (M = T, N = D, K = V)
-//   dW = G^T H                    (M = V, N = D, K = T), every vocabulary row
+// ss_logprob_gemm.cu -- the logits again, for the backward pass of the head's
+// log-probabilities: G = (a exp(z - lse)) dz/ds with z = H W^T (M = T, N = V, K = D),
+// on the GEMM cores of ss_gemm.cuh and ss_gemm2.cuh.
 #include "ss_gemm.cuh"
 #include "ss_gemm2.cuh"
 #include "ss_logprob.cuh"
@@ -93,70 +91,6 @@ struct EpiCoef {
   }
 };
 
-// dW tile: rows of the vocabulary, fp32 or bf16, stored or added.
-template <bool FP32>
-struct EpiRows {
-  static constexpr int kStageBytes = 0;
-  static constexpr bool kKeepOperands = false;
-  struct Params {
-    int V, D, accumulate;
-    void* dW;
-    const float* scale;  // null: 1
-  };
-  __device__ static void begin(const Params& p, EpiState& es) {
-    es.f0 = p.scale ? __ldg(p.scale) : 1.f;
-  }
-  __device__ static void finish(const Params&, EpiState&) {}
-  template <int BN, int NCG>
-  __device__ static void apply(const Params& p, int mt, int nt, int row, uint32_t taddr,
-                               EpiState& es, int cg) {
-    constexpr int CPG = BN / 32 / NCG;
-    const float f = es.f0;
-    const int j = mt * BM + row;
-    const bool valid = j < p.V;
-    const int n0 = nt * BN + cg * CPG * 32;
-    const int ncols = min(CPG * 32, p.D - n0);
-    if (ncols <= 0) return;
-    const size_t at = static_cast<size_t>(valid ? j : 0) * p.D + n0;
-    for_tmem_chunks<CPG>(taddr, cg * CPG, [&](const uint32_t(&r)[32], int i) {
-      const int jc = i * 32;  // D is a multiple of 64: whole chunks
-      if (jc >= ncols || !valid) return;
-      if constexpr (FP32) {
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.dW) + at + jc);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          float4 o =
-              make_float4(__uint_as_float(r[4 * k]) * f, __uint_as_float(r[4 * k + 1]) * f,
-                          __uint_as_float(r[4 * k + 2]) * f, __uint_as_float(r[4 * k + 3]) * f);
-          if (p.accumulate) {
-            const float4 old = dst[k];
-            o.x += old.x, o.y += old.y, o.z += old.z, o.w += old.w;
-          }
-          dst[k] = o;
-        }
-      } else {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dW) + at + jc);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t old[4] = {0u, 0u, 0u, 0u};
-          if (p.accumulate) {
-            const uint4 x = dst[k];
-            old[0] = x.x, old[1] = x.y, old[2] = x.z, old[3] = x.w;
-          }
-          uint32_t o[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            o[e] = pack_bf16x2(
-                fmaf(__uint_as_float(r[8 * k + 2 * e]), f, __uint_as_float(old[e] << 16)),
-                fmaf(__uint_as_float(r[8 * k + 2 * e + 1]), f,
-                     __uint_as_float(old[e] & 0xffff0000u)));
-          dst[k] = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-      }
-    });
-  }
-};
-
 template <bool CAP>
 cudaError_t coef_gemm(const LogprobArgs& p, const float* coef, const float* lse, uint16_t* G,
                       int64_t ldG, cudaStream_t s) {
@@ -184,41 +118,12 @@ cudaError_t coef_gemm(const LogprobArgs& p, const float* coef, const float* lse,
                                                                   p.num_sms, s);
 }
 
-template <bool FP32>
-cudaError_t grad_rows(const LogprobArgs& p, const CUtensorMap& tG, const CUtensorMap& tH,
-                      const float* scale, void* dW, int accumulate, cudaStream_t s) {
-  // launched right behind dH, which it neither reads nor writes
-  GemmShape shp{(p.V + 2 * BM - 1) / (2 * BM), (p.D + kBnGrad - 1) / kBnGrad,
-                (p.T + BK - 1) / BK, 2};
-  typename EpiRows<FP32>::Params ep{p.V, p.D, accumulate, dW, scale};
-  return launch_gemm2<kBnGrad, 6, true, true, EpiRows<FP32>, 8>(tG, tH, shp, ep, p.status,
-                                                                p.num_sms, s);
-}
-
 }  // namespace
 
 cudaError_t launch_logprob_g(const LogprobArgs& p, const float* coef, const float* lse,
                              uint16_t* G, int64_t ldG, cudaStream_t s) {
   return p.cap > 0.f ? coef_gemm<true>(p, coef, lse, G, ldG, s)
                      : coef_gemm<false>(p, coef, lse, G, ldG, s);
-}
-
-cudaError_t launch_logprob_grads(const LogprobArgs& p, const uint16_t* G, int64_t ldG,
-                                 const uint16_t* Hs, const float* rowfac, const float* scale,
-                                 uint16_t* dH, void* dW, int dw_fp32, int accumulate,
-                                 cudaStream_t s) {
-  CUtensorMap tGk, tGm, tWm, tHm;
-  const uint64_t row = static_cast<uint64_t>(p.D) * 2, g_row = static_cast<uint64_t>(ldG) * 2;
-  if (!make_bf16_map(&tGk, G, p.V, p.T, g_row, 64, 128) ||
-      !make_bf16_map(&tGm, G, p.V, p.T, g_row, 64, 64) ||
-      !make_bf16_map(&tWm, p.W, p.D, p.V, row, 64, 64) ||
-      !make_bf16_map(&tHm, Hs, p.D, p.T, row, 64, 64))
-    return cudaErrorInvalidValue;
-  const cudaError_t e =
-      launch_grad_h(tGk, tWm, p.T, p.V, p.D, dH, p.status, p.num_sms, s, rowfac);
-  if (e != cudaSuccess) return e;
-  return dw_fp32 ? grad_rows<true>(p, tGm, tHm, scale, dW, accumulate, s)
-                 : grad_rows<false>(p, tGm, tHm, scale, dW, accumulate, s);
 }
 
 }  // namespace ss

@@ -1,0 +1,409 @@
+// ss_logprob_grads.cu -- the two gradients of the head's log-probabilities in one
+// launch of CTA pairs (the protocol of ss_gemm2.cuh):
+//   dH = G W     (M = T, N = D, K = V), rows times their factor
+//   dW = G^T Hs  (M = V, N = D, K = T), every vocabulary row, times one scale
+// With few tokens dH has a handful of 256 x 256 tiles and the whole vocabulary to sum
+// over: then K is cut into slices, whose sums k_join_dh adds in their order (the same
+// bits every time). The tiles of dW keep the other pairs busy meanwhile; a tile of
+// either length goes to the pair that is free first (deal_units of ss_ffn_plan.h).
+#include <algorithm>
+
+#include "ss_ffn.cuh"
+#include "ss_gemm.cuh"
+#include "ss_gemm2.cuh"
+#include "ss_logprob.cuh"
+
+namespace ss {
+
+namespace {
+
+constexpr int kBN = 256;
+constexpr int kStages = 6;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+using L = Gemm2Smem<kBN, kStages, 0>;
+
+struct GradArgs {
+  CUtensorMap tmGk, tmW;   // dH: G [T, V] by rows, W [V, D]
+  CUtensorMap tmGm, tmHs;  // dW: G [T, V] by columns, Hs [T, D]
+  UnitDeal deal;           // units 0 .. n_dw - 1: dW's tiles, then dH's tiles by slice
+  int n_dw, n_nt, m_dh, slices, kb_dw, kb_dh;
+  int T, V, D;
+  uint16_t* dH;
+  float* part;          // slices > 1: [slices][T][D] sums of dH
+  const float* rowfac;  // null: 1
+  void* dW;
+  const float* scale;   // null: 1
+  int accumulate, wide;  // wide: rows of dW on 32-byte boundaries
+  int* status;
+};
+
+struct GradUnit {
+  int dw, mt, nt, slice, kb0, kb1;
+};
+
+__device__ __forceinline__ GradUnit grad_unit(const GradArgs& p, int u) {
+  GradUnit g;
+  g.dw = u < p.n_dw;
+  const int v = g.dw ? u : u - p.n_dw;
+  g.nt = v % p.n_nt;
+  const int r = v / p.n_nt;
+  g.slice = g.dw ? 0 : r / p.m_dh;
+  g.mt = g.dw ? r : r % p.m_dh;
+  g.kb0 = g.dw ? 0 : static_cast<int>(static_cast<int64_t>(p.kb_dh) * g.slice / p.slices);
+  g.kb1 = g.dw ? p.kb_dw
+               : static_cast<int>(static_cast<int64_t>(p.kb_dh) * (g.slice + 1) / p.slices);
+  return g;
+}
+
+// 32 columns of a row of dW
+template <bool FP32>
+__device__ __forceinline__ void store_dw(const GradArgs& p, size_t at, const uint32_t (&r)[32],
+                                         float f) {
+  if constexpr (FP32) {
+    float* dst = static_cast<float*>(p.dW) + at;
+#pragma unroll
+    for (int c = 0; c < 32; c += 8) {
+      uint32_t w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(__uint_as_float(r[c + k]) * f);
+      if (p.accumulate) {
+#pragma unroll
+        for (int k = 0; k < 8; k += 4) {
+          const float4 old = *reinterpret_cast<const float4*>(dst + c + k);
+          w[k] = __float_as_uint(__uint_as_float(w[k]) + old.x);
+          w[k + 1] = __float_as_uint(__uint_as_float(w[k + 1]) + old.y);
+          w[k + 2] = __float_as_uint(__uint_as_float(w[k + 2]) + old.z);
+          w[k + 3] = __float_as_uint(__uint_as_float(w[k + 3]) + old.w);
+        }
+      }
+      if (p.wide) {
+        st_global_v8(dst + c, w);
+      } else {
+        *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(dst + c + 4) = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+    }
+  } else {
+    uint16_t* dst = static_cast<uint16_t*>(p.dW) + at;
+#pragma unroll
+    for (int c = 0; c < 32; c += 16) {
+      uint32_t w[8], old[8] = {};
+      if (p.accumulate) {
+#pragma unroll
+        for (int k = 0; k < 8; k += 4) {
+          const uint4 x = *reinterpret_cast<const uint4*>(dst + c + 2 * k);
+          old[k] = x.x, old[k + 1] = x.y, old[k + 2] = x.z, old[k + 3] = x.w;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        w[k] = pack_bf16x2(fmaf(__uint_as_float(r[c + 2 * k]), f, bf16_lo(old[k])),
+                           fmaf(__uint_as_float(r[c + 2 * k + 1]), f, bf16_hi(old[k])));
+      if (p.wide) {
+        st_global_v8(dst + c, w);
+      } else {
+        *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+    }
+  }
+}
+
+template <bool FP32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    k_logprob_grads(const __grid_constant__ GradArgs p) {
+  pdl_enter();
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int s_go;
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  GemmCtrl* ctrl = reinterpret_cast<GemmCtrl*>(smem + L::CTRL_OFFSET);
+  const uint32_t tiles = smem_u32(smem);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_ctarank();
+  const PairShare share = share_of(p.deal, static_cast<int>(blockIdx.x >> 1),
+                                   static_cast<int>(gridDim.x >> 1));
+  const int units = share.count();
+
+  // both CTAs of a pair take the same decision
+  if (threadIdx.x == 0) s_go = read_status(p.status) == 0;
+  cluster_sync_all();
+  if (threadIdx.x == 0)
+    s_go = s_go && ld_shared_cluster_u32(mapa_shared(smem_u32(&s_go), rank ^ 1u));
+  cluster_sync_all();
+  if (!s_go) return;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&ctrl->full[s], 1);
+      mbar_init(&ctrl->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&ctrl->tfull[b], 1);
+      mbar_init(&ctrl->tempty[b], 2 * kEpiWarps);
+    }
+    mbar_init(&ctrl->drain, 1);
+    ctrl->abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_map(&p.tmGk);
+    tma_prefetch_map(&p.tmW);
+    tma_prefetch_map(&p.tmGm);
+    tma_prefetch_map(&p.tmHs);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&ctrl->tmem_base, 2 * kBN);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = ctrl->tmem_base;
+  volatile int* abort_flag = &ctrl->abort_flag;
+
+  if (warp == 0) {
+    // ------------------------------------------------ producer (both CTAs)
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0, issued = 0, issued_ph = 0;
+      bool ok = true;
+      const uint64_t keep = l2_evict_last();  // B: W or Hs, re-read by every row tile
+      for (int i = 0; ok && i < units; ++i) {
+        const GradUnit g = grad_unit(p, share.unit(i));
+        const int m0 = g.mt * 2 * BM + static_cast<int>(rank) * BM;
+        const int n0 = g.nt * kBN + static_cast<int>(rank) * (kBN / 2);
+        const CUtensorMap* mb = g.dw ? &p.tmHs : &p.tmW;
+        for (int kb = g.kb0; kb < g.kb1; ++kb) {
+          if (!mbar_wait(&ctrl->empty[s], ph ^ 1u, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb_local = smem_u32(&ctrl->full[s]);
+          if (rank == 0) mbar_arrive_expect_tx(&ctrl->full[s], 2 * L::STAGE_BYTES);
+          const uint32_t fb = rank == 0 ? fb_local : mapa_shared(fb_local, 0);
+          const uint32_t a_dst = tiles + s * L::STAGE_BYTES;
+          const uint32_t b_dst = a_dst + L::A_BYTES;
+          if (g.dw) {
+            tma_load_2d_pair(a_dst, &p.tmGm, fb, m0, kb * BK);
+            tma_load_2d_pair(a_dst + 8192, &p.tmGm, fb, m0 + 64, kb * BK);
+          } else {
+            tma_load_2d_pair(a_dst, &p.tmGk, fb, kb * BK, m0);
+          }
+          tma_load_2d_pair_hint(b_dst, mb, fb, n0, kb * BK, keep);
+          tma_load_2d_pair_hint(b_dst + 8192, mb, fb, n0 + 64, kb * BK, keep);
+          issued |= 1u << s;
+          issued_ph = (issued_ph & ~(1u << s)) | (ph << s);
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (rank == 0) {
+        for (int i = 0; i < kStages; ++i)
+          if ((issued >> i) & 1u) mbar_drain(&ctrl->full[i], (issued_ph >> i) & 1u, p.status);
+      } else if (!ok) {
+        // aborted: the peer cannot observe the leader's barriers; its copies in
+        // flight get a bounded moment to land before shared memory goes
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 200000ull) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMA issuer (leader)
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc_dw = idesc_bf16_f32(2 * BM, kBN, true, true);
+      constexpr uint32_t idesc_dh = idesc_bf16_f32(2 * BM, kBN, false, true);
+      int s = 0, b = 0;
+      uint32_t ph = 0, aph = 0;
+      bool ok = true;
+      for (int i = 0; ok && i < units; ++i) {
+        const GradUnit g = grad_unit(p, share.unit(i));
+        if (!mbar_wait(&ctrl->tempty[b], aph ^ 1u, abort_flag, p.status)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(b * kBN);
+        for (int kb = g.kb0; kb < g.kb1; ++kb) {
+          if (!mbar_wait(&ctrl->full[s], ph, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_addr = tiles + s * L::STAGE_BYTES;
+          const uint32_t b_addr = a_addr + L::A_BYTES;
+#pragma unroll
+          for (int k = 0; k < BK / UMMA_K; ++k) {
+            const uint64_t ad = g.dw ? sdesc_sw128(a_addr + k * 2048, 8192, 1024)
+                                     : sdesc_sw128(a_addr + k * 32, 16, 1024);
+            mma_bf16_pair(d_tmem, ad, sdesc_sw128(b_addr + k * 2048, 8192, 1024),
+                          g.dw ? idesc_dw : idesc_dh, (kb > g.kb0 || k > 0) ? 1u : 0u);
+          }
+          mma_commit_pair(&ctrl->empty[s], 0x3);
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+        mma_commit_pair(&ctrl->tfull[b], 0x3);
+        if (++b == 2) {
+          b = 0;
+          aph ^= 1u;
+        }
+      }
+      mma_commit_pair(&ctrl->drain, 0x1);
+      mbar_drain(&ctrl->drain, 0, p.status);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------ epilogue (both CTAs)
+    const int q = warp & 3;         // TMEM lane quarter this warp may access
+    const int cg = (warp - 2) / 4;  // its half of the tile's columns
+    const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + cg * (kBN / 2);
+    const float scale = p.scale ? __ldg(p.scale) : 1.f;
+    int b = 0;
+    uint32_t aph = 0;
+    for (int i = 0; i < units; ++i) {
+      const bool ok = mbar_wait(&ctrl->tfull[b], aph, abort_flag, p.status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const GradUnit g = grad_unit(p, share.unit(i));
+      const int row = g.mt * 2 * BM + static_cast<int>(rank) * BM + q * 32 + lane;
+      const bool valid = row < (g.dw ? p.V : p.T);
+      const int n0 = g.nt * kBN + cg * (kBN / 2);
+      const int chunks = valid ? min(4, (p.D - n0 + 31) / 32) : 0;  // D is a multiple of 64
+      const size_t at = static_cast<size_t>(valid ? row : 0) * p.D + n0;
+      const uint32_t acc = lane_addr + static_cast<uint32_t>(b * kBN);
+      auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          const uint32_t te = smem_u32(&ctrl->tempty[b]);
+          if (rank == 0) mbar_arrive(&ctrl->tempty[b]);
+          else mbar_arrive_cluster(mapa_shared(te, 0));
+        }
+      };
+      if (g.dw) {
+        for_tmem_chunks<4>(acc, 0, [&](const uint32_t(&r)[32], int c) {
+          if (c < chunks) store_dw<FP32>(p, at + c * 32, r, scale);
+        }, release);
+      } else if (p.slices > 1) {
+        float* dst = p.part + static_cast<size_t>(g.slice) * p.T * p.D + at;
+        for_tmem_chunks<4>(acc, 0, [&](const uint32_t(&r)[32], int c) {
+          if (c >= chunks) return;
+#pragma unroll
+          for (int k = 0; k < 32; k += 8) {
+            const uint32_t w[8] = {r[k],     r[k + 1], r[k + 2], r[k + 3],
+                                   r[k + 4], r[k + 5], r[k + 6], r[k + 7]};
+            st_global_v8(dst + c * 32 + k, w);
+          }
+        }, release);
+      } else {
+        const float f = valid && p.rowfac ? __ldg(p.rowfac + row) : 1.f;
+        for_tmem_chunks<4>(acc, 0, [&](const uint32_t(&r)[32], int c) {
+          if (c >= chunks) return;
+          uint4* dst = reinterpret_cast<uint4*>(p.dH + at + c * 32);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = pack_bf16x2(__uint_as_float(r[8 * k + 2 * e]) * f,
+                                 __uint_as_float(r[8 * k + 2 * e + 1]) * f);
+            dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }, release);
+      }
+      if (++b == 2) {
+        b = 0;
+        aph ^= 1u;
+      }
+    }
+  }
+  __syncthreads();
+  cluster_sync_all();  // the leader's MMAs are drained before either CTA frees TMEM
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 2 * kBN);
+  }
+}
+
+// dH = rowfac times the slices' sums, in their order; eight columns a thread.
+__global__ void __launch_bounds__(256) k_join_dh(const float* __restrict__ part, int slices,
+                                                 int64_t n8, int D8,
+                                                 const float* __restrict__ rowfac,
+                                                 uint16_t* __restrict__ dH, int* status) {
+  pdl_enter();
+  if (read_status(status) != 0) return;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= n8) return;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+#pragma unroll 8
+  for (int s = 0; s < slices; ++s) {
+    const float4* src = reinterpret_cast<const float4*>(part) + (s * n8 + i) * 2;
+    const float4 x = __ldcs(src), y = __ldcs(src + 1);
+    a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+    b.x += y.x, b.y += y.y, b.z += y.z, b.w += y.w;
+  }
+  const float f = rowfac ? __ldg(rowfac + i / D8) : 1.f;
+  reinterpret_cast<uint4*>(dH)[i] =
+      make_uint4(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f),
+                 pack_bf16x2(b.x * f, b.y * f), pack_bf16x2(b.z * f, b.w * f));
+}
+
+// The slices of dH's K. A slice is at most half of what a pair has to do in all, so
+// that the deal can even it out, and at least kLeastKb k-blocks; a tile of dW counts
+// as kLeastDw k-blocks at least, the time of its outputs.
+constexpr int kLeastKb = 8, kLeastDw = 4;
+constexpr int kMostSlices = 32, kMostSliceUnits = 160;
+
+int dh_slices(int64_t T, int64_t V, int64_t D, int pairs) {
+  const int64_t n_nt = cdiv(D, kBN), dh = cdiv(T, 2 * BM) * n_nt, dw = cdiv(V, 2 * BM) * n_nt;
+  const int64_t kb = cdiv(V, BK);
+  const int64_t each = (dh * kb + dw * std::max<int64_t>(cdiv(T, BK), kLeastDw)) / pairs;
+  const int64_t most = std::min({int64_t(kMostSlices), kMostSliceUnits / dh, kb / kLeastKb});
+  return static_cast<int>(
+      std::max<int64_t>(1, std::min(most, cdiv(2 * kb, std::max<int64_t>(each, 1)))));
+}
+
+}  // namespace
+
+size_t logprob_part_bytes(int64_t T, int64_t D) {
+  return static_cast<size_t>(std::min<int64_t>(4 * kMostSlices * T * D,
+                                               4 * int64_t(kMostSliceUnits) * 2 * BM * kBN));
+}
+
+cudaError_t launch_logprob_grads(const LogprobArgs& p, const uint16_t* G, int64_t ldG,
+                                 const uint16_t* Hs, const float* rowfac, const float* scale,
+                                 float* part, uint16_t* dH, void* dW, int dw_fp32, int accumulate,
+                                 cudaStream_t s) {
+  GradArgs a = {};
+  if (!map_kmajor(&a.tmGk, G, p.T, p.V, ldG) || !map_mnmajor(&a.tmW, p.W, p.V, p.D, p.D) ||
+      !map_mnmajor(&a.tmGm, G, p.T, p.V, ldG) || !map_mnmajor(&a.tmHs, Hs, p.T, p.D, p.D))
+    return cudaErrorInvalidValue;
+  const int most = p.num_sms / 2;
+  a.n_nt = tiles_of(p.D, kBN);
+  a.m_dh = tiles_of(p.T, 2 * BM);
+  a.n_dw = tiles_of(p.V, 2 * BM) * a.n_nt;
+  a.slices = dh_slices(p.T, p.V, p.D, most);
+  a.kb_dw = tiles_of(p.T, BK);
+  a.kb_dh = tiles_of(p.V, BK);
+  const int n_dh = a.m_dh * a.n_nt * a.slices;
+  a.deal = deal_units(a.n_dw, a.kb_dw, n_dh, cdiv(a.kb_dh, a.slices));
+  a.T = p.T, a.V = p.V, a.D = p.D;
+  a.dH = dH, a.part = part, a.rowfac = rowfac;
+  a.dW = dW, a.scale = scale, a.accumulate = accumulate;
+  a.wide = reinterpret_cast<uintptr_t>(dW) % 32 == 0;
+  a.status = p.status;
+  const int pairs = std::min(a.n_dw + n_dh, most);
+  const dim3 grid(static_cast<unsigned>(2 * pairs)), block(kThreads);
+  cudaError_t e = dw_fp32 ? launch_pdl(k_logprob_grads<true>, grid, block, L::TOTAL, s, a)
+                          : launch_pdl(k_logprob_grads<false>, grid, block, L::TOTAL, s, a);
+  if (e != cudaSuccess || a.slices == 1) return e;
+  const int64_t n8 = static_cast<int64_t>(p.T) * p.D / 8;
+  return launch_pdl(k_join_dh, dim3(static_cast<unsigned>((n8 + 255) / 256)), dim3(256), 0, s,
+                    static_cast<const float*>(part), a.slices, n8, p.D / 8, rowfac, dH, p.status);
+}
+
+}  // namespace ss

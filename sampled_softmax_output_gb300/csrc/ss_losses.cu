@@ -3,6 +3,7 @@
 // teacher's top values. Each is one kernel that writes the loss and its gradient.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "ss_logprob.cuh"
 
@@ -90,7 +91,7 @@ __global__ void __launch_bounds__(256) k_policy_loss(const PolicyArgs p) {
 struct PreferenceArgs {
   const float *logp, *ref_logp, *weight;
   const int32_t* offsets;
-  int pairs, n, kind, average;
+  int pairs, n, kind, average, cluster, vec;
   float beta, smoothing, scale;
   float *loss, *reward, *dlogp;
   int* status;
@@ -98,50 +99,136 @@ struct PreferenceArgs {
 
 constexpr int kPrefThreads = 512;
 
-__device__ __forceinline__ double warp_sum(double v) {
+// A number as two floats, hi + lo: 48 bits.
+struct Pair {
+  float hi, lo;
+};
+
+// a + b
+__device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
+  const float s = a.hi + b.hi, v = s - a.hi;
+  const float e = (a.hi - (s - v)) + (b.hi - v);  // what s lost
+  // (an infinity loses nothing, and the differences above are no numbers then)
+  return Pair{s, fabsf(s) < INFINITY ? e + (a.lo + b.lo) : 0.f};
+}
+template <int LANES>
+__device__ __forceinline__ Pair pair_join(Pair v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 1; o < LANES; o <<= 1)
+    v = pair_add(v, Pair{__shfl_xor_sync(0xffffffffu, v.hi, o),
+                         __shfl_xor_sync(0xffffffffu, v.lo, o)});
   return v;
 }
 
-// One block per pair: the two sequences' sums, the loss, then the gradient of
-// each of their tokens.
+// fn(i, n) for the elements i .. i + n - 1 (n = 4 at a multiple of 4, else 1) of this
+// thread's share of [begin, end): `threads` threads, of which it is the me-th.
+template <class F>
+__device__ __forceinline__ void for_quads(int64_t begin, int64_t end, bool vec, int me,
+                                          int threads, F&& fn) {
+  if (!vec) {
+    for (int64_t i = begin + me; i < end; i += threads) fn(i, std::integral_constant<int, 1>{});
+    return;
+  }
+  const int64_t head = min((begin + 3) / 4 * 4, end), tail = max(end / 4 * 4, head);
+  if (me < head - begin) fn(begin + me, std::integral_constant<int, 1>{});
+  if (me < end - tail) fn(tail + me, std::integral_constant<int, 1>{});
+  for (int64_t i = head + 4 * static_cast<int64_t>(me); i < tail;
+       i += 4 * static_cast<int64_t>(threads))
+    fn(i, std::integral_constant<int, 4>{});
+}
+
+template <int N>
+struct Quad {
+  float v[N];
+};
+template <int N>
+__device__ __forceinline__ Quad<N> load_quad(const float* p, int64_t i, float none) {
+  Quad<N> q;
+  if constexpr (N == 4) {
+    float4 x = make_float4(none, none, none, none);
+    if (p) x = *reinterpret_cast<const float4*>(p + i);
+    q.v[0] = x.x, q.v[1] = x.y, q.v[2] = x.z, q.v[3] = x.w;
+  } else {
+    q.v[0] = p ? p[i] : none;
+  }
+  return q;
+}
+template <int N>
+__device__ __forceinline__ void store_quad(float* p, int64_t i, const Quad<N>& q) {
+  if constexpr (N == 4)
+    *reinterpret_cast<float4*>(p + i) = make_float4(q.v[0], q.v[1], q.v[2], q.v[3]);
+  else
+    p[i] = q.v[0];
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  return __uint_as_float(ld_shared_cluster_u32(addr));
+}
+
+// A cluster of CTAs per pair: each sums its share of both sequences, the CTAs' sums
+// meet in distributed shared memory in the order of their ranks, each CTA makes the
+// loss of them and writes the gradient of its share (the weights are read again, from
+// L2). 64 pairs of 32768 tokens on average, with reference and weights: a block alone
+// per pair took 281 us.
 __global__ void __launch_bounds__(kPrefThreads) k_preference_loss(const PreferenceArgs p) {
-  __shared__ double s_part[kPrefThreads / 32][4];
+  __shared__ Pair s_warp[kPrefThreads / 32][4];  // sums and weights of both sequences
+  __shared__ Pair s_cta[4];
   __shared__ float s_slope[2];
   pdl_enter();
-  if (p.status && read_status(p.status) != 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  for (int pair = blockIdx.x; pair < p.pairs; pair += gridDim.x) {
-    const int o0 = p.offsets[2 * pair], o1 = p.offsets[2 * pair + 1], o2 = p.offsets[2 * pair + 2];
-    if (o0 < 0 || o1 < o0 || o2 < o1 || o2 > p.n) {  // the same for the whole block
-      if (threadIdx.x == 0) {
+  const int rank = static_cast<int>(cluster_ctarank()), size = p.cluster;
+  const int me = rank * kPrefThreads + static_cast<int>(threadIdx.x);
+  const int threads = size * kPrefThreads;
+  const int clusters = static_cast<int>(gridDim.x) / size;
+  for (int pair = static_cast<int>(blockIdx.x) / size; pair < p.pairs; pair += clusters) {
+    const int o[3] = {p.offsets[2 * pair], p.offsets[2 * pair + 1], p.offsets[2 * pair + 2]};
+    if (o[0] < 0 || o[1] < o[0] || o[2] < o[1] || o[2] > p.n) {  // the same for all CTAs
+      if (threadIdx.x == 0 && rank == 0) {
         set_status(p.status, SS_ERR_INDEX);
         p.loss[pair] = p.reward[2 * pair] = p.reward[2 * pair + 1] = NAN;
       }
       continue;
     }
-    double sum[2] = {0., 0.}, mass[2] = {0., 0.};
-    for (int64_t i = static_cast<int64_t>(o0) + threadIdx.x; i < o2; i += kPrefThreads) {
-      const float m = p.weight ? p.weight[i] : 1.f;
-      if (m == 0.f) continue;
-      const float x = m * (p.logp[i] - (p.ref_logp ? p.ref_logp[i] : 0.f));
-      const bool second = i >= o1;
-      sum[0] += second ? 0.f : x;
-      sum[1] += second ? x : 0.f;
-      mass[0] += second ? 0.f : m;
-      mass[1] += second ? m : 0.f;
-    }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const double a = warp_sum(sum[k]), b = warp_sum(mass[k]);
-      if (lane == 0) s_part[warp][k] = a, s_part[warp][2 + k] = b;
+      Pair sum{0.f, 0.f}, mass{0.f, 0.f};
+      for_quads(o[k], o[k + 1], p.vec, me, threads, [&](int64_t i, auto count) {
+        constexpr int N = decltype(count)::value;
+        const Quad<N> m = load_quad<N>(p.weight, i, 1.f), l = load_quad<N>(p.logp, i, 0.f),
+                      r = load_quad<N>(p.ref_logp, i, 0.f);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const float x = m.v[j] != 0.f ? m.v[j] * (l.v[j] - r.v[j]) : 0.f;
+          sum = pair_add(sum, Pair{x, 0.f});
+          mass = pair_add(mass, Pair{m.v[j], 0.f});
+        }
+      });
+      sum = pair_join<32>(sum);
+      mass = pair_join<32>(mass);
+      if (lane == 0) s_warp[warp][k] = sum, s_warp[warp][2 + k] = mass;
     }
     __syncthreads();
+    if (threadIdx.x < 4) {
+      Pair t = s_warp[0][threadIdx.x];
+      for (int w = 1; w < kPrefThreads / 32; ++w) t = pair_add(t, s_warp[w][threadIdx.x]);
+      s_cta[threadIdx.x] = t;
+    }
+    __syncthreads();
+    if (size > 1) cluster_sync_all();
     if (threadIdx.x == 0) {
-      double t[4] = {0., 0., 0., 0.};
-      for (int w = 0; w < kPrefThreads / 32; ++w)
-        for (int k = 0; k < 4; ++k) t[k] += s_part[w][k];
+      double t[4];
+      for (int k = 0; k < 4; ++k) {
+        Pair all{0.f, 0.f};
+        for (int r = 0; r < size; ++r) {
+          Pair v = s_cta[k];
+          if (size > 1) {
+            const uint32_t at = mapa_shared(smem_u32(&s_cta[k]), r);
+            v = Pair{ld_cluster_f32(at), ld_cluster_f32(at + 4)};
+          }
+          all = pair_add(all, v);
+        }
+        t[k] = static_cast<double>(all.hi) + static_cast<double>(all.lo);
+      }
       double per[2] = {1., 1.};
       if (p.average)
         for (int k = 0; k < 2; ++k) per[k] = t[2 + k] != 0. ? 1. / t[2 + k] : 0.;
@@ -162,24 +249,36 @@ __global__ void __launch_bounds__(kPrefThreads) k_preference_loss(const Preferen
         loss = static_cast<float>(d * d);
         slope = static_cast<float>(2. * d);
       }
-      p.loss[pair] = loss;
-      p.reward[2 * pair] = static_cast<float>(p.beta * r0);
-      p.reward[2 * pair + 1] = static_cast<float>(p.beta * r1);
+      if (rank == 0) {
+        p.loss[pair] = loss;
+        p.reward[2 * pair] = static_cast<float>(p.beta * r0);
+        p.reward[2 * pair + 1] = static_cast<float>(p.beta * r1);
+      }
       s_slope[0] = static_cast<float>(p.scale * (slope * per[0]));
       s_slope[1] = static_cast<float>(-p.scale * (slope * per[1]));
     }
     __syncthreads();
-    const float c0 = s_slope[0], c1 = s_slope[1];
-    for (int64_t i = static_cast<int64_t>(o0) + threadIdx.x; i < o2; i += kPrefThreads) {
-      const float m = p.weight ? p.weight[i] : 1.f;
-      p.dlogp[i] = m == 0.f ? 0.f : m * (i >= o1 ? c1 : c0);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float c = s_slope[k];
+      for_quads(o[k], o[k + 1], p.vec, me, threads, [&](int64_t i, auto count) {
+        constexpr int N = decltype(count)::value;
+        Quad<N> m = load_quad<N>(p.weight, i, 1.f);
+#pragma unroll
+        for (int j = 0; j < N; ++j) m.v[j] = m.v[j] != 0.f ? m.v[j] * c : 0.f;
+        store_quad<N>(p.dlogp, i, m);
+      });
     }
-    __syncthreads();
+    // the peers have read this CTA's sums before the next pair's replace them (or the
+    // CTA exits); shared memory is reused by this CTA's own threads too
+    if (size > 1) cluster_sync_all();
+    else __syncthreads();
   }
   // what lies outside every sequence
-  const int begin = p.pairs > 0 ? min(max(p.offsets[0], 0), p.n) : p.n;
-  const int end = p.pairs > 0 ? min(max(p.offsets[2 * p.pairs], begin), p.n) : p.n;
-  const int64_t outside = static_cast<int64_t>(begin) + (p.n - end);
+  const int64_t begin = p.pairs > 0 ? min(max(p.offsets[0], 0), p.n) : p.n;
+  const int64_t end = p.pairs > 0 ? min(max(p.offsets[2 * p.pairs], static_cast<int>(begin)), p.n)
+                                  : p.n;
+  const int64_t outside = begin + (p.n - end);
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPrefThreads + threadIdx.x; i < outside;
        i += static_cast<int64_t>(gridDim.x) * kPrefThreads)
     p.dlogp[i < begin ? i : i - begin + end] = 0.f;
@@ -201,17 +300,7 @@ constexpr float kTailFloor = 1.f / 4096.f;
 
 // What the top ids leave of 1 can be a thousandth, and a rounding of fp32 in their
 // sum is then a ten-thousandth of it: with a tail, the exponentials and their sums
-// are pairs of floats, value hi + lo.
-struct Pair {
-  float hi, lo;
-};
-
-// a + b
-__device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
-  const float s = a.hi + b.hi, v = s - a.hi;
-  const float e = (a.hi - (s - v)) + (b.hi - v);  // what s lost
-  return Pair{s, e + (a.lo + b.lo)};
-}
+// are pairs of floats.
 
 // exp(x) for x <= 0: x = n log 2 + r, |r| <= log(2) / 2, with log 2 in two parts (the
 // first has 16 bits, so that n times it is exact) and what the subtraction of the
@@ -290,10 +379,7 @@ __global__ void __launch_bounds__(256) k_distill_loss(const DistillArgs p) {
       return v;
     };
     auto rest_of_1 = [](Pair v) {
-#pragma unroll
-      for (int o = 1; o < LANES; o <<= 1)
-        v = pair_add(v, Pair{__shfl_xor_sync(0xffffffffu, v.hi, o),
-                             __shfl_xor_sync(0xffffffffu, v.lo, o)});
+      v = pair_join<LANES>(v);
       return (1.f - v.hi) - v.lo;
     };
     float pr[4], extra = 0.f, ratio = 0.f, loss = 0.f;
@@ -427,15 +513,38 @@ ss_status ss_preference_loss(const float* logp, const float* ref_logp, const flo
   if (workspace_bytes < kHeaderBytes) return SS_ERR_WORKSPACE;
   const int nsm = current_num_sms();
   if (nsm <= 0) return record_failure("cudaGetDevice/cudaDeviceGetAttribute", cudaGetLastError());
-  const PreferenceArgs p{logp,      ref_logp, weight,          offsets,
-                         static_cast<int>(pairs), static_cast<int>(n), kind, average,
-                         beta,      smoothing, scale,          loss,
-                         reward,    dlogp,    static_cast<int*>(workspace)};
-  const int64_t want = std::max<int64_t>(pairs, (n + 8 * kPrefThreads - 1) / (8 * kPrefThreads));
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(std::max<int64_t>(want, 1), nsm * 4)));
+  PreferenceArgs p{};
+  p.logp = logp, p.ref_logp = ref_logp, p.weight = weight, p.offsets = offsets;
+  p.pairs = static_cast<int>(pairs), p.n = static_cast<int>(n);
+  p.kind = kind, p.average = average;
+  p.beta = beta, p.smoothing = smoothing, p.scale = scale;
+  p.loss = loss, p.reward = reward, p.dlogp = dlogp;
+  p.status = static_cast<int*>(workspace);
+  p.vec = aligned(logp, 16) && aligned(ref_logp, 16) && aligned(weight, 16) && aligned(dlogp, 16);
+  // a CTA per 4096 tokens of a pair of average length, up to the largest portable
+  // cluster; pairs beyond the resident clusters take turns
+  const int64_t each = n / std::max<int64_t>(pairs, 1);
+  while (p.cluster < 8 && each > 4096 * int64_t(p.cluster)) p.cluster = std::max(1, 2 * p.cluster);
+  p.cluster = std::max(1, p.cluster);
+  const int64_t ctas = std::min<int64_t>(std::max<int64_t>(pairs, 1) * p.cluster, int64_t(nsm) * 4);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   StageTrace trace(s, "preference_loss");
-  const cudaError_t e = launch_pdl(k_preference_loss, grid, dim3(kPrefThreads), 0, s, p);
+  cudaError_t e = prepare_kernel(k_preference_loss, 0);
+  if (e == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas / p.cluster * p.cluster));
+    cfg.blockDim = dim3(kPrefThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {static_cast<unsigned>(p.cluster), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, k_preference_loss, p);
+    if (e == cudaSuccess) ++g_kernel_launches;
+  }
   return e == cudaSuccess ? SS_OK : record_failure("launch k_preference_loss", e);
 }
 
