@@ -30,7 +30,10 @@ LogprobLayout logprob_layout(int64_t T, int64_t V, int64_t D, bool backward) {
   L.ldG = (V + 63) / 64 * 64;
   L.n_parts = static_cast<int>(2 * ((V + kBnLogits - 1) / kBnLogits));
   L.part = L.coef = kHeaderBytes;
-  L.sorted = L.part + up1024(static_cast<size_t>(L.n_parts) * T * sizeof(float2));
+  // (a few tokens have partials of another number, kMostFewParts at most)
+  const size_t parts = std::max<size_t>(static_cast<size_t>(L.n_parts) * T,
+                                        kMostFewParts * std::min<int64_t>(T, kFewTokens));
+  L.sorted = L.part + up1024(parts * sizeof(float2));
   L.bin_ends = L.sorted + up1024(static_cast<size_t>(T) * SS_MAX_IDS * sizeof(uint32_t));
   const size_t forward =
       L.bin_ends + up1024(static_cast<size_t>((T + 31) / 32) * L.n_parts * sizeof(uint16_t));
@@ -369,12 +372,16 @@ ss_status ss_logprob_forward(const uint16_t* H, const uint16_t* W, const int32_t
   cudaError_t e;
   uint32_t* sorted = reinterpret_cast<uint32_t*>(ws + L.sorted);
   uint16_t* bin_ends = reinterpret_cast<uint16_t*>(ws + L.bin_ends);
-  {
-    StageTrace trace(s, "bin_ids");
-    e = launch_bin_ids(p, ids, iK, L.n_parts, sorted, bin_ends, s);
-  }
-  if (e != cudaSuccess) return record_failure("launch k_bin_ids", e);
-  {
+  const int few = logprob_few_parts(T, V, D, p.num_sms);
+  if (few) {
+    StageTrace trace(s, "gemm_forward_lse");
+    e = launch_logprob_few(p, iK, ids, few, part, logp, s);
+  } else {
+    {
+      StageTrace trace(s, "bin_ids");
+      e = launch_bin_ids(p, ids, iK, L.n_parts, sorted, bin_ends, s);
+    }
+    if (e != cudaSuccess) return record_failure("launch k_bin_ids", e);
     StageTrace trace(s, "gemm_forward_lse");
     e = launch_logprob_partials(p, iK, sorted, bin_ends, part, logp, s);
   }
@@ -382,7 +389,7 @@ ss_status ss_logprob_forward(const uint16_t* H, const uint16_t* W, const int32_t
   {
     StageTrace trace(s, "logprob_merge");
     e = launch_pdl(k_logprob_merge, dim3(static_cast<unsigned>((T + 31) / 32)),
-                   dim3(32 * kMergeWarps), 0, s, part, L.n_parts, p.T, iK, ids, logp, lse,
+                   dim3(32 * kMergeWarps), 0, s, part, few ? few : L.n_parts, p.T, iK, ids, logp, lse,
                    p.status);
   }
   return e == cudaSuccess ? SS_OK : record_failure("launch k_logprob_merge", e);

@@ -220,6 +220,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t ph = 0, issued = 0, issued_ph = 0;
       bool ok = true;
       // W is re-read by every row tile, H by every column tile: both stay in L2
+      const bool again = p.m_tiles > 1;
       const uint64_t keep = l2_evict_last();
       for (int u = pair; ok && u < num_units; u += npairs) {
         int mt, nt;
@@ -236,7 +237,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t fb = rank == 0 ? fb_local : mapa_shared(fb_local, 0);
           const uint32_t dst = tiles + s * L::STAGE_BYTES;
           tma_load_2d_pair(dst, &tmH, fb, kb * BK, m0);
-          tma_load_2d_pair_hint(dst + L::A_BYTES, &tmW, fb, kb * BK, n0, keep);
+          if (again) tma_load_2d_pair_hint(dst + L::A_BYTES, &tmW, fb, kb * BK, n0, keep);
+          else tma_load_2d_pair(dst + L::A_BYTES, &tmW, fb, kb * BK, n0);
           issued |= 1u << s;
           issued_ph = (issued_ph & ~(1u << s)) | (ph << s);
           if (++s == kStages) {
@@ -415,11 +417,166 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
+// --------------------------------------------------------------- few tokens
+//
+// One token or two (a served model's next position): W is read once, at memory's rate,
+// and the products run on the fp32 pipe beside it, where a tile of 256 tokens on the
+// tensor cores would be mostly empty (V 50304, D 768, one token: 18.7 us with the merge,
+// 77 MB, where the tiles take 35; four tokens: 29 and 31, D 2048 64 and 58). A warp
+// takes kRows vocabulary rows at a time, each lane eight columns of every 256; the
+// tokens lie in shared memory. The ids' logits are more rows of the same kind, so that
+// the sums are the same ones.
+constexpr int kFewThreads = 256, kRows = 4;
+
+struct FewArgs {
+  const uint16_t *H, *W;
+  const int32_t* ids;
+  int T, V, D, K;
+  float cap, tau;
+  float2* part;  // [gridDim.x][T]
+  float* z;      // [T, K]
+  int* status;
+};
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// acc[r][t] = W[row[r]] . H[t], in every lane
+template <int N, int R>
+__device__ __forceinline__ void rows_dot(const FewArgs& p, const uint4* h, const uint4* (&row)[R],
+                                         int lane, float (&acc)[R][N]) {
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < N; ++t) acc[r][t] = 0.f;
+  const int d8 = p.D / 8;
+#pragma unroll 3
+  for (int c = lane; c < d8; c += 32) {
+    uint4 w[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) w[r] = __ldcs(row[r] + c);
+    float x[R][8];
+#pragma unroll
+    for (int r = 0; r < R; ++r) unpack8(w[r], x[r]);
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+      float y[8];
+      unpack8(h[t * d8 + c], y);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[r][t] = fmaf(x[r][i], y[i], acc[r][t]);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int t = 0; t < N; ++t) acc[r][t] += __shfl_xor_sync(0xffffffffu, acc[r][t], o);
+}
+
+// (m, s) and the logit z
+__device__ __forceinline__ void take_logit(float z, float& m, float& s) {
+  const float top = fmaxf(m, z);
+  // (the first logit: exp(-inf) = 0; a NaN stays in the sum)
+  s = top > -INFINITY ? s * expf(m - top) + expf(z - top) : s + z;
+  m = top;
+}
+__device__ __forceinline__ void take_partial(float om, float os, float& m, float& s) {
+  if (om == -INFINITY) return;
+  const float top = fmaxf(m, om);
+  s = s * expf(m - top) + os * expf(om - top);
+  m = top;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kFewThreads) k_logprob_few(const FewArgs p) {
+  pdl_enter();
+  extern __shared__ uint4 s_h[];
+  __shared__ float2 s_part[kFewThreads / 32][N];
+  __shared__ int s_go;
+  if (threadIdx.x == 0) s_go = read_status(p.status) == 0;
+  const int d8 = p.D / 8;
+  for (int i = threadIdx.x; i < N * d8; i += kFewThreads)
+    s_h[i] = i < p.T * d8 ? __ldg(reinterpret_cast<const uint4*>(p.H) + i)
+                          : make_uint4(0u, 0u, 0u, 0u);
+  __syncthreads();
+  if (!s_go) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int w = static_cast<int>(blockIdx.x) * (kFewThreads / 32) + warp;
+  const int warps = static_cast<int>(gridDim.x) * (kFewThreads / 32);
+  const uint4* W = reinterpret_cast<const uint4*>(p.W);
+  auto capped = [&](float z) { return p.cap > 0.f ? p.cap / (1.f + expf(-z / p.tau)) : z; };
+  // the chosen ids, one at a time
+  for (int64_t i = w; i < static_cast<int64_t>(p.T) * p.K; i += warps) {
+    const int id = __ldg(p.ids + i);
+    if (id < 0 || id >= p.V) {
+      if (lane == 0 && id != -1) set_status(p.status, SS_ERR_TARGET_RANGE);
+      continue;
+    }
+    const uint4* row[1] = {W + static_cast<int64_t>(id) * d8};
+    float acc[1][1];
+    rows_dot<1, 1>(p, s_h + (i / p.K) * d8, row, lane, acc);
+    if (lane == 0) p.z[i] = capped(acc[0][0]);
+  }
+  // lane t keeps token t's running pair
+  float m = -INFINITY, s = 0.f;
+  for (int v0 = w * kRows; v0 < p.V; v0 += warps * kRows) {
+    const uint4* row[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+      row[r] = W + static_cast<int64_t>(min(v0 + r, p.V - 1)) * d8;
+    float acc[kRows][N];
+    rows_dot<N, kRows>(p, s_h, row, lane, acc);
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      float z = acc[r][0];
+#pragma unroll
+      for (int t = 1; t < N; ++t)
+        if (lane == t) z = acc[r][t];
+      if (lane < N && v0 + r < p.V) take_logit(capped(z), m, s);
+    }
+  }
+  if (lane < N) s_part[warp][lane] = make_float2(m, s);
+  __syncthreads();
+  if (threadIdx.x < p.T) {
+    for (int k = 1; k < kFewThreads / 32; ++k)
+      take_partial(s_part[k][threadIdx.x].x, s_part[k][threadIdx.x].y, m, s);
+    p.part[static_cast<int64_t>(blockIdx.x) * p.T + threadIdx.x] = make_float2(m, s);
+  }
+}
+
+template <int N>
+cudaError_t few(const FewArgs& p, int blocks, cudaStream_t s) {
+  return launch_pdl(k_logprob_few<N>, dim3(static_cast<unsigned>(blocks)), dim3(kFewThreads),
+                    static_cast<size_t>(N) * p.D * 2, s, p);
+}
+
 // Units walk groups of this many rows column tile by column tile, so that W is
 // read from memory once per group.
 constexpr int kGroupRows = 8192;
 
 }  // namespace
+
+int logprob_few_parts(int64_t T, int64_t V, int64_t D, int num_sms) {
+  if (T > kFewTokens) return 0;
+  const int64_t want = (V + kRows * kFewThreads / 32 - 1) / (kRows * kFewThreads / 32);
+  return static_cast<int>(std::min<int64_t>({want, int64_t(num_sms) * 3, kMostFewParts}));
+}
+
+cudaError_t launch_logprob_few(const LogprobArgs& p, int K, const int32_t* ids, int parts,
+                               float2* part, float* z, cudaStream_t s) {
+  const FewArgs a{p.H, p.W, ids, p.T, p.V, p.D, K, p.cap, p.tau, part, z, p.status};
+  static_assert(kFewTokens == 2 && 2 * SS_MAX_D * 2 <= 64 * 1024, "tokens in shared memory");
+  return p.T <= 1 ? few<1>(a, parts, s) : few<2>(a, parts, s);
+}
 
 cudaError_t launch_bin_ids(const LogprobArgs& p, const int32_t* ids, int K, int bins,
                            uint32_t* sorted, uint16_t* bin_ends, cudaStream_t s) {

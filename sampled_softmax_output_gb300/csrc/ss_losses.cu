@@ -14,6 +14,33 @@ namespace {
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 bool usable(const void* p, uintptr_t a) { return p != nullptr && aligned(p, a); }
 
+constexpr int64_t kMostBlocks = (int64_t(1) << 31) - 1;  // what lies beyond is walked
+
+// N consecutive elements; p null: `none` each
+template <int N>
+struct Quad {
+  float v[N];
+};
+template <int N>
+__device__ __forceinline__ Quad<N> load_quad(const float* p, int64_t i, float none) {
+  Quad<N> q;
+  if constexpr (N == 4) {
+    float4 x = make_float4(none, none, none, none);
+    if (p) x = *reinterpret_cast<const float4*>(p + i);
+    q.v[0] = x.x, q.v[1] = x.y, q.v[2] = x.z, q.v[3] = x.w;
+  } else {
+    q.v[0] = p ? p[i] : none;
+  }
+  return q;
+}
+template <int N>
+__device__ __forceinline__ void store_quad(float* p, int64_t i, const Quad<N>& q) {
+  if constexpr (N == 4)
+    *reinterpret_cast<float4*>(p + i) = make_float4(q.v[0], q.v[1], q.v[2], q.v[3]);
+  else
+    p[i] = q.v[0];
+}
+
 // ------------------------------------------------------------ policy loss
 
 struct PolicyArgs {
@@ -51,36 +78,53 @@ __device__ __forceinline__ PolicyOut policy_token(const PolicyArgs& p, float log
 }
 
 // Memory-bound: 20 bytes read and 12 written a token (with a reference and
-// weights). VEC tokens a thread, 16 bytes an access where the pointers allow.
-template <int VEC>
+// weights). Q groups of four tokens a thread, 16 bytes an access where the pointers
+// allow; else (Q = 0) a token a thread.
+template <int Q>
 __global__ void __launch_bounds__(256) k_policy_loss(const PolicyArgs p) {
   pdl_enter();
-  const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
   const bool has_ref = p.ref_logp != nullptr;
-  for (int64_t g = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; g * VEC < p.n; g += step) {
-    const int64_t i = g * VEC;
-    if (VEC == 4 && i + 4 <= p.n) {
-      const float4 z = make_float4(0.f, 0.f, 0.f, 0.f), u = make_float4(1.f, 1.f, 1.f, 1.f);
-      const float4 x = *reinterpret_cast<const float4*>(p.logp + i);
-      const float4 b = *reinterpret_cast<const float4*>(p.old_logp + i);
-      const float4 A = *reinterpret_cast<const float4*>(p.advantage + i);
-      const float4 r = has_ref ? *reinterpret_cast<const float4*>(p.ref_logp + i) : z;
-      const float4 m = p.weight ? *reinterpret_cast<const float4*>(p.weight + i) : u;
-      const PolicyOut o0 = policy_token(p, x.x, b.x, A.x, r.x, m.x, has_ref);
-      const PolicyOut o1 = policy_token(p, x.y, b.y, A.y, r.y, m.y, has_ref);
-      const PolicyOut o2 = policy_token(p, x.z, b.z, A.z, r.z, m.z, has_ref);
-      const PolicyOut o3 = policy_token(p, x.w, b.w, A.w, r.w, m.w, has_ref);
-      *reinterpret_cast<float4*>(p.loss + i) = make_float4(o0.loss, o1.loss, o2.loss, o3.loss);
-      *reinterpret_cast<float4*>(p.dlogp + i) = make_float4(o0.dlogp, o1.dlogp, o2.dlogp, o3.dlogp);
-      if (p.kl) *reinterpret_cast<float4*>(p.kl + i) = make_float4(o0.kl, o1.kl, o2.kl, o3.kl);
-    } else {
-      for (int64_t j = i; j < std::min<int64_t>(i + VEC, p.n); ++j) {
-        const PolicyOut o =
-            policy_token(p, p.logp[j], p.old_logp[j], p.advantage[j],
-                         has_ref ? p.ref_logp[j] : 0.f, p.weight ? p.weight[j] : 1.f, has_ref);
-        p.loss[j] = o.loss;
-        p.dlogp[j] = o.dlogp;
-        if (p.kl) p.kl[j] = o.kl;
+  auto one = [&](int64_t j) {
+    const PolicyOut o =
+        policy_token(p, p.logp[j], p.old_logp[j], p.advantage[j], has_ref ? p.ref_logp[j] : 0.f,
+                     p.weight ? p.weight[j] : 1.f, has_ref);
+    p.loss[j] = o.loss;
+    p.dlogp[j] = o.dlogp;
+    if (p.kl) p.kl[j] = o.kl;
+  };
+  const int64_t blocks = gridDim.x;
+  if constexpr (Q == 0) {
+    for (int64_t j = blockIdx.x * int64_t(256) + threadIdx.x; j < p.n; j += blocks * 256) one(j);
+  } else {
+    // a block takes Q * 256 groups in a row
+    const int64_t groups = p.n / 4;
+    if (blockIdx.x == 0 && threadIdx.x < (p.n & 3)) one(groups * 4 + threadIdx.x);
+    for (int64_t g0 = blockIdx.x * int64_t(256 * Q); g0 < groups; g0 += blocks * 256 * Q) {
+      Quad<4> x[Q], b[Q], A[Q], r[Q], m[Q];
+#pragma unroll
+      for (int u = 0; u < Q; ++u) {
+        const int64_t g = g0 + u * 256 + threadIdx.x;
+        if (g >= groups) continue;
+        x[u] = load_quad<4>(p.logp, g * 4, 0.f);
+        b[u] = load_quad<4>(p.old_logp, g * 4, 0.f);
+        A[u] = load_quad<4>(p.advantage, g * 4, 0.f);
+        r[u] = load_quad<4>(p.ref_logp, g * 4, 0.f);
+        m[u] = load_quad<4>(p.weight, g * 4, 1.f);
+      }
+#pragma unroll
+      for (int u = 0; u < Q; ++u) {
+        const int64_t g = g0 + u * 256 + threadIdx.x;
+        if (g >= groups) continue;
+        Quad<4> loss, kl, d;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const PolicyOut o = policy_token(p, x[u].v[j], b[u].v[j], A[u].v[j], r[u].v[j],
+                                           m[u].v[j], has_ref);
+          loss.v[j] = o.loss, kl.v[j] = o.kl, d.v[j] = o.dlogp;
+        }
+        store_quad<4>(p.loss, g * 4, loss);
+        store_quad<4>(p.dlogp, g * 4, d);
+        if (p.kl) store_quad<4>(p.kl, g * 4, kl);
       }
     }
   }
@@ -97,7 +141,8 @@ struct PreferenceArgs {
   int* status;
 };
 
-constexpr int kPrefThreads = 512;
+constexpr int kPrefThreads = 256;
+constexpr int kPrefMostCluster = 8;
 
 // A number as two floats, hi + lo: 48 bits.
 struct Pair {
@@ -120,45 +165,30 @@ __device__ __forceinline__ Pair pair_join(Pair v) {
   return v;
 }
 
-// fn(i, n) for the elements i .. i + n - 1 (n = 4 at a multiple of 4, else 1) of this
-// thread's share of [begin, end): `threads` threads, of which it is the me-th.
+// This thread's share of [begin, end), `threads` threads of which it is the me-th, as
+// fn(i, step, n, u): u groups of n elements at i, i + step, ...; n is 4 at multiples of
+// 4, else 1. Two groups at a time, so that their loads are in flight together.
 template <class F>
-__device__ __forceinline__ void for_quads(int64_t begin, int64_t end, bool vec, int me,
-                                          int threads, F&& fn) {
-  if (!vec) {
-    for (int64_t i = begin + me; i < end; i += threads) fn(i, std::integral_constant<int, 1>{});
-    return;
-  }
-  const int64_t head = min((begin + 3) / 4 * 4, end), tail = max(end / 4 * 4, head);
-  if (me < head - begin) fn(begin + me, std::integral_constant<int, 1>{});
-  if (me < end - tail) fn(tail + me, std::integral_constant<int, 1>{});
-  for (int64_t i = head + 4 * static_cast<int64_t>(me); i < tail;
-       i += 4 * static_cast<int64_t>(threads))
-    fn(i, std::integral_constant<int, 4>{});
+__device__ __forceinline__ void for_groups(int64_t begin, int64_t end, bool vec, int me,
+                                           int threads, F&& fn) {
+  constexpr std::integral_constant<int, 1> one{};
+  constexpr std::integral_constant<int, 2> two{};
+  constexpr std::integral_constant<int, 4> four{};
+  const int64_t head = vec ? min((begin + 3) / 4 * 4, end) : end;
+  const int64_t tail = vec ? max(end / 4 * 4, head) : end;
+  for (int64_t i = begin + me; i < head; i += threads) fn(i, int64_t(0), one, one);
+  if (me < end - tail) fn(tail + me, int64_t(0), one, one);
+  const int64_t step = 4 * static_cast<int64_t>(threads);
+  int64_t i = head + 4 * static_cast<int64_t>(me);
+  for (; i + step < tail; i += 2 * step) fn(i, step, four, two);
+  for (; i < tail; i += step) fn(i, step, four, one);
 }
 
-template <int N>
-struct Quad {
-  float v[N];
-};
-template <int N>
-__device__ __forceinline__ Quad<N> load_quad(const float* p, int64_t i, float none) {
-  Quad<N> q;
-  if constexpr (N == 4) {
-    float4 x = make_float4(none, none, none, none);
-    if (p) x = *reinterpret_cast<const float4*>(p + i);
-    q.v[0] = x.x, q.v[1] = x.y, q.v[2] = x.z, q.v[3] = x.w;
-  } else {
-    q.v[0] = p ? p[i] : none;
-  }
-  return q;
-}
-template <int N>
-__device__ __forceinline__ void store_quad(float* p, int64_t i, const Quad<N>& q) {
-  if constexpr (N == 4)
-    *reinterpret_cast<float4*>(p + i) = make_float4(q.v[0], q.v[1], q.v[2], q.v[3]);
-  else
-    p[i] = q.v[0];
+// a / b for b not 0
+__device__ __forceinline__ Pair pair_over(Pair a, Pair b) {
+  const float q = a.hi / b.hi;
+  const float left = (fmaf(-q, b.hi, a.hi) + a.lo) - q * b.lo;
+  return Pair{q, left / b.hi};
 }
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
@@ -166,11 +196,14 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
 }
 
 // A cluster of CTAs per pair: each sums its share of both sequences, the CTAs' sums
-// meet in distributed shared memory in the order of their ranks, each CTA makes the
-// loss of them and writes the gradient of its share (the weights are read again, from
-// L2). 64 pairs of 32768 tokens on average, with reference and weights: a block alone
-// per pair took 281 us.
-__global__ void __launch_bounds__(kPrefThreads) k_preference_loss(const PreferenceArgs p) {
+// meet in distributed shared memory and are joined in the order of their ranks, each
+// CTA makes the loss of them and writes the gradient of its share (the weights are read
+// again, from L2). What bounds it is the chain of latencies of the longest pair: 64
+// pairs of 2^21 tokens of random lengths take 14.6 us (33 MB, 5 us at the copy rate),
+// one of 64 tokens 6.3. A single block of 512 threads per pair took 281 us, clusters of
+// 512 threads a CTA, which are not all resident at once, 20.6.
+__global__ void __launch_bounds__(kPrefThreads, 6) k_preference_loss(const PreferenceArgs p) {
+  static_assert(kPrefThreads >= 128 && 4 * kPrefMostCluster <= 32, "a warp for each sum");
   __shared__ Pair s_warp[kPrefThreads / 32][4];  // sums and weights of both sequences
   __shared__ Pair s_cta[4];
   __shared__ float s_slope[2];
@@ -192,81 +225,100 @@ __global__ void __launch_bounds__(kPrefThreads) k_preference_loss(const Preferen
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       Pair sum{0.f, 0.f}, mass{0.f, 0.f};
-      for_quads(o[k], o[k + 1], p.vec, me, threads, [&](int64_t i, auto count) {
-        constexpr int N = decltype(count)::value;
-        const Quad<N> m = load_quad<N>(p.weight, i, 1.f), l = load_quad<N>(p.logp, i, 0.f),
-                      r = load_quad<N>(p.ref_logp, i, 0.f);
+      for_groups(o[k], o[k + 1], p.vec, me, threads,
+                 [&](int64_t i, int64_t step, auto count, auto groups) {
+        constexpr int N = decltype(count)::value, U = decltype(groups)::value;
+        Quad<N> m[U], l[U], r[U];
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const float x = m.v[j] != 0.f ? m.v[j] * (l.v[j] - r.v[j]) : 0.f;
-          sum = pair_add(sum, Pair{x, 0.f});
-          mass = pair_add(mass, Pair{m.v[j], 0.f});
+        for (int u = 0; u < U; ++u) {
+          m[u] = load_quad<N>(p.weight, i + u * step, 1.f);
+          l[u] = load_quad<N>(p.logp, i + u * step, 0.f);
+          r[u] = load_quad<N>(p.ref_logp, i + u * step, 0.f);
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            const float w = m[u].v[j];
+            sum = pair_add(sum, Pair{w != 0.f ? w * (l[u].v[j] - r[u].v[j]) : 0.f, 0.f});
+            if (p.average) mass = pair_add(mass, Pair{w, 0.f});
+          }
       });
       sum = pair_join<32>(sum);
       mass = pair_join<32>(mass);
       if (lane == 0) s_warp[warp][k] = sum, s_warp[warp][2 + k] = mass;
     }
     __syncthreads();
-    if (threadIdx.x < 4) {
-      Pair t = s_warp[0][threadIdx.x];
-      for (int w = 1; w < kPrefThreads / 32; ++w) t = pair_add(t, s_warp[w][threadIdx.x]);
-      s_cta[threadIdx.x] = t;
+    if (warp < 4) {  // warp k joins the k-th of the four
+      constexpr int kWarps = kPrefThreads / 32;
+      Pair t = lane < kWarps ? s_warp[lane][warp] : Pair{0.f, 0.f};
+      t = pair_join<kWarps>(t);
+      if (lane == 0) s_cta[warp] = t;
     }
     __syncthreads();
     if (size > 1) cluster_sync_all();
-    if (threadIdx.x == 0) {
-      double t[4];
-      for (int k = 0; k < 4; ++k) {
-        Pair all{0.f, 0.f};
-        for (int r = 0; r < size; ++r) {
-          Pair v = s_cta[k];
-          if (size > 1) {
-            const uint32_t at = mapa_shared(smem_u32(&s_cta[k]), r);
-            v = Pair{ld_cluster_f32(at), ld_cluster_f32(at + 4)};
-          }
-          all = pair_add(all, v);
+    if (warp == 0) {
+      // lane k + 4 r holds the k-th of rank r; joined over the ranks
+      Pair t{0.f, 0.f};
+      if (lane < 4 * size) {
+        t = s_cta[lane & 3];
+        if (size > 1) {
+          const uint32_t at = mapa_shared(smem_u32(&s_cta[lane & 3]), lane >> 2);
+          t = Pair{ld_cluster_f32(at), ld_cluster_f32(at + 4)};
         }
-        t[k] = static_cast<double>(all.hi) + static_cast<double>(all.lo);
       }
-      double per[2] = {1., 1.};
-      if (p.average)
-        for (int k = 0; k < 2; ++k) per[k] = t[2 + k] != 0. ? 1. / t[2 + k] : 0.;
-      const double r0 = t[0] * per[0], r1 = t[1] * per[1], x = r0 - r1;
-      const double h = p.beta * x;
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1)
+        t = pair_add(t, Pair{__shfl_xor_sync(0xffffffffu, t.hi, o),
+                             __shfl_xor_sync(0xffffffffu, t.lo, o)});
+      const Pair mass{__shfl_sync(0xffffffffu, t.hi, (lane & 1) + 2),
+                      __shfl_sync(0xffffffffu, t.lo, (lane & 1) + 2)};
+      if (p.average) t = mass.hi != 0.f ? pair_over(t, mass) : Pair{0.f, 0.f};
+      const float per = !p.average ? 1.f : mass.hi != 0.f ? 1.f / (mass.hi + mass.lo) : 0.f;
+      // lanes 0 and 1: R of the two sequences; the difference in both
+      const Pair other{__shfl_xor_sync(0xffffffffu, t.hi, 1), __shfl_xor_sync(0xffffffffu, t.lo, 1)};
+      const float sign = (lane & 1) ? -1.f : 1.f;
+      const Pair x = pair_add(Pair{sign * t.hi, sign * t.lo}, Pair{-sign * other.hi, -sign * other.lo});
+      const float h = p.beta * (x.hi + x.lo);
       float loss, slope;  // slope: d loss / d x
       if (p.kind == SS_PREF_SIGMOID) {
         // log s(h) = min(h, 0) - log(1 + exp(-|h|))
-        const float hf = static_cast<float>(h), e = expf(-fabsf(hf)), l = log1pf(e);
-        loss = (1.f - p.smoothing) * (fmaxf(-hf, 0.f) + l) + p.smoothing * (fmaxf(hf, 0.f) + l);
-        const float s_neg = hf >= 0.f ? e / (1.f + e) : 1.f / (1.f + e);  // s(-h)
+        const float e = expf(-fabsf(h)), l = log1pf(e);
+        loss = (1.f - p.smoothing) * (fmaxf(-h, 0.f) + l) + p.smoothing * (fmaxf(h, 0.f) + l);
+        const float s_neg = h >= 0.f ? e / (1.f + e) : 1.f / (1.f + e);  // s(-h)
         slope = p.beta * (p.smoothing - s_neg);
       } else if (p.kind == SS_PREF_HINGE) {
-        loss = static_cast<float>(fmax(0., 1. - h));
-        slope = h < 1. ? -p.beta : 0.f;
+        loss = fmaxf(0.f, 1.f - h);
+        slope = h < 1.f ? -p.beta : 0.f;
+        if (isnan(h)) loss = h;
       } else {
-        const double d = x - 0.5 / p.beta;
-        loss = static_cast<float>(d * d);
-        slope = static_cast<float>(2. * d);
+        const Pair d = pair_add(x, Pair{-0.5f / p.beta, 0.f});
+        const float df = d.hi + d.lo;
+        loss = df * df;
+        slope = 2.f * df;
       }
-      if (rank == 0) {
-        p.loss[pair] = loss;
-        p.reward[2 * pair] = static_cast<float>(p.beta * r0);
-        p.reward[2 * pair + 1] = static_cast<float>(p.beta * r1);
+      if (lane < 2) {
+        s_slope[lane] = sign * p.scale * (slope * per);
+        if (rank == 0) p.reward[2 * pair + lane] = p.beta * (t.hi + t.lo);
       }
-      s_slope[0] = static_cast<float>(p.scale * (slope * per[0]));
-      s_slope[1] = static_cast<float>(-p.scale * (slope * per[1]));
+      if (lane == 0 && rank == 0) p.loss[pair] = loss;
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const float c = s_slope[k];
-      for_quads(o[k], o[k + 1], p.vec, me, threads, [&](int64_t i, auto count) {
-        constexpr int N = decltype(count)::value;
-        Quad<N> m = load_quad<N>(p.weight, i, 1.f);
+      for_groups(o[k], o[k + 1], p.vec, me, threads,
+                 [&](int64_t i, int64_t step, auto count, auto groups) {
+        constexpr int N = decltype(count)::value, U = decltype(groups)::value;
+        Quad<N> m[U];
 #pragma unroll
-        for (int j = 0; j < N; ++j) m.v[j] = m.v[j] != 0.f ? m.v[j] * c : 0.f;
-        store_quad<N>(p.dlogp, i, m);
+        for (int u = 0; u < U; ++u) m[u] = load_quad<N>(p.weight, i + u * step, 1.f);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+          for (int j = 0; j < N; ++j) m[u].v[j] = m[u].v[j] != 0.f ? m[u].v[j] * c : 0.f;
+          store_quad<N>(p.dlogp, i + u * step, m[u]);
+        }
       });
     }
     // the peers have read this CTA's sums before the next pair's replace them (or the
@@ -297,53 +349,72 @@ struct DistillArgs {
 };
 
 constexpr float kTailFloor = 1.f / 4096.f;
+// a teacher's log-probability up to here is a probability of 0 (the least normal
+// number is exp(-87.3))
+constexpr float kLeastLog = -87.f;
 
 // What the top ids leave of 1 can be a thousandth, and a rounding of fp32 in their
-// sum is then a ten-thousandth of it: with a tail, the exponentials and their sums
-// are pairs of floats.
+// sum is then a ten-thousandth of it: with a tail, the exponentials come with their
+// roundings and are summed in two parts.
 
-// exp(x) for x <= 0: x = n log 2 + r, |r| <= log(2) / 2, with log 2 in two parts (the
-// first has 16 bits, so that n times it is exact) and what the subtraction of the
-// second rounds off kept in r_lo; exp(r) = 1 + r + r^2 / 2 + r^3 P(r), what the
-// first three terms' sum and the square lose kept too, P the series up to r^8 / 8!,
-// whose rest is 2e-10.
-__device__ __forceinline__ Pair exp_pair(float x) {
-  constexpr float c1 = 0x1.62e4p-1f, c2 = 0x1.7f7d1cp-20f;
-  x = fmaxf(x, -100.f);
-  const float n = rintf(x * 1.4426950408889634f);
-  const float t = fmaf(-n, c1, x);
-  const float r = fmaf(-n, c2, t), r_lo = fmaf(-n, c2, t - r);
-  float q = 1.f / 40320.f;
-  q = fmaf(q, r, 1.f / 5040.f);
-  q = fmaf(q, r, 1.f / 720.f);
-  q = fmaf(q, r, 1.f / 120.f);
-  q = fmaf(q, r, 1.f / 24.f);
-  q = fmaf(q, r, 1.f / 6.f);
-  const float h = 0.5f * r, sq = h * r, sq_lo = fmaf(h, r, -sq);  // r^2 / 2
-  const float one = 1.f + r, one_lo = r - (one - 1.f);
-  const float hi = one + sq, hi_lo = sq - (hi - one);
-  const float lo = (one_lo + hi_lo) + fmaf(sq * (2.f * r), q, fmaf(one, r_lo, sq_lo));
-  // 2^n, 0 below the normal numbers
-  const float scale = n >= -126.f ? __int_as_float((127 + static_cast<int>(n)) << 23) : 0.f;
-  return Pair{hi * scale, lo * scale};
+// exp(x) for two x <= 0: x = n log 2 + r, |r| <= log(2) / 2, with log 2 in two parts
+// (the first has 16 bits, so that n times it is exact) and what the subtraction of the
+// second rounds off kept in r_lo; exp(r) = 1 + r + r^2 / 2 + r^3 P(r), what the first
+// three terms' sum and the square lose kept too, P the series up to r^8 / 8!, whose
+// rest is 2e-10. `top` is a multiple of 2^-23, so that sums of it up to 2 are exact in
+// fp32; `rest` is what it leaves, below 2^-23.
+struct Exp2 {
+  float v[2], top[2], rest[2];
+};
+__device__ __forceinline__ Exp2 exp_pairs(float x0, float x1) {
+  const auto both = [](float c) { return f32x2(c, c); };
+  const uint64_t x = f32x2(x0 < -87.f ? -87.f : x0, x1 < -87.f ? -87.f : x1);  // (a NaN stays)
+  // n by rounding to an integer at 2^23 + 2^22; its low bits then hold it
+  const uint64_t magic = both(12582912.f), none = both(-1.f);
+  const uint64_t m = fma_f32x2(x, both(1.4426950408889634f), magic);
+  const uint64_t n = add_f32x2(m, both(-12582912.f));
+  const uint64_t t = fma_f32x2(n, both(-0x1.62e4p-1f), x);
+  const uint64_t r = fma_f32x2(n, both(-0x1.7f7d1cp-20f), t);
+  const uint64_t r_lo = fma_f32x2(n, both(-0x1.7f7d1cp-20f), fma_f32x2(r, none, t));
+  uint64_t q = fma_f32x2(r, both(1.f / 40320.f), both(1.f / 5040.f));
+  q = fma_f32x2(q, r, both(1.f / 720.f));
+  q = fma_f32x2(q, r, both(1.f / 120.f));
+  q = fma_f32x2(q, r, both(1.f / 24.f));
+  q = fma_f32x2(q, r, both(1.f / 6.f));
+  const uint64_t h = mul_f32x2(r, both(0.5f)), sq = mul_f32x2(h, r);  // r^2 / 2
+  const uint64_t sq_lo = fma_f32x2(h, r, mul_f32x2(sq, none));
+  const uint64_t one = add_f32x2(r, both(1.f));
+  const uint64_t one_lo = fma_f32x2(add_f32x2(one, both(-1.f)), none, r);
+  const uint64_t hi = add_f32x2(one, sq);
+  const uint64_t hi_lo = fma_f32x2(fma_f32x2(one, none, hi), none, sq);
+  uint64_t lo = fma_f32x2(one, r_lo, sq_lo);
+  lo = fma_f32x2(mul_f32x2(sq, add_f32x2(r, r)), q, lo);
+  lo = add_f32x2(lo, add_f32x2(one_lo, hi_lo));
+  float m0, m1, h0, h1, l0, l1;
+  f32x2_split(m, m0, m1);
+  // 2^n, n in [-126, 0]
+  const uint64_t scale = f32x2(__int_as_float((__float_as_int(m0) << 23) + 0x3f800000),
+                               __int_as_float((__float_as_int(m1) << 23) + 0x3f800000));
+  f32x2_split(mul_f32x2(hi, scale), h0, h1);
+  f32x2_split(mul_f32x2(lo, scale), l0, l1);
+  Exp2 e;
+  e.v[0] = h0 + l0, e.v[1] = h1 + l1;
+  e.top[0] = (h0 + 1.f) - 1.f, e.top[1] = (h1 + 1.f) - 1.f;
+  e.rest[0] = (h0 - e.top[0]) + l0, e.rest[1] = (h1 - e.top[1]) + l1;
+  return e;
 }
 
-// A token's K entries over LANES lanes, four each.
-template <int LANES, bool BF16, bool VEC>
-__global__ void __launch_bounds__(256) k_distill_loss(const DistillArgs p) {
-  pdl_enter();
-  const int64_t lanes = static_cast<int64_t>(p.T) * LANES;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
-  // the same trip count for every lane of a warp
-  for (int64_t g0 = static_cast<int64_t>(blockIdx.x) * 256; g0 < lanes; g0 += step) {
-    const int64_t g = g0 + threadIdx.x;
-    const bool valid = g < lanes;
-    const int64_t t = valid ? g / LANES : 0;
-    const int k0 = static_cast<int>(g % LANES) * 4;
+// Four entries of a token, those that are not there absent.
+template <bool BF16, bool VEC>
+struct Entries {
+  float l[4], x[4], m;
+  unsigned on;  // bit i: entry i is there
+  __device__ __forceinline__ void load(const DistillArgs& p, int64_t t, int k0) {
+    const bool valid = t < p.T;
     const int64_t at = t * p.K + k0;
     const int nk = valid ? min(max(p.K - k0, 0), 4) : 0;
-    float l[4], x[4];
-    bool here[4];
+    m = valid ? (p.weight ? p.weight[t] : 1.f) : 0.f;
+    on = 0u;
     if (VEC && nk == 4) {
       const float4 a = *reinterpret_cast<const float4*>(p.logp + at);
       l[0] = a.x, l[1] = a.y, l[2] = a.z, l[3] = a.w;
@@ -356,86 +427,115 @@ __global__ void __launch_bounds__(256) k_distill_loss(const DistillArgs p) {
         const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(p.teacher) + at);
         x[0] = b.x, x[1] = b.y, x[2] = b.z, x[3] = b.w;
       }
-      int4 id = make_int4(0, 0, 0, 0);
-      if (p.ids) id = *reinterpret_cast<const int4*>(p.ids + at);
-      here[0] = id.x >= 0, here[1] = id.y >= 0, here[2] = id.z >= 0, here[3] = id.w >= 0;
+      on = 15u;
+      if (p.ids) {
+        const int4 id = *reinterpret_cast<const int4*>(p.ids + at);
+        on = (id.x >= 0 ? 1u : 0u) | (id.y >= 0 ? 2u : 0u) | (id.z >= 0 ? 4u : 0u) |
+             (id.w >= 0 ? 8u : 0u);
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        here[i] = i < nk && (!p.ids || p.ids[at + i] >= 0);
-        l[i] = i < nk ? p.logp[at + i] : 0.f;
-        x[i] = 0.f;
-        if (i < nk)
-          x[i] = BF16 ? __uint_as_float(
-                            static_cast<uint32_t>(static_cast<const uint16_t*>(p.teacher)[at + i])
-                            << 16)
-                      : static_cast<const float*>(p.teacher)[at + i];
+        l[i] = x[i] = 0.f;
+        if (i >= nk) continue;
+        on |= !p.ids || p.ids[at + i] >= 0 ? 1u << i : 0u;
+        l[i] = p.logp[at + i];
+        x[i] = BF16 ? __uint_as_float(
+                          static_cast<uint32_t>(static_cast<const uint16_t*>(p.teacher)[at + i])
+                          << 16)
+                    : static_cast<const float*>(p.teacher)[at + i];
       }
     }
-    const float m = valid ? (p.weight ? p.weight[t] : 1.f) : 0.f;
+  }
+};
+
+// A token's K entries over LANES lanes, four a lane. The instructions bound it, not the
+// 14 bytes an entry: 65536 tokens of K 128 in 29 us, 40 with a tail (3.4 of 4 possible
+// instructions a cycle, most of them the exponentials'), where a copy of as many bytes
+// takes 17. Two or four times as many entries a lane, which halve the steps of each
+// sum over lanes, take registers that cost more (36 and 39 us without a tail); the
+// next token's entries loaded ahead took 45 us with a tail.
+template <int LANES, bool BF16, bool VEC>
+__global__ void __launch_bounds__(256, 5) k_distill_loss(const DistillArgs p) {
+  pdl_enter();
+  const int64_t lanes = (static_cast<int64_t>(p.T) * LANES + 255) / 256 * 256;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int k0 = static_cast<int>(first % LANES) * 4;
+  // the same trip count for every lane of a block
+  for (int64_t g = first; g < lanes; g += step) {
+    const int64_t t = g / LANES;
+    Entries<BF16, VEC> now;
+    now.load(p, t, k0);
+    float (&l)[4] = now.l, (&x)[4] = now.x;
+    const float m = now.m;
+    const bool here[4] = {(now.on & 1u) != 0u, (now.on & 2u) != 0u, (now.on & 4u) != 0u,
+                          (now.on & 8u) != 0u};
     auto join = [](float v) {
 #pragma unroll
       for (int o = 1; o < LANES; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
       return v;
     };
-    auto rest_of_1 = [](Pair v) {
-      v = pair_join<LANES>(v);
-      return (1.f - v.hi) - v.lo;
-    };
-    float pr[4], extra = 0.f, ratio = 0.f, loss = 0.f;
-    float any = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) any = here[i] ? 1.f : any;
-#pragma unroll
-    for (int o = 1; o < LANES; o <<= 1) any = fmaxf(any, __shfl_xor_sync(0xffffffffu, any, o));
-    const bool used = m != 0.f && any != 0.f;
+    float extra = 0.f, loss = 0.f;
+    const unsigned mine = (0xffffffffu >> (32 - LANES)) << (threadIdx.x & 31 & ~(LANES - 1));
+    const bool used = (__ballot_sync(0xffffffffu, now.on != 0u) & mine) != 0u && m != 0.f;
+    // l becomes the slope
     if (p.tail) {
-      Pair sp{0.f, 0.f}, sq{0.f, 0.f};
-      float q[4];
+      float sp[2] = {0.f, 0.f}, sq[2] = {0.f, 0.f}, q[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const Pair a = here[i] ? exp_pair(x[i]) : Pair{0.f, 0.f};
-        const Pair b = here[i] ? exp_pair(l[i]) : Pair{0.f, 0.f};
-        pr[i] = a.hi + a.lo;
-        q[i] = b.hi + b.lo;
-        sp = pair_add(sp, a);
-        sq = pair_add(sq, b);
-        if (pr[i] > 0.f) loss += pr[i] * (x[i] - l[i]);
+      for (int i = 0; i < 4; i += 2) {
+        const Exp2 a = exp_pairs(x[i], x[i + 1]), b = exp_pairs(l[i], l[i + 1]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const bool on = here[i + j], known = on && !(x[i + j] <= kLeastLog);
+          const float pr = known ? a.v[j] : 0.f;
+          q[i + j] = on ? b.v[j] : 0.f;
+          sp[0] += known ? a.top[j] : 0.f, sp[1] += known ? a.rest[j] : 0.f;
+          sq[0] += on ? b.top[j] : 0.f, sq[1] += on ? b.rest[j] : 0.f;
+          if (known) loss += pr * (x[i + j] - l[i + j]);
+          x[i + j] = pr;
+        }
       }
-      const float p1 = fmaxf(rest_of_1(sp), 0.f);
-      const float rest = rest_of_1(sq), q1 = fmaxf(rest, kTailFloor);
+      loss = join(loss);
+      const float p1 = fmaxf((1.f - join(sp[0])) - join(sp[1]), 0.f);
+      const float rest = (1.f - join(sq[0])) - join(sq[1]), q1 = fmaxf(rest, kTailFloor);
       if (p1 > 0.f) extra = p1 * (logf(p1) - logf(q1));
-      ratio = rest > kTailFloor ? p1 / q1 : 0.f;
+      const float ratio = rest > kTailFloor ? p1 / q1 : 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) l[i] = fmaf(ratio, q[i], -pr[i]);  // the slope
+      for (int i = 0; i < 4; ++i) l[i] = fmaf(ratio, q[i], -x[i]);
     } else {
       float top = -INFINITY;
 #pragma unroll
       for (int i = 0; i < 4; ++i) top = here[i] ? fmaxf(top, x[i]) : top;
 #pragma unroll
       for (int o = 1; o < LANES; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      float sp = 0.f;
+      // sum of exp(x - top); and, with log p = x - top - log(sum), of exp(x - top)
+      // times (x - top - l), from which the loss is made
+      float sum = 0.f, part = 0.f, pr[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        pr[i] = here[i] && top > -INFINITY ? expf(x[i] - top) : 0.f;
-        sp += pr[i];
+        const float d = x[i] - top;
+        pr[i] = here[i] && top > -INFINITY ? expf(d) : 0.f;
+        sum += pr[i];
+        if (pr[i] > 0.f) part += pr[i] * (d - l[i]);
       }
-      sp = join(sp);
-      const float per = sp > 0.f ? 1.f / sp : 0.f, ls = top + logf(sp);
+      sum = join(sum);
+      part = join(part);
+      const float per = sum > 0.f ? 1.f / sum : 0.f;
+      loss = part * per;
+      if (sum > 0.f) extra = -logf(sum);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        pr[i] *= per;
-        if (pr[i] > 0.f) loss += pr[i] * ((x[i] - ls) - l[i]);
-        l[i] = -pr[i];
-      }
+      for (int i = 0; i < 4; ++i) l[i] = -per * pr[i];
     }
-    loss = join(loss) + extra;
-    if (!valid) continue;
+    loss += extra;
+    if (t >= p.T) continue;
+    const int64_t at = t * p.K + k0;
+    const int nk = min(max(p.K - k0, 0), 4);
     if (k0 == 0) p.loss[t] = used ? m * loss : 0.f;
-    const float c = p.scale * m;
+    const float scale = p.scale * m;
     float d[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) d[i] = used && here[i] ? c * l[i] : 0.f;
+    for (int i = 0; i < 4; ++i) d[i] = used && here[i] ? scale * l[i] : 0.f;
     if (VEC && nk == 4) {
       *reinterpret_cast<float4*>(p.dlogp + at) = make_float4(d[0], d[1], d[2], d[3]);
     } else {
@@ -447,9 +547,9 @@ __global__ void __launch_bounds__(256) k_distill_loss(const DistillArgs p) {
 }
 
 template <int LANES>
-cudaError_t distill(const DistillArgs& p, bool bf16, bool vec, int num_sms, cudaStream_t s) {
+cudaError_t distill(const DistillArgs& p, bool bf16, bool vec, cudaStream_t s) {
   const int64_t blocks = (static_cast<int64_t>(p.T) * LANES + 255) / 256;
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(blocks, int64_t(num_sms) * 32)));
+  const dim3 grid(static_cast<unsigned>(std::min(blocks, kMostBlocks)));
   if (bf16)
     return vec ? launch_pdl(k_distill_loss<LANES, true, true>, grid, dim3(256), 0, s, p)
                : launch_pdl(k_distill_loss<LANES, true, false>, grid, dim3(256), 0, s, p);
@@ -485,12 +585,13 @@ ss_status ss_policy_loss(const float* logp, const float* old_logp, const float* 
   const bool vec = aligned(logp, 16) && aligned(old_logp, 16) && aligned(advantage, 16) &&
                    aligned(ref_logp, 16) && aligned(weight, 16) && aligned(loss, 16) &&
                    aligned(kl, 16) && aligned(dlogp, 16);
-  const int64_t items = vec ? (n + 3) / 4 : n;
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>((items + 255) / 256, int64_t(nsm) * 32)));
+  constexpr int kQ = 1;
+  const int64_t each = vec ? 256 * 4 * kQ : 256;
+  const dim3 grid(static_cast<unsigned>(std::min((n + each - 1) / each, kMostBlocks)));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   StageTrace trace(s, "policy_loss");
-  const cudaError_t e = vec ? launch_pdl(k_policy_loss<4>, grid, dim3(256), 0, s, p)
-                            : launch_pdl(k_policy_loss<1>, grid, dim3(256), 0, s, p);
+  const cudaError_t e = vec ? launch_pdl(k_policy_loss<kQ>, grid, dim3(256), 0, s, p)
+                            : launch_pdl(k_policy_loss<0>, grid, dim3(256), 0, s, p);
   return e == cudaSuccess ? SS_OK : record_failure("launch k_policy_loss", e);
 }
 
@@ -524,7 +625,7 @@ ss_status ss_preference_loss(const float* logp, const float* ref_logp, const flo
   // a CTA per 4096 tokens of a pair of average length, up to the largest portable
   // cluster; pairs beyond the resident clusters take turns
   const int64_t each = n / std::max<int64_t>(pairs, 1);
-  while (p.cluster < 8 && each > 4096 * int64_t(p.cluster)) p.cluster = std::max(1, 2 * p.cluster);
+  while (p.cluster < kPrefMostCluster && each > 4096 * int64_t(p.cluster)) p.cluster = std::max(1, 2 * p.cluster);
   p.cluster = std::max(1, p.cluster);
   const int64_t ctas = std::min<int64_t>(std::max<int64_t>(pairs, 1) * p.cluster, int64_t(nsm) * 4);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -568,12 +669,12 @@ ss_status ss_distill_loss(const float* logp, const void* teacher, int teacher_dt
                    aligned(ids, 16) && aligned(dlogp, 16);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   StageTrace trace(s, "distill_loss");
-  const cudaError_t e = K <= 4    ? distill<1>(p, bf16, vec, nsm, s)
-                        : K <= 8  ? distill<2>(p, bf16, vec, nsm, s)
-                        : K <= 16 ? distill<4>(p, bf16, vec, nsm, s)
-                        : K <= 32 ? distill<8>(p, bf16, vec, nsm, s)
-                        : K <= 64 ? distill<16>(p, bf16, vec, nsm, s)
-                                  : distill<32>(p, bf16, vec, nsm, s);
+  const cudaError_t e = K <= 4    ? distill<1>(p, bf16, vec, s)
+                        : K <= 8  ? distill<2>(p, bf16, vec, s)
+                        : K <= 16 ? distill<4>(p, bf16, vec, s)
+                        : K <= 32 ? distill<8>(p, bf16, vec, s)
+                        : K <= 64 ? distill<16>(p, bf16, vec, s)
+                                  : distill<32>(p, bf16, vec, s);
   return e == cudaSuccess ? SS_OK : record_failure("launch k_distill_loss", e);
 }
 
