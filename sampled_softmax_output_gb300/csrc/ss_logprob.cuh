@@ -25,8 +25,8 @@ struct LogprobArgs {
 cudaError_t launch_bin_ids(const LogprobArgs& p, const int32_t* ids, int K, int bins,
                            uint32_t* sorted, uint16_t* bin_ends, cudaStream_t s);
 // part[c][t]: the largest logit of row t among columns 128 c to 128 c + 127 and the
-// sum of the exponentials above it, c < bins; (-inf, 0) past the end. z [T, K]: the
-// ids' logits (absent ones are left alone).
+// sum of the exponentials above it, c < bins; (-inf, 0) past the end. z: the logits of
+// the sorted ids, place by place.
 cudaError_t launch_logprob_partials(const LogprobArgs& p, int K, const uint32_t* sorted,
                                     const uint16_t* bin_ends, float2* part, float* z,
                                     cudaStream_t s);

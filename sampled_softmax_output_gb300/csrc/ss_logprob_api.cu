@@ -16,15 +16,15 @@ constexpr size_t kHdrScale = 128;  // byte offset in the header: the scale of dW
 size_t up1024(size_t x) { return (x + 1023) / 1024 * 1024; }
 
 struct LogprobLayout {
-  size_t part, sorted, bin_ends, coef, f, rowfac, hs, dh_part, g, total;
+  size_t part, sorted, z, bin_ends, coef, f, rowfac, hs, dh_part, g, total;
   int64_t ldG;
   int n_parts;
 };
 
-// After the header, the forward's softmax partials and sorted ids, or, in the same
-// place, what the backward pass needs: the coefficients, the factors of H's and of
-// dH's rows, the scaled H, partial sums of dH, and G. The scale of dW lies in the
-// header.
+// After the header, the forward's softmax partials and sorted ids with their logits,
+// or, in the same place, what the backward pass needs: the coefficients, the factors of
+// H's and of dH's rows, the scaled H, partial sums of dH, and G. The scale of dW lies
+// in the header.
 LogprobLayout logprob_layout(int64_t T, int64_t V, int64_t D, bool backward) {
   LogprobLayout L;
   L.ldG = (V + 63) / 64 * 64;
@@ -34,7 +34,8 @@ LogprobLayout logprob_layout(int64_t T, int64_t V, int64_t D, bool backward) {
   const size_t parts = std::max<size_t>(static_cast<size_t>(L.n_parts) * T,
                                         kMostFewParts * std::min<int64_t>(T, kFewTokens));
   L.sorted = L.part + up1024(parts * sizeof(float2));
-  L.bin_ends = L.sorted + up1024(static_cast<size_t>(T) * SS_MAX_IDS * sizeof(uint32_t));
+  L.z = L.sorted + up1024(static_cast<size_t>(T) * SS_MAX_IDS * sizeof(uint32_t));
+  L.bin_ends = L.z + up1024(static_cast<size_t>(T) * SS_MAX_IDS * sizeof(float));
   const size_t forward =
       L.bin_ends + up1024(static_cast<size_t>((T + 31) / 32) * L.n_parts * sizeof(uint16_t));
   L.f = L.coef + up1024(static_cast<size_t>(T) * sizeof(float));
@@ -76,8 +77,8 @@ ss_status logprob_head(const ss_head* head, LogprobArgs* p) {
 
 // ------------------------------------------------------------- small kernels
 
-// lse[t] from the (max, sum) partials of n_parts column groups, and logp = z - lse
-// in z's place. A block takes 32 tokens: warp w folds the partials w, w + 32, ...
+// lse[t] from the (max, sum) partials of n_parts column groups, and logp = z - lse: of
+// the sorted ids' logits z, or (sorted null) in the place of z = logp. A block takes 32 tokens: warp w folds the partials w, w + 32, ...
 // of its lane's token, the warps' pairs meet in shared memory.
 constexpr int kMergeWarps = 32;
 
@@ -94,8 +95,10 @@ __device__ __forceinline__ void fold(float& M, float& S, float m, float s) {
 
 __global__ void __launch_bounds__(32 * kMergeWarps)
     k_logprob_merge(const float2* __restrict__ part, int n_parts, int T, int K,
-                    const int32_t* __restrict__ ids, float* __restrict__ logp,
-                    float* __restrict__ lse, int* status) {
+                    const int32_t* __restrict__ ids, const uint32_t* __restrict__ sorted,
+                    const uint16_t* __restrict__ bin_ends, int bins,
+                    const float* __restrict__ z, float* logp, float* __restrict__ lse,
+                    int* status) {
   __shared__ float2 red[kMergeWarps][33];
   __shared__ float s_lse[32];
   __shared__ int s_go;
@@ -139,10 +142,21 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   }
   __syncthreads();
   const int nt = T - t0 < 32 ? static_cast<int>(T - t0) : 32;
-  for (int i = static_cast<int>(threadIdx.x); i < nt * K; i += 32 * kMergeWarps) {
-    const int64_t at = t0 * K + i;
-    logp[at] = __ldg(ids + at) >= 0 ? logp[at] - s_lse[i / K] : 0.f;
+  const int64_t at0 = t0 * K;
+  if (sorted == nullptr) {
+    for (int i = static_cast<int>(threadIdx.x); i < nt * K; i += 32 * kMergeWarps)
+      logp[at0 + i] = __ldg(ids + at0 + i) >= 0 ? logp[at0 + i] - s_lse[i / K] : 0.f;
+    return;
   }
+  const int known = __ldg(bin_ends + (static_cast<int64_t>(blockIdx.x) + 1) * bins - 1);
+  for (int i = static_cast<int>(threadIdx.x); i < known; i += 32 * kMergeWarps) {
+    const uint32_t e = __ldg(sorted + at0 + i);
+    const int row = static_cast<int>((e >> 7) & 31u);
+    logp[at0 + row * K + (e >> 12)] = __ldg(z + at0 + i) - s_lse[row];
+  }
+  if (known < nt * K)
+    for (int i = static_cast<int>(threadIdx.x); i < nt * K; i += 32 * kMergeWarps)
+      if (__ldg(ids + at0 + i) < 0) logp[at0 + i] = 0.f;
 }
 
 // How the backward's two operands are scaled. G's rows are a[t] times probabilities
@@ -372,6 +386,7 @@ ss_status ss_logprob_forward(const uint16_t* H, const uint16_t* W, const int32_t
   cudaError_t e;
   uint32_t* sorted = reinterpret_cast<uint32_t*>(ws + L.sorted);
   uint16_t* bin_ends = reinterpret_cast<uint16_t*>(ws + L.bin_ends);
+  float* z = reinterpret_cast<float*>(ws + L.z);
   const int few = logprob_few_parts(T, V, D, p.num_sms);
   if (few) {
     StageTrace trace(s, "gemm_forward_lse");
@@ -383,14 +398,14 @@ ss_status ss_logprob_forward(const uint16_t* H, const uint16_t* W, const int32_t
     }
     if (e != cudaSuccess) return record_failure("launch k_bin_ids", e);
     StageTrace trace(s, "gemm_forward_lse");
-    e = launch_logprob_partials(p, iK, sorted, bin_ends, part, logp, s);
+    e = launch_logprob_partials(p, iK, sorted, bin_ends, part, z, s);
   }
   if (e != cudaSuccess) return record_failure("launch gemm_forward_lse", e);
   {
     StageTrace trace(s, "logprob_merge");
     e = launch_pdl(k_logprob_merge, dim3(static_cast<unsigned>((T + 31) / 32)),
-                   dim3(32 * kMergeWarps), 0, s, part, few ? few : L.n_parts, p.T, iK, ids, logp, lse,
-                   p.status);
+                   dim3(32 * kMergeWarps), 0, s, part, few ? few : L.n_parts, p.T, iK, ids,
+                   few ? nullptr : sorted, bin_ends, L.n_parts, z, logp, lse, p.status);
   }
   return e == cudaSuccess ? SS_OK : record_failure("launch k_logprob_merge", e);
 }

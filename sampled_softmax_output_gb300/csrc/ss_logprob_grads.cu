@@ -21,9 +21,12 @@ constexpr int kBN = 256;
 constexpr int kStages = 6;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
-using L = Gemm2Smem<kBN, kStages, 0>;
+// a 16 KB buffer for each column group's stores of dW beside the ring
+constexpr int kStageBytes = 2 * 16384;
+using L = Gemm2Smem<kBN, kStages, kStageBytes>;
 
 struct GradArgs {
+  CUtensorMap tmDw;        // dW [V, D] as rows of two-byte words, fp32 too
   CUtensorMap tmGk, tmW;   // dH: G [T, V] by rows, W [V, D]
   CUtensorMap tmGm, tmHs;  // dW: G [T, V] by columns, Hs [T, D]
   UnitDeal deal;           // units 0 .. n_dw - 1: dW's tiles, then dH's tiles by slice
@@ -34,7 +37,7 @@ struct GradArgs {
   const float* rowfac;  // null: 1
   void* dW;
   const float* scale;   // null: 1
-  int accumulate, wide;  // wide: rows of dW on 32-byte boundaries
+  int accumulate;
   int* status;
 };
 
@@ -56,56 +59,32 @@ __device__ __forceinline__ GradUnit grad_unit(const GradArgs& p, int u) {
   return g;
 }
 
-// 32 columns of a row of dW
+// 32 columns of a row of dW, added to what is there
 template <bool FP32>
-__device__ __forceinline__ void store_dw(const GradArgs& p, size_t at, const uint32_t (&r)[32],
-                                         float f) {
+__device__ __forceinline__ void add_dw(const GradArgs& p, size_t at, const uint32_t (&r)[32],
+                                       float f) {
   if constexpr (FP32) {
-    float* dst = static_cast<float*>(p.dW) + at;
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.dW) + at);
 #pragma unroll
-    for (int c = 0; c < 32; c += 8) {
-      uint32_t w[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(__uint_as_float(r[c + k]) * f);
-      if (p.accumulate) {
-#pragma unroll
-        for (int k = 0; k < 8; k += 4) {
-          const float4 old = *reinterpret_cast<const float4*>(dst + c + k);
-          w[k] = __float_as_uint(__uint_as_float(w[k]) + old.x);
-          w[k + 1] = __float_as_uint(__uint_as_float(w[k + 1]) + old.y);
-          w[k + 2] = __float_as_uint(__uint_as_float(w[k + 2]) + old.z);
-          w[k + 3] = __float_as_uint(__uint_as_float(w[k + 3]) + old.w);
-        }
-      }
-      if (p.wide) {
-        st_global_v8(dst + c, w);
-      } else {
-        *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(dst + c + 4) = make_uint4(w[4], w[5], w[6], w[7]);
-      }
+    for (int k = 0; k < 8; ++k) {
+      const float4 old = dst[k];
+      dst[k] = make_float4(fmaf(__uint_as_float(r[4 * k]), f, old.x),
+                           fmaf(__uint_as_float(r[4 * k + 1]), f, old.y),
+                           fmaf(__uint_as_float(r[4 * k + 2]), f, old.z),
+                           fmaf(__uint_as_float(r[4 * k + 3]), f, old.w));
     }
   } else {
-    uint16_t* dst = static_cast<uint16_t*>(p.dW) + at;
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dW) + at);
 #pragma unroll
-    for (int c = 0; c < 32; c += 16) {
-      uint32_t w[8], old[8] = {};
-      if (p.accumulate) {
+    for (int k = 0; k < 4; ++k) {
+      const uint4 x = dst[k];
+      const uint32_t old[4] = {x.x, x.y, x.z, x.w};
+      uint32_t w[4];
 #pragma unroll
-        for (int k = 0; k < 8; k += 4) {
-          const uint4 x = *reinterpret_cast<const uint4*>(dst + c + 2 * k);
-          old[k] = x.x, old[k + 1] = x.y, old[k + 2] = x.z, old[k + 3] = x.w;
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        w[k] = pack_bf16x2(fmaf(__uint_as_float(r[c + 2 * k]), f, bf16_lo(old[k])),
-                           fmaf(__uint_as_float(r[c + 2 * k + 1]), f, bf16_hi(old[k])));
-      if (p.wide) {
-        st_global_v8(dst + c, w);
-      } else {
-        *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-      }
+      for (int e = 0; e < 4; ++e)
+        w[e] = pack_bf16x2(fmaf(__uint_as_float(r[8 * k + 2 * e]), f, bf16_lo(old[e])),
+                           fmaf(__uint_as_float(r[8 * k + 2 * e + 1]), f, bf16_hi(old[e])));
+      dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
@@ -262,11 +241,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int cg = (warp - 2) / 4;  // its half of the tile's columns
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + cg * (kBN / 2);
     const float scale = p.scale ? __ldg(p.scale) : 1.f;
+    const int bar = 1 + 2 * cg;  // the column group's barrier
+    const bool leader = threadIdx.x - 64 - cg * 128 == 0;
+    const uint32_t buf = tiles + L::EPI_OFFSET + static_cast<uint32_t>(cg) * 16384u;
+    const uint32_t rowbase = buf + static_cast<uint32_t>(q * 32 + lane) * 128u;
+    const uint32_t r7 = static_cast<uint32_t>(lane & 7);
     int b = 0;
     uint32_t aph = 0;
     for (int i = 0; i < units; ++i) {
       const bool ok = mbar_wait(&ctrl->tfull[b], aph, abort_flag, p.status);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      // the warps stop together: they meet at the groups' barriers
+      const bool mine = __all_sync(0xffffffffu, ok);
+      if (lane == 0) ctrl->vote[i & 1][warp - 2] = mine ? 1 : 0;
+      named_bar_sync(2, 32 * kEpiWarps);
+      int all = 1;
+#pragma unroll
+      for (int w = 0; w < kEpiWarps; ++w) all &= ctrl->vote[i & 1][w];
+      if (!all) break;
       tc_fence_after();
       const GradUnit g = grad_unit(p, share.unit(i));
       const int row = g.mt * 2 * BM + static_cast<int>(rank) * BM + q * 32 + lane;
@@ -284,9 +275,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           else mbar_arrive_cluster(mapa_shared(te, 0));
         }
       };
-      if (g.dw) {
+      if (g.dw && p.accumulate) {
         for_tmem_chunks<4>(acc, 0, [&](const uint32_t(&r)[32], int c) {
-          if (c < chunks) store_dw<FP32>(p, at + c * 32, r, scale);
+          if (c < chunks) add_dw<FP32>(p, at + c * 32, r, scale);
+        }, release);
+      } else if (g.dw) {
+        // 128 bytes of each row at a time through shared memory, stored as whole lines
+        // (straight from the registers, 32 bytes a lane: the backward of 256 tokens 82 us
+        // for 74 in bf16, 113 for 105 in fp32)
+        const int all_chunks = min(4, (p.D - n0 + 31) / 32);  // of the tile, valid rows or not
+        for_tmem_chunks<4>(acc, 0, [&](const uint32_t(&r)[32], int c) {
+          if (c >= all_chunks) return;  // the same for the group
+          const int h = FP32 ? 0 : c & 1;
+          if (h == 0) {
+            if (leader) bulk_wait_read<0>();  // the store before has read the buffer
+            named_bar_sync(bar, 128);
+          }
+#pragma unroll
+          for (int v = 0; v < (FP32 ? 8 : 4); ++v) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = FP32 ? __float_as_uint(__uint_as_float(r[(4 * v + e) & 31]) * scale)
+                          : pack_bf16x2(__uint_as_float(r[(8 * v + 2 * e) & 31]) * scale,
+                                        __uint_as_float(r[(8 * v + 2 * e + 1) & 31]) * scale);
+            const uint32_t ci = static_cast<uint32_t>(h * 4 + v);
+            st_shared_v4(rowbase + ((ci ^ r7) << 4), w[0], w[1], w[2], w[3]);
+          }
+          if (FP32 || h == 1) {  // D is a multiple of 64
+            fence_proxy_async_smem();
+            named_bar_sync(bar, 128);
+            if (leader) {
+              // (the map counts two bytes)
+              tma_store_2d(&p.tmDw, buf, (n0 + (c - h) * 32) * (FP32 ? 2 : 1),
+                           g.mt * 2 * BM + static_cast<int>(rank) * BM);
+              bulk_commit();
+            }
+          }
         }, release);
       } else if (p.slices > 1) {
         float* dst = p.part + static_cast<size_t>(g.slice) * p.T * p.D + at;
@@ -320,6 +345,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         aph ^= 1u;
       }
     }
+    if (leader) bulk_wait<0>();
+    __syncwarp();
   }
   __syncthreads();
   cluster_sync_all();  // the leader's MMAs are drained before either CTA frees TMEM
@@ -352,19 +379,18 @@ __global__ void __launch_bounds__(256) k_join_dh(const float* __restrict__ part,
                  pack_bf16x2(b.x * f, b.y * f), pack_bf16x2(b.z * f, b.w * f));
 }
 
-// The slices of dH's K. A slice is at most half of what a pair has to do in all, so
-// that the deal can even it out, and at least kLeastKb k-blocks; a tile of dW counts
-// as kLeastDw k-blocks at least, the time of its outputs.
-constexpr int kLeastKb = 8, kLeastDw = 4;
-constexpr int kMostSlices = 32, kMostSliceUnits = 160;
+// The slices of dH's K: as many as make its tiles' slices about half the pairs, at least
+// kLeastKb k-blocks each. Those pairs then read W and G at the MMAs' rate while the
+// others write dW, and both end together (backward of V 50304, D 768, in us: T 256, 3
+// tiles, in 8, 12, 16, 24 slices 81, 75, 78, 83; T 1024, 12 tiles, in 1, 3, 6 slices
+// 343, 178, 193; T 4096, 48 tiles, in 1, 2 slices 657, 667).
+constexpr int kLeastKb = 8, kMostSlices = 36, kMostSliceUnits = 54;
 
 int dh_slices(int64_t T, int64_t V, int64_t D, int pairs) {
-  const int64_t n_nt = cdiv(D, kBN), dh = cdiv(T, 2 * BM) * n_nt, dw = cdiv(V, 2 * BM) * n_nt;
-  const int64_t kb = cdiv(V, BK);
-  const int64_t each = (dh * kb + dw * std::max<int64_t>(cdiv(T, BK), kLeastDw)) / pairs;
-  const int64_t most = std::min({int64_t(kMostSlices), kMostSliceUnits / dh, kb / kLeastKb});
+  const int64_t tiles = cdiv(T, 2 * BM) * cdiv(D, kBN);
+  const int64_t half = std::min(pairs, 76) * 36 / 76;
   return static_cast<int>(
-      std::max<int64_t>(1, std::min(most, cdiv(2 * kb, std::max<int64_t>(each, 1)))));
+      std::max<int64_t>(1, std::min((2 * half + tiles) / (2 * tiles), cdiv(V, BK) / kLeastKb)));
 }
 
 }  // namespace
@@ -382,6 +408,8 @@ cudaError_t launch_logprob_grads(const LogprobArgs& p, const uint16_t* G, int64_
   if (!map_kmajor(&a.tmGk, G, p.T, p.V, ldG) || !map_mnmajor(&a.tmW, p.W, p.V, p.D, p.D) ||
       !map_mnmajor(&a.tmGm, G, p.T, p.V, ldG) || !map_mnmajor(&a.tmHs, Hs, p.T, p.D, p.D))
     return cudaErrorInvalidValue;
+  const uint64_t words = static_cast<uint64_t>(p.D) * (dw_fp32 ? 2 : 1);
+  if (!make_bf16_map(&a.tmDw, dW, words, p.V, words * 2, 64, BM)) return cudaErrorInvalidValue;
   const int most = p.num_sms / 2;
   a.n_nt = tiles_of(p.D, kBN);
   a.m_dh = tiles_of(p.T, 2 * BM);
@@ -394,7 +422,6 @@ cudaError_t launch_logprob_grads(const LogprobArgs& p, const uint16_t* G, int64_
   a.T = p.T, a.V = p.V, a.D = p.D;
   a.dH = dH, a.part = part, a.rowfac = rowfac;
   a.dW = dW, a.scale = scale, a.accumulate = accumulate;
-  a.wide = reinterpret_cast<uintptr_t>(dW) % 32 == 0;
   a.status = p.status;
   const int pairs = std::min(a.n_dw + n_dh, most);
   const dim3 grid(static_cast<unsigned>(2 * pairs)), block(kThreads);
