@@ -177,15 +177,62 @@ __device__ __forceinline__ float head_slope(float z, const HeadCap& h) {
   return h.cap > 0.f ? z * (h.cap - z) * h.icap_tau : 1.f;
 }
 
-// K = 1: coef[t] = c, with the sign of a; f[t] and rowfac[t] = |a| / |c|, 0 where a
-// is; *scale = m. One block: m is needed before anything else.
-constexpr int kCoefThreads = 1024;
+// K = 1: the largest |w| among tokens first, first + step, ... and whether an id is bad.
+__device__ __forceinline__ float top_coef(const float* __restrict__ dlogp,
+                                          const int32_t* __restrict__ ids, int64_t first,
+                                          int64_t step, int T, int V, bool& bad) {
+  float top = 0.f;
+#pragma unroll 4
+  for (int64_t t = first; t < T; t += step) {
+    const int id = __ldg(ids + t);
+    const float w = __ldg(dlogp + t);
+    bad |= id < -1 || id >= V;
+    if (id >= 0) top = fmaxf(top, fabsf(w));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  return top;
+}
+
+struct CoefArgs {
+  const float* dlogp;
+  const int32_t* ids;
+  const float *logp, *lse;
+  HeadCap head;
+  float *coef, *f, *rowfac;
+};
+
+// K = 1: coef[t] = c, with the sign of a; f[t] and rowfac[t] = |a| / |c|, 0 where a is.
+__device__ __forceinline__ void scale_coef(const CoefArgs& p, int64_t t, float top) {
+  const float w = __ldg(p.ids + t) >= 0 ? __ldg(p.dlogp + t) : 0.f;
+  const float l = __ldg(p.logp + t), z = l + __ldg(p.lse + t);
+  float c = 0.f, ft = 0.f, rf = 0.f;
+  if (w != 0.f) {  // (a NaN too)
+    const float size = fabsf(w), x = size / top;
+    // the power of two below x; x itself where it is none or no normal number
+    ft = __uint_as_float(__float_as_uint(x) & 0x7f800000u);
+    if (!(ft > 0.f && ft <= 1.f)) ft = x;
+    c = x > 0.f ? x / ft : 1.f;  // (beside an infinite coefficient x is 0)
+    const float g = c * (1.f - expf(l)) * head_slope(z, p.head);
+    const float r = __uint_as_float(static_cast<uint32_t>(bf16_bits(g)) << 16);
+    if (x > 0.f && !(fabsf(r - g) <= kMostRounding * fabsf(g))) {
+      ft = x;
+      c = 1.f;
+    }
+    rf = size / c;
+    c = w > 0.f ? -c : c;
+  }
+  p.coef[t] = c;
+  p.f[t] = ft;
+  p.rowfac[t] = rf;
+}
+
+// Up to kOneBlockTokens in one block, which finds m and then scales; beyond, a kernel
+// for each (16384 tokens: 20 us in one block, 6 in two kernels).
+constexpr int kCoefThreads = 1024, kOneBlockTokens = 4096;
 
 __global__ void __launch_bounds__(kCoefThreads)
-    k_logprob_coef_one(const float* __restrict__ dlogp, const int32_t* __restrict__ ids, int T,
-                       int V, const float* __restrict__ logp, const float* __restrict__ lse,
-                       HeadCap head, float* __restrict__ coef, float* __restrict__ f,
-                       float* __restrict__ rowfac, float* __restrict__ scale, int* status) {
+    k_logprob_coef_one(const CoefArgs p, int T, int V, float* __restrict__ scale, int* status) {
   __shared__ float s_top[kCoefThreads / 32];
   __shared__ int s_go;
   pdl_enter();
@@ -193,48 +240,37 @@ __global__ void __launch_bounds__(kCoefThreads)
   __syncthreads();
   if (!s_go) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  float top = 0.f;
   bool bad = false;
-#pragma unroll 4
-  for (int64_t t = threadIdx.x; t < T; t += kCoefThreads) {
-    const int id = __ldg(ids + t);
-    const float w = __ldg(dlogp + t);
-    bad |= id < -1 || id >= V;
-    if (id >= 0) top = fmaxf(top, fabsf(w));
-  }
+  float top = top_coef(p.dlogp, p.ids, threadIdx.x, kCoefThreads, T, V, bad);
   if (bad) set_status(status, SS_ERR_TARGET_RANGE);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   if (lane == 0) s_top[warp] = top;
   __syncthreads();
   top = s_top[lane];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   if (threadIdx.x == 0) *scale = top;
-#pragma unroll 4
-  for (int64_t t = threadIdx.x; t < T; t += kCoefThreads) {
-    const float w = __ldg(ids + t) >= 0 ? __ldg(dlogp + t) : 0.f;
-    const float l = __ldg(logp + t), z = l + __ldg(lse + t);
-    float c = 0.f, ft = 0.f, rf = 0.f;
-    if (w != 0.f) {  // (a NaN too)
-      const float size = fabsf(w), x = size / top;
-      // the power of two below x; x itself where it is none or no normal number
-      ft = __uint_as_float(__float_as_uint(x) & 0x7f800000u);
-      if (!(ft > 0.f && ft <= 1.f)) ft = x;
-      c = x > 0.f ? x / ft : 1.f;  // (beside an infinite coefficient x is 0)
-      const float g = c * (1.f - expf(l)) * head_slope(z, head);
-      const float r = __uint_as_float(static_cast<uint32_t>(bf16_bits(g)) << 16);
-      if (x > 0.f && !(fabsf(r - g) <= kMostRounding * fabsf(g))) {
-        ft = x;
-        c = 1.f;
-      }
-      rf = size / c;
-      c = w > 0.f ? -c : c;
-    }
-    coef[t] = c;
-    f[t] = ft;
-    rowfac[t] = rf;
-  }
+  for (int64_t t = threadIdx.x; t < T; t += kCoefThreads) scale_coef(p, t, top);
+}
+
+// *scale, 0 before, as the bits of a number that is not negative
+__global__ void __launch_bounds__(256) k_logprob_top(const CoefArgs p, int T, int V,
+                                                     uint32_t* scale, int* status) {
+  pdl_enter();
+  if (read_status(status) != 0) return;
+  bool bad = false;
+  const float top = top_coef(p.dlogp, p.ids, blockIdx.x * int64_t(256) + threadIdx.x,
+                             int64_t(gridDim.x) * 256, T, V, bad);
+  if (bad) set_status(status, SS_ERR_TARGET_RANGE);
+  if ((threadIdx.x & 31) == 0 && top > 0.f) atomicMax(scale, __float_as_uint(top));
+}
+
+__global__ void __launch_bounds__(256) k_logprob_scale(const CoefArgs p, int T,
+                                                       const float* scale, int* status) {
+  pdl_enter();
+  if (read_status(status) != 0) return;
+  const float top = *scale;
+  for (int64_t t = blockIdx.x * int64_t(256) + threadIdx.x; t < T; t += int64_t(gridDim.x) * 256)
+    scale_coef(p, t, top);
 }
 
 // K > 1: coef[t] = -sum_k w[t, k], and f[t] = 1 or 0: whether any w is not 0. A warp
@@ -456,10 +492,23 @@ ss_status ss_logprob_backward(const float* dlogp, const uint16_t* H, const uint1
   cudaError_t e;
   {
     StageTrace trace(s, "logprob_coef");
-    e = iK == 1 ? launch_pdl(k_logprob_coef_one, dim3(1), dim3(kCoefThreads), 0, s, dlogp, ids,
-                             p.T, p.V, logp, lse, p.head, coef, f, rowfac, scale, p.status)
-                : launch_pdl(k_logprob_coef, dim3(grid), dim3(256), 0, s, dlogp, ids, iK, p.T,
-                             p.V, coef, f, p.status);
+    const CoefArgs c{dlogp, ids, logp, lse, p.head, coef, f, rowfac};
+    const dim3 blocks(static_cast<unsigned>(std::min((T + 255) / 256, int64_t(p.num_sms) * 4)));
+    if (iK > 1) {
+      e = launch_pdl(k_logprob_coef, dim3(grid), dim3(256), 0, s, dlogp, ids, iK, p.T, p.V, coef,
+                     f, p.status);
+    } else if (T <= kOneBlockTokens) {
+      e = launch_pdl(k_logprob_coef_one, dim3(1), dim3(kCoefThreads), 0, s, c, p.T, p.V, scale,
+                     p.status);
+    } else {
+      e = cudaMemsetAsync(scale, 0, sizeof *scale, s);
+      if (e == cudaSuccess)
+        e = launch_pdl(k_logprob_top, blocks, dim3(256), 0, s, c, p.T, p.V,
+                       reinterpret_cast<uint32_t*>(scale), p.status);
+      if (e == cudaSuccess)
+        e = launch_pdl(k_logprob_scale, blocks, dim3(256), 0, s, c, p.T,
+                       static_cast<const float*>(scale), p.status);
+    }
   }
   if (e != cudaSuccess) return record_failure("launch k_logprob_coef", e);
   {

@@ -405,3 +405,13 @@ def test_past_two_to_the_32_logits():
     want = P.T @ H.to(F64)
     # two roundings of at most 2^-8, 1e-4 for a sum of 90000 in fp32
     assert (dW[cols].to(F64) - want).norm() <= (2 ** -7 + 1e-4) * want.norm()
+
+
+def test_more_tokens_than_one_block_scales():
+    """One id per token, and more tokens than one block looks through for the largest
+    coefficient."""
+    T, V, D = 5000, 200, 64
+    H, W, ids, dlogp = _inputs(T, V, D, 1, seed=9)
+    dlogp[3:4000:7] = 0
+    logp, lse = _forward(H, W, ids)
+    _backward(dlogp, H, W, ids, logp, lse)
