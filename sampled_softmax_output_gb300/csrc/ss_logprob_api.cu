@@ -315,8 +315,9 @@ __global__ void __launch_bounds__(256) k_logprob_patch(
     const float* __restrict__ coef, const float* __restrict__ f, int K, int T, int V, int D,
     HeadCap head, const uint16_t* __restrict__ H, uint16_t* __restrict__ Hs,
     uint16_t* __restrict__ G, int64_t ldG, int* status) {
-  __shared__ int s_id[8][SS_MAX_IDS];
+  __shared__ __align__(16) int s_id[8][SS_MAX_IDS];
   __shared__ float s_w[8][SS_MAX_IDS];
+  static_assert(SS_MAX_IDS % 4 == 0, "four ids at a time");
   pdl_enter();
   if (read_status(status) != 0) return;  // no barrier of the block follows
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
@@ -332,8 +333,9 @@ __global__ void __launch_bounds__(256) k_logprob_patch(
                                    : uint16_t(0);
       }
     } else {
-      for (int k = lane; k < K; k += 32) {
-        const int id = __ldg(ids + t * K + k);
+      const int K4 = (K + 3) / 4 * 4;
+      for (int k = lane; k < K4; k += 32) {
+        const int id = k < K ? __ldg(ids + t * K + k) : -1;
         s_id[warp][k] = id < V ? id : -1;
         s_w[warp][k] = id >= 0 ? __ldg(dlogp + t * K + k) : 0.f;
       }
@@ -341,14 +343,22 @@ __global__ void __launch_bounds__(256) k_logprob_patch(
       for (int k = lane; k < K; k += 32) {
         const int id = s_id[warp][k];
         if (id < 0) continue;
-        float w = 0.f;
-        bool first = true;
-        for (int j = 0; j < K; ++j)
-          if (s_id[warp][j] == id) {
-            first = first && j >= k;
-            w += s_w[warp][j];
-          }
-        if (!first) continue;
+        float w = s_w[warp][k];
+        int equal = 0;
+        for (int j = 0; j < K4; j += 4) {
+          const int4 v = *reinterpret_cast<const int4*>(&s_id[warp][j]);
+          equal += (v.x == id) + (v.y == id) + (v.z == id) + (v.w == id);
+        }
+        if (equal > 1) {  // rare: the sum of them all, written by the first
+          bool first = true;
+          w = 0.f;
+          for (int j = 0; j < K; ++j)
+            if (s_id[warp][j] == id) {
+              first = first && j >= k;
+              w += s_w[warp][j];
+            }
+          if (!first) continue;
+        }
         const float l = __ldg(logp + t * K + k);
         const float g = a != 0.f ? fmaf(a, expf(l), w) : w;
         G[t * ldG + id] =

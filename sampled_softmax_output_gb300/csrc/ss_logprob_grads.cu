@@ -7,6 +7,7 @@
 // bits every time). The tiles of dW keep the other pairs busy meanwhile; a tile of
 // either length goes to the pair that is free first (deal_units of ss_ffn_plan.h).
 #include <algorithm>
+#include <type_traits>
 
 #include "ss_ffn.cuh"
 #include "ss_gemm.cuh"
@@ -146,27 +147,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int s = 0;
       uint32_t ph = 0, issued = 0, issued_ph = 0;
       bool ok = true;
-      const uint64_t keep = l2_evict_last();  // B: W or Hs, re-read by every row tile
-      for (int i = 0; ok && i < units; ++i) {
-        const GradUnit g = grad_unit(p, share.unit(i));
+      const uint64_t keep = l2_evict_last();  // W and Hs are re-read by every row tile
+      // (a loop for each kind of unit, here and below: what this one thread decides per
+      // k-block, both CTAs' tensor cores wait for; T 3001, D 1024, V 24576: 177 us, with
+      // the kind asked for at every copy and MMA 202)
+      auto load = [&](const GradUnit& g, const CUtensorMap* ma, const CUtensorMap* mb, auto dw) {
         const int m0 = g.mt * 2 * BM + static_cast<int>(rank) * BM;
         const int n0 = g.nt * kBN + static_cast<int>(rank) * (kBN / 2);
-        const CUtensorMap* mb = g.dw ? &p.tmHs : &p.tmW;
         for (int kb = g.kb0; kb < g.kb1; ++kb) {
-          if (!mbar_wait(&ctrl->empty[s], ph ^ 1u, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
+          if (!mbar_wait(&ctrl->empty[s], ph ^ 1u, abort_flag, p.status)) return false;
           const uint32_t fb_local = smem_u32(&ctrl->full[s]);
           if (rank == 0) mbar_arrive_expect_tx(&ctrl->full[s], 2 * L::STAGE_BYTES);
           const uint32_t fb = rank == 0 ? fb_local : mapa_shared(fb_local, 0);
           const uint32_t a_dst = tiles + s * L::STAGE_BYTES;
           const uint32_t b_dst = a_dst + L::A_BYTES;
-          if (g.dw) {
-            tma_load_2d_pair(a_dst, &p.tmGm, fb, m0, kb * BK);
-            tma_load_2d_pair(a_dst + 8192, &p.tmGm, fb, m0 + 64, kb * BK);
+          if constexpr (decltype(dw)::value) {
+            tma_load_2d_pair(a_dst, ma, fb, m0, kb * BK);
+            tma_load_2d_pair(a_dst + 8192, ma, fb, m0 + 64, kb * BK);
           } else {
-            tma_load_2d_pair(a_dst, &p.tmGk, fb, kb * BK, m0);
+            tma_load_2d_pair(a_dst, ma, fb, kb * BK, m0);
           }
           tma_load_2d_pair_hint(b_dst, mb, fb, n0, kb * BK, keep);
           tma_load_2d_pair_hint(b_dst + 8192, mb, fb, n0 + 64, kb * BK, keep);
@@ -177,6 +176,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ph ^= 1u;
           }
         }
+        return true;
+      };
+      for (int i = 0; ok && i < units; ++i) {
+        const GradUnit g = grad_unit(p, share.unit(i));
+        ok = g.dw ? load(g, &p.tmGm, &p.tmHs, std::true_type{})
+                  : load(g, &p.tmGk, &p.tmW, std::false_type{});
       }
       if (rank == 0) {
         for (int i = 0; i < kStages; ++i)
@@ -193,37 +198,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer (leader)
     if (lane == 0 && rank == 0) {
-      constexpr uint32_t idesc_dw = idesc_bf16_f32(2 * BM, kBN, true, true);
-      constexpr uint32_t idesc_dh = idesc_bf16_f32(2 * BM, kBN, false, true);
       int s = 0, b = 0;
       uint32_t ph = 0, aph = 0;
       bool ok = true;
-      for (int i = 0; ok && i < units; ++i) {
-        const GradUnit g = grad_unit(p, share.unit(i));
-        if (!mbar_wait(&ctrl->tempty[b], aph ^ 1u, abort_flag, p.status)) break;
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(b * kBN);
+      auto multiply = [&](const GradUnit& g, uint32_t d_tmem, auto dw) {
+        constexpr bool kDw = decltype(dw)::value;
+        constexpr uint32_t idesc = idesc_bf16_f32(2 * BM, kBN, kDw, true);
         for (int kb = g.kb0; kb < g.kb1; ++kb) {
-          if (!mbar_wait(&ctrl->full[s], ph, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
+          if (!mbar_wait(&ctrl->full[s], ph, abort_flag, p.status)) return false;
           tc_fence_after();
           const uint32_t a_addr = tiles + s * L::STAGE_BYTES;
           const uint32_t b_addr = a_addr + L::A_BYTES;
 #pragma unroll
-          for (int k = 0; k < BK / UMMA_K; ++k) {
-            const uint64_t ad = g.dw ? sdesc_sw128(a_addr + k * 2048, 8192, 1024)
-                                     : sdesc_sw128(a_addr + k * 32, 16, 1024);
-            mma_bf16_pair(d_tmem, ad, sdesc_sw128(b_addr + k * 2048, 8192, 1024),
-                          g.dw ? idesc_dw : idesc_dh, (kb > g.kb0 || k > 0) ? 1u : 0u);
-          }
+          for (int k = 0; k < BK / UMMA_K; ++k)
+            mma_bf16_pair(d_tmem,
+                          kDw ? sdesc_sw128(a_addr + k * 2048, 8192, 1024)
+                              : sdesc_sw128(a_addr + k * 32, 16, 1024),
+                          sdesc_sw128(b_addr + k * 2048, 8192, 1024), idesc,
+                          (kb > g.kb0 || k > 0) ? 1u : 0u);
           mma_commit_pair(&ctrl->empty[s], 0x3);
           if (++s == kStages) {
             s = 0;
             ph ^= 1u;
           }
         }
+        return true;
+      };
+      for (int i = 0; ok && i < units; ++i) {
+        const GradUnit g = grad_unit(p, share.unit(i));
+        if (!mbar_wait(&ctrl->tempty[b], aph ^ 1u, abort_flag, p.status)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(b * kBN);
+        ok = g.dw ? multiply(g, d_tmem, std::true_type{}) : multiply(g, d_tmem, std::false_type{});
         if (!ok) break;
         mma_commit_pair(&ctrl->tfull[b], 0x3);
         if (++b == 2) {
@@ -382,8 +388,8 @@ __global__ void __launch_bounds__(256) k_join_dh(const float* __restrict__ part,
 // The slices of dH's K: as many as make its tiles' slices about half the pairs, at least
 // kLeastKb k-blocks each. Those pairs then read W and G at the MMAs' rate while the
 // others write dW, and both end together (backward of V 50304, D 768, in us: T 256, 3
-// tiles, in 8, 12, 16, 24 slices 81, 75, 78, 83; T 1024, 12 tiles, in 1, 3, 6 slices
-// 343, 178, 193; T 4096, 48 tiles, in 1, 2 slices 657, 667).
+// tiles, in 8, 12, 16, 24 slices 77, 72, 76, 81; T 1024, 12 tiles, in 1, 3, 6 slices
+// 306, 167, 183; T 4096, 48 tiles, in 1, 2 slices 612, 630).
 constexpr int kLeastKb = 8, kMostSlices = 36, kMostSliceUnits = 54;
 
 int dh_slices(int64_t T, int64_t V, int64_t D, int pairs) {
@@ -418,15 +424,15 @@ cudaError_t launch_logprob_grads(const LogprobArgs& p, const uint16_t* G, int64_
   a.kb_dw = tiles_of(p.T, BK);
   a.kb_dh = tiles_of(p.V, BK);
   const int n_dh = a.m_dh * a.n_nt * a.slices;
-  a.deal = deal_units(a.n_dw, a.kb_dw, n_dh, cdiv(a.kb_dh, a.slices));
   a.T = p.T, a.V = p.V, a.D = p.D;
   a.dH = dH, a.part = part, a.rowfac = rowfac;
   a.dW = dW, a.scale = scale, a.accumulate = accumulate;
   a.status = p.status;
-  const int pairs = std::min(a.n_dw + n_dh, most);
-  const dim3 grid(static_cast<unsigned>(2 * pairs)), block(kThreads);
-  cudaError_t e = dw_fp32 ? launch_pdl(k_logprob_grads<true>, grid, block, L::TOTAL, s, a)
-                          : launch_pdl(k_logprob_grads<false>, grid, block, L::TOTAL, s, a);
+  a.deal = deal_units(a.n_dw, a.kb_dw, n_dh, cdiv(a.kb_dh, a.slices));
+  const dim3 grid(static_cast<unsigned>(2 * std::min(a.n_dw + n_dh, most))), block(kThreads);
+  const cudaError_t e =
+      dw_fp32 ? launch_pdl(k_logprob_grads<true>, grid, block, L::TOTAL, s, a)
+              : launch_pdl(k_logprob_grads<false>, grid, block, L::TOTAL, s, a);
   if (e != cudaSuccess || a.slices == 1) return e;
   const int64_t n8 = static_cast<int64_t>(p.T) * p.D / 8;
   return launch_pdl(k_join_dh, dim3(static_cast<unsigned>((n8 + 255) / 256)), dim3(256), 0, s,
