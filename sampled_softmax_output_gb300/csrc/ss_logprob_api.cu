@@ -42,7 +42,7 @@ LogprobLayout logprob_layout(int64_t T, int64_t V, int64_t D, bool backward) {
   L.rowfac = L.f + up1024(static_cast<size_t>(T) * sizeof(float));
   L.hs = L.rowfac + up1024(static_cast<size_t>(T) * sizeof(float));
   L.dh_part = L.hs + up1024(static_cast<size_t>(T) * D * 2);
-  L.g = L.dh_part + up1024(logprob_part_bytes(T, D) + 32);
+  L.g = L.dh_part + up1024(T > 0 ? logprob_part_bytes(T, D) + 32 : 0);
   const size_t both = L.g + up1024(static_cast<size_t>(T) * L.ldG * 2);
   L.total = backward ? std::max(forward, both) : forward;
   return L;

@@ -55,6 +55,9 @@ def _head_of(cap, tau):
     return None if cap == 0 else Head(cap, tau, 0)
 
 
+# As in block.py, the checks run in front of launches of a few microseconds: the cheap
+# questions first, _need, which says what is wrong, only where one of them fails.
+
 def _expect(t, name, dtype, index, shape, device):
     if not _fits(t, dtype, index, shape):
         _need(t, name, dtype, device, shape)
@@ -65,6 +68,27 @@ def _out(t, name, dtype, like_shape, index, device):
         return torch.empty(like_shape, dtype=dtype, device=device)
     _expect(t, name, dtype, index, like_shape, device)
     return t
+
+
+def _rows_like(logp, **others):
+    """The device index of logp, an fp32 tensor, which `others` (None: not given) are
+    like."""
+    try:
+        index, shape = logp.get_device(), logp.shape
+        if index >= 0 and logp.dtype is _F32 and logp.is_contiguous():
+            for t in others.values():
+                if t is not None and not (t.dtype is _F32 and t.shape == shape
+                                          and t.get_device() == index and t.is_contiguous()):
+                    break
+            else:
+                return index
+    except AttributeError:  # no tensor
+        pass
+    _need(logp, "logp", _F32)
+    for name, t in others.items():
+        if t is not None:
+            _need(t, name, _F32, logp.device, logp.shape)
+    raise AssertionError("unreachable: one of the checks above fails")
 
 
 def logprob_workspace_size(T: int, V: int, D: int, backward: bool = True) -> int:
@@ -86,19 +110,31 @@ def logprob_workspace(T: int, V: int, D: int, backward: bool = True, device=None
 
 def _logprob_args(H, W, ids, ws):
     """Checked (device index, T, V, D, K)."""
+    try:
+        index = H.get_device()
+        T, D = H.shape
+        V = W.shape[0]
+        n = ids.shape
+        if (index >= 0 and H.dtype is W.dtype is _BF16 and ids.dtype is _I32 and ws.dtype is _U8
+                and W.shape == (V, D) and 1 <= len(n) <= 2 and n[0] == T
+                and W.get_device() == ids.get_device() == ws.get_device() == index
+                and H.is_contiguous() and W.is_contiguous() and ids.is_contiguous()
+                and ws.is_contiguous()):
+            return index, T, V, D, n[1] if len(n) == 2 else 1
+    except (AttributeError, IndexError, ValueError):
+        pass
     _need(H, "H", _BF16)
     if H.dim() != 2:
         raise ValueError(f"H must be [T, D], got {tuple(H.shape)}")
     T, D = H.shape
-    dev, index = H.device, H.get_device()
+    dev = H.device
     _need(W, "W", _BF16, dev)
-    V = W.shape[0] if W.dim() else 0
-    _need(W, "W", _BF16, dev, (V, D))
+    _need(W, "W", _BF16, dev, (W.shape[0] if W.dim() else 0, D))
     _need(ids, "ids", _I32, dev)
     if ids.dim() not in (1, 2) or ids.shape[0] != T:
         raise ValueError(f"ids must be [{T}] or [{T}, K], got {tuple(ids.shape)}")
     _need(ws, "workspace", _U8, dev)
-    return index, T, V, D, ids.shape[1] if ids.dim() == 2 else 1
+    raise AssertionError("unreachable: one of the checks above fails")
 
 
 def logprobs(H: torch.Tensor, W: torch.Tensor, ids: torch.Tensor, ws: torch.Tensor,
@@ -142,14 +178,6 @@ def logprobs_backward(dlogp: torch.Tensor, H: torch.Tensor, W: torch.Tensor, ids
     return dH, dW
 
 
-def _rows(logp, name="logp"):
-    """The device index of an fp32 tensor of any shape."""
-    if not (isinstance(logp, torch.Tensor) and logp.dtype is _F32 and logp.is_cuda
-            and logp.is_contiguous()):
-        _need(logp, name, _F32)
-    return logp.get_device()
-
-
 def policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantage: torch.Tensor,
                 ref_logp: torch.Tensor | None = None, weight: torch.Tensor | None = None,
                 clip=0.2, kl: float = 0.0, scale: float = 1.0):
@@ -159,19 +187,19 @@ def policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantage: torch.Ten
     with r = exp(logp - old_logp), d = ref_logp - logp; clip is (low, high), or one
     number for both. Returns {"loss", "dlogp"} and with ref_logp "kl", each like
     logp; dlogp = scale * d loss / d logp. Tokens of weight 0 give 0."""
-    index, dev, shape = _rows(logp), logp.device, logp.shape
-    for t, name in ((old_logp, "old_logp"), (advantage, "advantage")):
-        _expect(t, name, _F32, index, shape, dev)
-    for t, name in ((ref_logp, "ref_logp"), (weight, "weight")):
-        if t is not None:
-            _expect(t, name, _F32, index, shape, dev)
+    if old_logp is None or advantage is None:
+        raise TypeError("old_logp and advantage must be torch.Tensors")
+    index = _rows_like(logp, old_logp=old_logp, advantage=advantage, ref_logp=ref_logp,
+                       weight=weight)
     low, high = clip if isinstance(clip, (tuple, list)) else (clip, clip)
-    out = {"loss": torch.empty_like(logp), "dlogp": torch.empty_like(logp)}
+    loss, dlogp = torch.empty_like(logp), torch.empty_like(logp)
+    out = {"loss": loss, "dlogp": dlogp}
+    k = None
     if ref_logp is not None:
-        out["kl"] = torch.empty_like(logp)
+        out["kl"] = k = torch.empty_like(logp)
     _call(_lib.ss_policy_loss, index, logp.data_ptr(), old_logp.data_ptr(), advantage.data_ptr(),
-          _at(ref_logp), _at(weight), logp.numel(), low, high, kl, scale, out["loss"].data_ptr(),
-          _at(out.get("kl")), out["dlogp"].data_ptr())
+          _at(ref_logp), _at(weight), logp.numel(), low, high, kl, scale, loss.data_ptr(), _at(k),
+          dlogp.data_ptr())
     return out
 
 
@@ -185,16 +213,15 @@ def preference_loss(logp: torch.Tensor, offsets: torch.Tensor, ws: torch.Tensor,
     (rejected). kind: "sigmoid" (with label smoothing), "hinge" or "ipo". Any
     workspace of the package records a bad offset. Returns {"loss" [P], "reward"
     [P, 2], "dlogp" [n]}; dlogp = scale * d loss / d logp, 0 outside the sequences."""
-    index, dev = _rows(logp), logp.device
+    index, dev = _rows_like(logp, ref_logp=ref_logp, weight=weight), logp.device
     if logp.dim() != 1:
         raise ValueError(f"logp must be [n], got {tuple(logp.shape)}")
-    _need(offsets, "offsets", _I32, dev)
+    if not _fits(offsets, _I32, index, getattr(offsets, "shape", None)):
+        _need(offsets, "offsets", _I32, dev)
     if offsets.dim() != 1 or offsets.numel() % 2 != 1:
         raise ValueError(f"offsets must be [2 P + 1], got {tuple(offsets.shape)}")
-    for t, name in ((ref_logp, "ref_logp"), (weight, "weight")):
-        if t is not None:
-            _expect(t, name, _F32, index, logp.shape, dev)
-    _need(ws, "workspace", _U8, dev)
+    if not _fits(ws, _U8, index, getattr(ws, "shape", None)):
+        _need(ws, "workspace", _U8, dev)
     code = PREFERENCES.get(kind)
     if code is None:
         raise ValueError(f"kind must be one of {sorted(PREFERENCES)}, got {kind!r}")
@@ -216,7 +243,7 @@ def distill_loss(logp: torch.Tensor, teacher: torch.Tensor, ids: torch.Tensor | 
     log-probabilities, what they leave of 1 being one more class. ids [T, K]: an
     entry of -1 is absent. weight [T]. Returns {"loss" [T], "dlogp" [T, K]}; dlogp =
     scale * d loss / d logp."""
-    index, dev = _rows(logp), logp.device
+    index, dev = _rows_like(logp), logp.device
     if logp.dim() != 2:
         raise ValueError(f"logp must be [T, K], got {tuple(logp.shape)}")
     T, K = logp.shape
