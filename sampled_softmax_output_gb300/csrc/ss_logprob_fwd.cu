@@ -32,7 +32,9 @@ namespace ss {
 
 namespace {
 
-constexpr int kRunKb = 4;  // k-blocks of 64 in one accumulator
+// k-blocks of 64 in one accumulator (T 16384, V 50304, D 768: 753, 722 and 687 us for
+// 4, 6 and 12)
+constexpr int kRunKb = 6;
 constexpr int kIdRows = 32;  // tokens whose ids are sorted together: an epilogue warp's
 constexpr int kBN = kBnLogits;
 constexpr int kStages = 6;
