@@ -34,7 +34,7 @@ cudaError_t launch_logprob_partials(const LogprobArgs& p, int K, const uint32_t*
 // The same for a few tokens in one kernel, with partials of its own: how many there are
 // (0: too many tokens for it), part [parts][T].
 constexpr int kFewTokens = 2, kMostFewParts = 1024;
-int logprob_few_parts(int64_t T, int64_t V, int64_t D, int num_sms);
+int logprob_few_parts(int64_t T, int64_t V, int num_sms);
 cudaError_t launch_logprob_few(const LogprobArgs& p, int K, const int32_t* ids, int parts,
                                float2* part, float* z, cudaStream_t s);
 

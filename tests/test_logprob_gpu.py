@@ -13,7 +13,9 @@ BF16, F32T, I32 = torch.bfloat16, torch.float32, torch.int32
 # one k-block, of a run and a part of one, several runs
 SIZES = [(1, 1, 64, 1), (1, 1000, 768, 1), (2, 257, 64, 3), (31, 300, 192, 5), (33, 129, 256, 1),
          (100, 255, 320, 7), (128, 256, 128, 1), (129, 1023, 832, 20), (255, 127, 576, 32),
-         (257, 513, 1088, 1), (300, 3001, 768, 128), (513, 2049, 64, 2), (1003, 777, 448, 4)]
+         (257, 513, 1088, 1), (300, 3001, 768, 128), (513, 2049, 64, 2), (1003, 777, 448, 4),
+         # the widest model, the largest vocabulary
+         (2, 70, 16384, 1), (3, 300, 16384, 2), (40, 524288, 64, 3), (1, 524288, 64, 128)]
 
 
 def _inputs(T, V, D, K, seed=0, std=3.0):
@@ -210,6 +212,7 @@ def test_garbage_in_tokens_without_a_gradient(K):
     ref_logp, ref_lse = ss.logprobs(clean, W, ids, ws)
     live = ~(pad | gone)
     assert torch.equal(logp[live], ref_logp[live]) and torch.equal(lse[live], ref_lse[live])
+    assert not lse[pad].isfinite().any() and not logp[pad].isfinite().any()
     dH, dW = ss.logprobs_backward(dlogp, H, W, ids, logp, lse, ws)
     ref_dH, ref_dW = ss.logprobs_backward(dlogp, clean, W, ids, ref_logp, ref_lse, ws)
     assert torch.equal(dW, ref_dW) and torch.equal(dH, ref_dH)
@@ -415,3 +418,12 @@ def test_more_tokens_than_one_block_scales():
     dlogp[3:4000:7] = 0
     logp, lse = _forward(H, W, ids)
     _backward(dlogp, H, W, ids, logp, lse)
+
+
+@pytest.mark.parametrize("T", [1, 2, 5])
+def test_a_row_that_is_no_number(T):
+    H, W, ids, _ = _inputs(T, 300, 128, 2)
+    H[T - 1] = float("nan")
+    logp, lse = ss.logprobs(H, W, ids, ss.logprob_workspace(T, 300, 128))
+    assert lse[T - 1].isnan() and logp[T - 1].isnan().all()
+    assert lse[:T - 1].isfinite().all() and logp[:T - 1].isfinite().all()
