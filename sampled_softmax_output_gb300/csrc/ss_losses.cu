@@ -164,7 +164,7 @@ __device__ __forceinline__ void for_groups(int64_t begin, int64_t end, bool vec,
 __device__ __forceinline__ Pair pair_over(Pair a, Pair b) {
   const float q = a.hi / b.hi;
   const float left = (fmaf(-q, b.hi, a.hi) + a.lo) - q * b.lo;
-  return Pair{q, left / b.hi};
+  return Pair{q, fabsf(q) < INFINITY ? left / b.hi : 0.f};
 }
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
@@ -260,7 +260,8 @@ __global__ void __launch_bounds__(kPrefThreads, 6) k_preference_loss(const Prefe
       if (p.kind == SS_PREF_SIGMOID) {
         // log s(h) = min(h, 0) - log(1 + exp(-|h|))
         const float e = expf(-fabsf(h)), l = log1pf(e);
-        loss = (1.f - p.smoothing) * (fmaxf(-h, 0.f) + l) + p.smoothing * (fmaxf(h, 0.f) + l);
+        loss = (1.f - p.smoothing) * (fmaxf(-h, 0.f) + l);
+        if (p.smoothing > 0.f) loss += p.smoothing * (fmaxf(h, 0.f) + l);  // (not 0 times inf)
         const float s_neg = h >= 0.f ? e / (1.f + e) : 1.f / (1.f + e);  // s(-h)
         slope = p.beta * (p.smoothing - s_neg);
       } else if (p.kind == SS_PREF_HINGE) {

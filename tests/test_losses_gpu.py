@@ -197,6 +197,20 @@ def test_preference_far_margins():
     assert got["loss"].tolist() == [0.0, 5001.0]
 
 
+@pytest.mark.parametrize("average", [False, True])
+def test_preference_of_an_impossible_token(average):
+    """A log-probability of -infinity that counts: an infinite margin, not a NaN."""
+    logp = torch.tensor([-1.0, -2.0, -3.0, -INF, -1.0, -1.0, -INF, -1.0], device="cuda")
+    at = torch.tensor([0, 2, 4, 6, 8], dtype=I32, device="cuda")
+    got = ss.preference_loss(logp, at, _ws(), average=average)
+    assert got["loss"].tolist() == [0.0, 0.0] and got["reward"][:, 1].tolist() == [-INF, -INF]
+    assert (got["dlogp"] == 0).all()
+    swapped = torch.cat([logp[2:4], logp[:2]])
+    got = ss.preference_loss(swapped, at[:3], _ws(), average=average)
+    assert got["loss"].tolist() == [INF] and got["reward"][0, 0] == -INF
+    assert got["dlogp"].isfinite().all()
+
+
 def test_preference_masked_values_and_padding():
     logp, at, ref, m = _pref_inputs([50, 70, 0, 33], before=5, after=20)
     ws = _ws()
