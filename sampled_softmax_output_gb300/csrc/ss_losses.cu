@@ -484,10 +484,11 @@ __global__ void __launch_bounds__(256, 5) k_distill_loss(const DistillArgs p) {
         }
       }
       loss = join(loss);
-      const float p1 = fmaxf((1.f - join(sp[0])) - join(sp[1]), 0.f);
-      const float rest = (1.f - join(sq[0])) - join(sq[1]), q1 = fmaxf(rest, kTailFloor);
-      if (p1 > 0.f) extra = p1 * (logf(p1) - logf(q1));
-      const float ratio = rest > kTailFloor ? p1 / q1 : 0.f;
+      const float left = (1.f - join(sp[0])) - join(sp[1]), p1 = left < 0.f ? 0.f : left;
+      const float rest = (1.f - join(sq[0])) - join(sq[1]);
+      const float q1 = rest < kTailFloor ? kTailFloor : rest;  // (a NaN stays in both)
+      if (p1 != 0.f) extra = p1 * (logf(p1) - logf(q1));
+      const float ratio = rest <= kTailFloor ? 0.f : p1 / q1;
 #pragma unroll
       for (int i = 0; i < 4; ++i) l[i] = fmaf(ratio, q[i], -x[i]);
     } else {
@@ -508,7 +509,7 @@ __global__ void __launch_bounds__(256, 5) k_distill_loss(const DistillArgs p) {
       }
       sum = join(sum);
       part = join(part);
-      const float per = sum > 0.f ? 1.f / sum : 0.f;
+      const float per = sum != 0.f ? 1.f / sum : 0.f;  // (a NaN stays)
       loss = part * per;
       if (sum > 0.f) extra = -logf(sum);
 #pragma unroll
@@ -611,8 +612,8 @@ ss_status ss_preference_loss(const float* logp, const float* ref_logp, const flo
   // a CTA per 4096 tokens of a pair of average length, up to the largest portable
   // cluster; pairs beyond the resident clusters take turns
   const int64_t each = n / std::max<int64_t>(pairs, 1);
-  while (p.cluster < kPrefMostCluster && each > 4096 * int64_t(p.cluster)) p.cluster = std::max(1, 2 * p.cluster);
-  p.cluster = std::max(1, p.cluster);
+  p.cluster = 1;
+  while (p.cluster < kPrefMostCluster && each > 4096 * int64_t(p.cluster)) p.cluster *= 2;
   const int64_t ctas = std::min<int64_t>(std::max<int64_t>(pairs, 1) * p.cluster, int64_t(nsm) * 4);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   StageTrace trace(s, "preference_loss");

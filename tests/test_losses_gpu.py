@@ -331,6 +331,25 @@ def test_distill_values_of_minus_infinity_and_garbage(tail):
     assert (got["dlogp"][gone] == 0).all()
 
 
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("which", ["teacher", "student"])
+def test_distill_nan_of_an_entry_that_counts(tail, which):
+    """It is in the row's sums: the loss is NaN, of that row alone, and so is the gradient
+    where those sums are its factor."""
+    s, t, _, _ = _distill_inputs(64, 10)
+    want = ss.distill_loss(s, t, tail=tail)
+    (t if which == "teacher" else s)[5, 3] = NAN
+    if which == "student" and tail:
+        t[5, 3] = -INF                  # its share of the tail counts all the same
+    got = ss.distill_loss(s, t, tail=tail)
+    assert got["loss"][5].isnan()
+    # (without a tail the student's values are no factor of the gradient)
+    assert got["dlogp"][5].isnan().all() or (which == "student" and not tail)
+    rest = torch.arange(64, device="cuda") != 5
+    for k in ("loss", "dlogp"):
+        assert torch.equal(got[k][rest], want[k][rest])
+
+
 def test_distill_without_a_teacher_value():
     """A row whose values are all -infinity is no distribution: nothing without a tail,
     everything in the tail with one."""
