@@ -55,8 +55,8 @@ size_t ss_logprob_workspace_size(int64_t T, int64_t V, int64_t D, int backward);
  *   head: NULL (plain) or cap and tau as for ss_forward_head; no FP8
  *   (SS_ERR_UNSUPPORTED).
  *   logp [T, K], lse [T] fp32 out.
- * A row of H that is not finite gives lse and logp that are not finite for that
- * token only. T = 0: nothing is enqueued.
+ * A row of H that is not finite touches that token's lse and logp only: a NaN in it
+ * makes them NaN, an infinity what the formulas give. T = 0: nothing is enqueued.
  */
 ss_status ss_logprob_forward(const uint16_t* H, const uint16_t* W, const int32_t* ids, int64_t K,
                              int64_t T, int64_t V, int64_t D, const ss_head* head, float* logp,
@@ -70,7 +70,9 @@ ss_status ss_logprob_forward(const uint16_t* H, const uint16_t* W, const int32_t
  *   dH = G W      dW = G^T H
  * The logits are computed again from H, W and lse; G is rounded once to bf16
  * for the two products, whose sums are held in fp32.
- *   dlogp [T, K] fp32; H, W, ids, logp, lse, head: as in the forward.
+ *   dlogp [T, K] fp32; H, W, ids, logp, lse, head: as in the forward, but for a
+ *   cap below 2^-6 (SS_ERR_UNSUPPORTED): the ids' z, from which their dz/ds is made,
+ *   is logp + lse here and has no digits left beside so small a cap.
  *   dH [T, D] bf16 out; dW [V, D] out of dw_dtype (ss_dtype), every row.
  *   accumulate: 0 -> dW is overwritten; 1 -> added to.
  * A token whose w are all 0 adds nothing to dW, and its row of dH is 0, whatever

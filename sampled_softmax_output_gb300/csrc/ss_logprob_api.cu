@@ -174,8 +174,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 // With several ids per token G's entries round independently: f = 1, G' = G.
 constexpr float kMostRounding = 0x1.6p-10f;
 
+// dz/ds of a chosen id, whose z is logp + lse: off by some 1e-6, beside a slope of up to
+// cap / (4 tau) by 4e-6 / cap of it, which must be little beside G's rounding.
+constexpr float kLeastCap = 0x1p-6f;
+
 __device__ __forceinline__ float head_slope(float z, const HeadCap& h) {
-  return h.cap > 0.f ? z * (h.cap - z) * h.icap_tau : 1.f;
+  return h.cap > 0.f ? z * ((h.cap - z) * h.icap_tau) : 1.f;
 }
 
 // K = 1: the largest |w| among tokens first, first + step, ... and whether an id is bad.
@@ -469,7 +473,7 @@ ss_status ss_logprob_backward(const float* dlogp, const uint16_t* H, const uint1
   if (K < 1 || (dw_dtype != SS_BF16 && dw_dtype != SS_FP32) ||
       (accumulate != 0 && accumulate != 1))
     return SS_ERR_INVALID;
-  if (K > SS_MAX_IDS) return SS_ERR_UNSUPPORTED;
+  if (K > SS_MAX_IDS || (p.cap > 0.f && p.cap < kLeastCap)) return SS_ERR_UNSUPPORTED;
   if (!usable(workspace, 16) || !usable(W, 16) || !usable(dW, 16) ||
       (T > 0 && (!usable(H, 16) || !usable(dH, 16) || !usable(ids, 4) || !usable(dlogp, 4) ||
                  !usable(logp, 4) || !usable(lse, 4))))

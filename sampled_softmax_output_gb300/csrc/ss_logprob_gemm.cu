@@ -72,7 +72,7 @@ struct EpiCoef {
           const uint64_t w = f32x2(rcp_approx(y0), rcp_approx(y1));
           f32x2_split(fma_f32x2(w, both(p.head.cap * kLog2e), noff), y0, y1);
           const uint64_t slope = mul_f32x2(mul_f32x2(w, fma_f32x2(w, both(-1.f), both(1.f))),
-                                           both(p.head.cap * p.head.cap * p.head.icap_tau));
+                                           both(p.head.cap * (p.head.cap * p.head.icap_tau)));
           f32x2_split(mul_f32x2(f32x2(ex2_approx(y0), ex2_approx(y1)), slope), g0, g1);
         } else {
           f32x2_split(fma_f32x2(x, f32x2(kLog2e, kLog2e), noff), y0, y1);

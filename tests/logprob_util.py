@@ -79,8 +79,11 @@ def grads64(dlogp, H, W, ids, logp, lse, cap=0.0, tau=1.0, fp32_dw=True):
     G = torch.where(touched, a * q_at, G) + onto
     eG = torch.where(touched, (K + 8) * F32 * 2 * (size * q_at + size), eG)
     if slope is not None:
-        # at the ids z comes back as logp + lse
+        # at the ids z comes back as logp + lse: the rounding of the difference that made
+        # logp and that of the sum, and |d slope / dz| = |cap - 2 z| / (cap tau) <= 1 / tau
         e_slope = (cap / (4 * tau)) * (8 * ACT + 4 * e / tau) + 1e-30
+        l_at = torch.where(touched, z - lse, 0.0)
+        e_slope = e_slope + 2 * F32 * (l_at.abs() + z.abs()) * touched / tau
         eG = eG * slope + (G.abs() + eG) * e_slope
         G = G * slope
     eG = eG + (BF + 8 * F32) * (G.abs() + eG)

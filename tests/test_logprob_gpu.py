@@ -128,6 +128,23 @@ def test_cap_above_the_plain_range():
     assert_within(dW, ref["dW"], "dW")
 
 
+def test_least_cap():
+    """The smallest cap that the backward pass takes."""
+    head = {"cap": 2.0 ** -6, "tau": 2.0 ** -8}
+    for K in (1, 3):
+        H, W, ids, dlogp = _inputs(100, 500, 128, K, std=2.0 ** -8)
+        ws = ss.logprob_workspace(100, 500, 128)
+        logp, lse = ss.logprobs(H, W, ids, ws, **head)
+        ref = logprobs64(H, W, ids.view(100, -1), **head)
+        assert_within(lse, ref["lse"], "lse")
+        assert_within(logp.view(100, -1), ref["logp"], "logp")
+        dH, dW = ss.logprobs_backward(dlogp, H, W, ids, logp, lse, ws, **head)
+        two = [t.view(100, -1) for t in (dlogp, ids, logp)]
+        ref = grads64(two[0], H, W, two[1], two[2], lse, **head)
+        assert_within(dH, ref["dH"], "dH")
+        assert_within(dW, ref["dW"], "dW")
+
+
 @pytest.mark.parametrize("std", [0.0, 60.0])
 def test_flat_and_peaked_softmax(std):
     H, W, ids, dlogp = _inputs(150, 600, 128, 1, std=std)

@@ -86,6 +86,7 @@ def test_logprob_backward_argument_errors():
     for k in ("dH", "dW"):
         assert _bwd(**{k: 0}) == INVALID and _bwd(**{k: FAKE + 8}) == INVALID, k
     assert _bwd(dlogp=0) == INVALID and _bwd(dlogp=FAKE + 1) == INVALID
+    assert _bwd(head=ss.Head(2.0 ** -6 * 0.99, 1.0, 0)) == UNSUPPORTED
     assert _bwd(dw=2) == INVALID and _bwd(dw=-1) == INVALID and _bwd(acc=2) == INVALID
     assert _bwd(T=0, dlogp=0, H=0, ids=0, logp=0, lse=0, dH=0, acc=1) == OK
 
