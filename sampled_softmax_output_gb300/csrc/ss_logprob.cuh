@@ -24,9 +24,10 @@ struct LogprobArgs {
 // = 2 ceil(V / 256) of them, for the kernel below.
 cudaError_t launch_bin_ids(const LogprobArgs& p, const int32_t* ids, int K, int bins,
                            uint32_t* sorted, uint16_t* bin_ends, cudaStream_t s);
-// part[c][t]: the largest logit of row t among columns 128 c to 128 c + 127 and the
-// sum of the exponentials above it, c < bins; (-inf, 0) past the end. z: the logits of
-// the sorted ids, place by place.
+// part[c][t] = (n, s): the sum of exp(z) of row t over columns 128 c to 128 c + 127 is
+// 2^n s, n an integer near its largest logit (so that no digit is lost in taking it off
+// or in joining partials), c < bins; (-inf, 0) past the end. z: the logits of the
+// sorted ids, place by place.
 cudaError_t launch_logprob_partials(const LogprobArgs& p, int K, const uint32_t* sorted,
                                     const uint16_t* bin_ends, float2* part, float* z,
                                     cudaStream_t s);

@@ -77,21 +77,34 @@ ss_status logprob_head(const ss_head* head, LogprobArgs* p) {
 
 // ------------------------------------------------------------- small kernels
 
-// lse[t] from the (max, sum) partials of n_parts column groups, and logp = z - lse: of
-// the sorted ids' logits z, or (sorted null) in the place of z = logp. A block takes 32
+// lse[t] from the partials (n, s) of n_parts column groups, and logp = z - lse: of the
+// sorted ids' logits z, or (sorted null) in the place of z = logp. A block takes 32
 // tokens: warp w folds the partials w, w + 32, ... of its lane's token, the warps' pairs
 // meet in shared memory. (16384 tokens, 394 partials: 52 MB in 25 us.)
 constexpr int kMergeWarps = 32;
 
+// 2^d for an integer d <= 0; 0 from -127 on
+__device__ __forceinline__ float power_of_two(float d) {
+  return __int_as_float((static_cast<int>(fmaxf(d, -127.f)) + 127) << 23);
+}
+
+// 2^M S += 2^m s
 __device__ __forceinline__ void fold(float& M, float& S, float m, float s) {
   if (m == -INFINITY && s == 0.f) return;  // nothing (a row of NaN has a sum of NaN)
-  if (m == M) {
-    S += s;
-    return;
-  }
   const float nm = fmaxf(M, m);
-  S = S * expf(M - nm) + s * expf(m - nm);
+  S = S * power_of_two(M - nm) + s * power_of_two(m - nm);
   M = nm;
+}
+
+// log(2^M S), from S's fraction in [3/4, 3/2) and with log(2) in two parts, so that the
+// result is rounded once, in the last addition
+__device__ __forceinline__ float log_of(float M, float S) {
+  if (!(S > 0.f && S < INFINITY)) return logf(S);  // (no sum is subnormal)
+  constexpr float kLn2 = 0.693147180559945309f;
+  constexpr float kLn2Lo = static_cast<float>(0.693147180559945309 - double(kLn2));
+  const int bits = __float_as_int(S), e = (bits - 0x3f400000) >> 23;
+  M += static_cast<float>(e);
+  return fmaf(M, kLn2, fmaf(M, kLn2Lo, logf(__int_as_float(bits - e * (1 << 23)))));
 }
 
 __global__ void __launch_bounds__(32 * kMergeWarps)
@@ -136,7 +149,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
       fold(m, s, m2, s2);
     }
     if (lane == 0) {
-      const float l = m + logf(s);
+      const float l = log_of(m, s);
       s_lse[warp] = l;
       if (t0 + warp < T) lse[t0 + warp] = l;
     }

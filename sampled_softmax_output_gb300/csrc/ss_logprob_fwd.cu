@@ -1,6 +1,6 @@
 // ss_logprob_fwd.cu -- the softmax partials of the head's log-probabilities over
 // the whole vocabulary: logits S = H W^T tile by tile (M = T, N = V, K = D) on CTA
-// pairs, of which only (max, sum of exponentials) per row and 128 columns leave
+// pairs, of which only a scaled sum of exponentials per row and 128 columns leaves
 // the chip.
 //
 // A log-probability is the difference of two numbers near 10, so the logits want
@@ -48,12 +48,13 @@ constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kHalf = kBN / 2;  // columns of a row per epilogue thread
 static_assert(kHalf == 128, "seven bits of a sorted id");
 constexpr int kMostBins = SS_MAX_V / kHalf;
+constexpr double kLog2eExact = 1.4426950408889634074;
 using L = Gemm2Smem<kBN, kStages, 0>;
 
 struct FwdArgs {
   int T, V, m_tiles, n_tiles, k_blocks, group_m;
   HeadCap head;
-  float2* part;  // [2 n_tiles][T]
+  float2* part;  // [2 n_tiles][T]: (n, s), 2^n s
   int K;
   const uint32_t* sorted;    // [groups][32 K]: column in its bin, row and k of each id
   const uint16_t* bin_ends;  // [groups][2 n_tiles]: where each bin's ids end
@@ -406,7 +407,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (lane < n) p.z[static_cast<int64_t>(t0) * p.K + i + lane] = kept;
         }
         if (CAP && p.head.cap <= kStoredCapMax) {
-          m = p.head.cap;  // no logit is above it, and exp(-cap) is a normal number
+          // no logit is above it, and exp(-cap) is a normal number
+          m = rintf(p.head.cap * kLog2e);
         } else {
           float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
@@ -416,10 +418,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             m0 = fmaxf(m0, x);
             m1 = fmaxf(m1, y);
           }
-          m = fmaxf(m0, m1);
+          m = rintf(fmaxf(m0, m1) * kLog2e);
         }
         // a row of -infinity alone (or a NaN) has no number to subtract
-        const float r2 = m > -INFINITY ? m * kLog2e : 0.f;
+        const float r2 = m > -INFINITY ? m : 0.f;
         const uint64_t k2 = f32x2(kLog2e, kLog2e), nr2 = f32x2(-r2, -r2);
         uint64_t s0 = f32x2(0.f, 0.f), s1 = s0;
 #pragma unroll
@@ -434,6 +436,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         f32x2_split(s0, a0, a1);
         f32x2_split(s1, a2, a3);
         s = (a0 + a1) + (a2 + a3);
+        // What shifts every token's sum the same way, and so adds up over a sequence:
+        // kLog2e is 1.93e-8 above log2(e), so that exp(z) came out as exp(z (1 + 1.3e-8))
+        // (1.2e-7 of it where z is 9), which is taken off at the mean of z log2(e), some
+        // 3.6 below the logarithm of the sum; and the hardware's exponential is 5.0e-8 too
+        // small on average (a million points). Log-probabilities of tokens drawn from the
+        // model are then off by 1e-8 on average, 9e-7 with neither this nor integers as
+        // the exponents (a cap of 30).
+        constexpr float kOver = static_cast<float>((double(kLog2e) - kLog2eExact) /
+                                                   (kLog2eExact * kLog2eExact));
+        const float mean = fmaxf(r2 + __log2f(s) - 3.6f, -1e6f);  // (s can be 0)
+        s = fmaf(s, fmaf(-kOver, mean, 5.0e-8f), s);
       }
       if (t < p.T) p.part[static_cast<size_t>(nt * 2 + cg) * p.T + t] = make_float2(m, s);
     }
@@ -578,7 +591,11 @@ __global__ void __launch_bounds__(kFewThreads) k_logprob_few(const FewArgs p) {
   if (threadIdx.x < p.T) {
     for (int k = 1; k < kFewThreads / 32; ++k)
       take_partial(s_part[k][threadIdx.x].x, s_part[k][threadIdx.x].y, m, s);
-    p.part[static_cast<int64_t>(blockIdx.x) * p.T + threadIdx.x] = make_float2(m, s);
+    // 2^n s, log2(e) in two parts
+    constexpr float kLog2eLo = static_cast<float>(kLog2eExact - double(kLog2e));
+    const float n = rintf(m * kLog2e);
+    if (m > -INFINITY) s *= exp2f(fmaf(m, kLog2eLo, fmaf(m, kLog2e, -n)));
+    p.part[static_cast<int64_t>(blockIdx.x) * p.T + threadIdx.x] = make_float2(n, s);
   }
 }
 

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import sampled_softmax_output_gb300 as ss
-from logprob_util import F64, assert_within, grads64, logprobs64
+from logprob_util import F64, assert_within, grads64, logits64, logprobs64
 
 pytestmark = pytest.mark.gpu
 BF16, F32T, I32 = torch.bfloat16, torch.float32, torch.int32
@@ -126,6 +126,23 @@ def test_cap_above_the_plain_range():
     ref = grads64(dlogp, H, W, ids, logp, lse, cap=200.0, tau=20.0)
     assert_within(dH, ref["dH"], "dH")
     assert_within(dW, ref["dW"], "dW")
+
+
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+def test_no_shift_of_sampled_tokens(cap):
+    """What is off by the same amount for every token adds up over a sequence. Each of
+    these log-probabilities is within 1.5e-6 (rms) of its value, their mean within 4 of
+    its own standard deviations, and the log-sum-exp's corrections leave some 3e-8."""
+    T, V, D = 4096, 4000, 128
+    H, W, _, _ = _inputs(T, V, D, 1)
+    z = logits64(H, W, **_head(cap))[0]
+    want = torch.log_softmax(z, 1)
+    gen = torch.Generator("cuda").manual_seed(5)
+    ids = torch.multinomial(want.exp(), 1, generator=gen)
+    logp, _ = _forward(H, W, ids.to(I32), cap)
+    off = logp.to(F64) - want.gather(1, ids)
+    assert off.std() < 1.5e-6
+    assert off.mean().abs() < 4 * 1.5e-6 / T ** 0.5 + 3e-8
 
 
 def test_least_cap():
