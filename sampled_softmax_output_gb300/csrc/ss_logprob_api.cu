@@ -180,10 +180,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 //   G' = c (P - Y) dz/ds,  dH = (|a| / |c|) (G' W),  dW = m (G'^T (f H)),  |a| = m f |c|
 // where f is a power of two, which leaves H exact, and 1 <= |c| < 2; tokens of
 // coefficient m have c = 1. Where that would round the entry at the id, c (1 - P)
-// dz/ds, by more than kMostRounding, f takes all of |a| / m and c is 1 too: H's own
-// rounding is as large but differs from element to element. (32 tokens of one pair:
-// dH and dW, as bf16, 3.0e-3 off without, 1.8e-3 with. 16384 tokens of a policy loss:
-// 2.4e-3 without, 2.2e-3 with, 2.5e-3 with f = |a| / m for every token.)
+// dz/ds, by more than kMostRounding, c is the number nearest 1 that makes it a bf16
+// number and f takes the rest: H's own rounding is as large but differs from element to
+// element. (32 tokens of one pair: dH and dW, as bf16, 3.0e-3 off without, 1.7e-3 and
+// 2.1e-3 with. 16384 tokens of a policy loss: 2.4e-3 without, 1.8e-3 and 2.1e-3 with.)
 // With several ids per token G's entries round independently: f = 1, G' = G.
 constexpr float kMostRounding = 0x1.6p-10f;
 
@@ -231,11 +231,14 @@ __device__ __forceinline__ void scale_coef(const CoefArgs& p, int64_t t, float t
     ft = __uint_as_float(__float_as_uint(x) & 0x7f800000u);
     if (!(ft > 0.f && ft <= 1.f)) ft = x;
     c = x > 0.f ? x / ft : 1.f;  // (beside an infinite coefficient x is 0)
-    const float g = -c * expm1f(l) * head_slope(z, p.head);
-    const float r = __uint_as_float(static_cast<uint32_t>(bf16_bits(g)) << 16);
-    if (x > 0.f && !(fabsf(r - g) <= kMostRounding * fabsf(g))) {
-      ft = x;
-      c = 1.f;
+    const float q = -expm1f(l) * head_slope(z, p.head), g = c * q;
+    const auto rounded = [](float v) {
+      return __uint_as_float(static_cast<uint32_t>(bf16_bits(v)) << 16);
+    };
+    if (x > 0.f && !(fabsf(rounded(g) - g) <= kMostRounding * fabsf(g))) {
+      c = rounded(q) / q;
+      if (!(c > 0.5f && c < 2.f)) c = 1.f;  // (q is no normal number)
+      ft = x / c;
     }
     rf = size / c;
     c = w > 0.f ? -c : c;
