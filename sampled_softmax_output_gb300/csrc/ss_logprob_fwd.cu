@@ -19,7 +19,7 @@
 // ids of each 32 tokens by the 128 columns they fall into; a warp, which holds those
 // columns of those tokens, looks up the few that are its own.
 //
-// T 16384, V 50304, D 768: 722 us, 1.75 PFLOP/s; T 8192, D 2048: 923 us, 1.83. The
+// T 16384, V 50304, D 768: 712 us, 1.78 PFLOP/s; T 8192, D 2048: 907 us, 1.86. The
 // tensor pipe is active in 74% of the cycles (T 4096, 1.88 GHz); the rest is the
 // runs' ends, where the MMAs wait for an accumulator.
 //
@@ -463,7 +463,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 //
 // One token or two (a served model's next position): W is read once, at memory's rate,
 // and the products run on the fp32 pipe beside it, where a tile of 256 tokens on the
-// tensor cores would be mostly empty (V 50304, D 768, one token: 18.7 us with the merge,
+// tensor cores would be mostly empty (V 50304, D 768, one token: 16.7 us with the merge,
 // 77 MB, where the tiles take 35; four tokens: 29 and 31, D 2048 64 and 58). A warp
 // takes kRows vocabulary rows at a time, each lane eight columns of every 256; the
 // tokens lie in shared memory. The ids' logits are more rows of the same kind, so that

@@ -128,6 +128,25 @@ def test_cap_above_the_plain_range():
     assert_within(dW, ref["dW"], "dW")
 
 
+def test_few_tokens_again_and_again():
+    """One workspace for one token and two in turn, after an id out of range too, and the
+    same bits each time."""
+    V, D = 50257, 128
+    H, W, ids, _ = _inputs(2, V, D, 5)
+    ws = ss.logprob_workspace(2, V, D, backward=False)
+    want = [_forward(H[:T], W, ids[:T].contiguous(), ws=ws) for T in (1, 2)]
+    bad = ids.clone()
+    bad[1, 3] = V
+    for _ in range(20):
+        for T in (1, 2):
+            logp, lse = ss.logprobs(H[:T], W, ids[:T], ws)
+            assert torch.equal(logp, want[T - 1][0]) and torch.equal(lse, want[T - 1][1])
+        ss.logprobs(H, W, bad, ws)
+        ss.logprobs(H, W, ids, ws)  # does nothing
+        assert ss.read_status(ws)[0] != 0
+        ws[:ss.WORKSPACE_HEADER_BYTES].zero_()
+
+
 @pytest.mark.parametrize("cap", [0.0, 30.0])
 def test_no_shift_of_sampled_tokens(cap):
     """What is off by the same amount for every token adds up over a sequence. Each of
