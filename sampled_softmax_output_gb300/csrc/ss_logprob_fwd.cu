@@ -20,7 +20,7 @@
 // columns of those tokens, looks up the few that are its own.
 //
 // T 16384, V 50304, D 768: 712 us, 1.78 PFLOP/s; T 8192, D 2048: 907 us, 1.86. The
-// tensor pipe is active in 74% of the cycles (T 4096, 1.88 GHz); the rest is the
+// tensor pipe is active in 74% of the cycles (T 4096, 1.90 GHz); the rest is the
 // runs' ends, where the MMAs wait for an accumulator.
 //
 // The protocol is that of ss_gemm2.cuh (pairs of CTAs on 256 x 256 tiles, warp 0
