@@ -41,9 +41,11 @@ cudaError_t launch_logprob_few(const LogprobArgs& p, int K, const int32_t* ids, 
 
 // ---- ss_logprob_gemm.cu
 
-// G[t, j] = bf16(coef[t] exp(z[t, j] - lse[t]) dz/ds), 0 where coef[t] = 0. G [T, ldG]
+// G[t, j] = bf16(coef[t] exp(z[t, j] - lse[t]) dz/ds), 0 where coef[t] = 0; but entry[t],
+// bf16, where j is ids[t] (ids null: nowhere). G [T, ldG]
 cudaError_t launch_logprob_g(const LogprobArgs& p, const float* coef, const float* lse,
-                             uint16_t* G, int64_t ldG, cudaStream_t s);
+                             const int32_t* ids, const uint32_t* entry, uint16_t* G, int64_t ldG,
+                             cudaStream_t s);
 
 // ---- ss_logprob_grads.cu
 

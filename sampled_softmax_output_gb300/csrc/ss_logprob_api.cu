@@ -217,21 +217,51 @@ struct CoefArgs {
   const int32_t* ids;
   const float *logp, *lse;
   HeadCap head;
-  float *coef, *f, *rowfac;
+  float* coef;
+  uint32_t* entry;
+  float* rowfac;
+  const uint16_t* H;
+  uint16_t* Hs;
+  int D;
 };
 
-// K = 1: coef[t] = c, with the sign of a; f[t] and rowfac[t] = |a| / |c|, 0 where a is.
-__device__ __forceinline__ void scale_coef(const CoefArgs& p, int64_t t, float top) {
+// Hs[t] = f H[t], a warp's work: 0 for f = 0 (not 0 times an infinity or a NaN of H)
+__device__ __forceinline__ void scale_row(const uint16_t* __restrict__ H,
+                                          uint16_t* __restrict__ Hs, int64_t t, int D, float f,
+                                          int lane) {
+  const uint4* src = reinterpret_cast<const uint4*>(H + t * D);
+  uint4* dst = reinterpret_cast<uint4*>(Hs + t * D);
+  for (int c = lane; c < D / 8; c += 32) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (f != 0.f) {
+      v = __ldg(src + c);
+      if (f != 1.f) {
+        uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[i] = pack_bf16x2(__uint_as_float(x[i] << 16) * f,
+                             __uint_as_float(x[i] & 0xffff0000u) * f);
+        v = make_uint4(x[0], x[1], x[2], x[3]);
+      }
+    }
+    dst[c] = v;
+  }
+}
+
+// K = 1, a warp for token t: coef[t] = c, with the sign of a; rowfac[t] = |a| / |c|, 0
+// where a is; entry[t], G's at the id as bf16; Hs[t] = f H[t].
+__device__ __forceinline__ void scale_coef(const CoefArgs& p, int64_t t, float top, int lane) {
   const float w = __ldg(p.ids + t) >= 0 ? __ldg(p.dlogp + t) : 0.f;
   const float l = __ldg(p.logp + t), z = l + __ldg(p.lse + t);
-  float c = 0.f, ft = 0.f, rf = 0.f;
+  float c = 0.f, ft = 0.f, rf = 0.f, g = 0.f;
   if (w != 0.f) {  // (a NaN too)
     const float size = fabsf(w), x = size / top;
     // the power of two below x; x itself where it is none or no normal number
     ft = __uint_as_float(__float_as_uint(x) & 0x7f800000u);
     if (!(ft > 0.f && ft <= 1.f)) ft = x;
     c = x > 0.f ? x / ft : 1.f;  // (beside an infinite coefficient x is 0)
-    const float q = -expm1f(l) * head_slope(z, p.head), g = c * q;
+    const float q = -expm1f(l) * head_slope(z, p.head);
+    g = c * q;
     const auto rounded = [](float v) {
       return __uint_as_float(static_cast<uint32_t>(bf16_bits(v)) << 16);
     };
@@ -239,18 +269,25 @@ __device__ __forceinline__ void scale_coef(const CoefArgs& p, int64_t t, float t
       c = rounded(q) / q;
       if (!(c > 0.5f && c < 2.f)) c = 1.f;  // (q is no normal number)
       ft = x / c;
+      g = c * q;
     }
     rf = size / c;
-    c = w > 0.f ? -c : c;
+    if (w > 0.f) c = -c;
+    else g = -g;
   }
-  p.coef[t] = c;
-  p.f[t] = ft;
-  p.rowfac[t] = rf;
+  if (lane == 0) {
+    p.coef[t] = c;
+    p.rowfac[t] = rf;
+    p.entry[t] = bf16_bits(g);
+  }
+  scale_row(p.H, p.Hs, t, p.D, ft, lane);
 }
 
-// Up to kOneBlockTokens in one block, which finds m and then scales; beyond, a kernel
-// for each (16384 tokens: 20 us in one block, 6 in two kernels).
-constexpr int kCoefThreads = 1024, kOneBlockTokens = 4096;
+// Up to kOneKernelTokens every block finds m by itself, from 8 bytes a token, and scales
+// its tokens; beyond, a kernel for each. (With the entries written over G and H scaled in
+// a kernel of their own behind G's, the backward pass of 256, 1024 and 4096 tokens took
+// 73, 167 and 556 us for 71, 164 and 552.)
+constexpr int kCoefThreads = 256, kOneKernelTokens = 4096;
 
 __global__ void __launch_bounds__(kCoefThreads)
     k_logprob_coef_one(const CoefArgs p, int T, int V, float* __restrict__ scale, int* status) {
@@ -266,11 +303,11 @@ __global__ void __launch_bounds__(kCoefThreads)
   if (bad) set_status(status, SS_ERR_TARGET_RANGE);
   if (lane == 0) s_top[warp] = top;
   __syncthreads();
-  top = s_top[lane];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (threadIdx.x == 0) *scale = top;
-  for (int64_t t = threadIdx.x; t < T; t += kCoefThreads) scale_coef(p, t, top);
+  for (int w = 0; w < kCoefThreads / 32; ++w) top = fmaxf(top, s_top[w]);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *scale = top;
+  const int step = static_cast<int>(gridDim.x) * (kCoefThreads / 32);
+  for (int t = static_cast<int>(blockIdx.x) * (kCoefThreads / 32) + warp; t < T; t += step)
+    scale_coef(p, t, top, lane);
 }
 
 // *scale, 0 before, as the bits of a number that is not negative
@@ -290,8 +327,8 @@ __global__ void __launch_bounds__(256) k_logprob_scale(const CoefArgs p, int T,
   pdl_enter();
   if (read_status(status) != 0) return;
   const float top = *scale;
-  for (int64_t t = blockIdx.x * int64_t(256) + threadIdx.x; t < T; t += int64_t(gridDim.x) * 256)
-    scale_coef(p, t, top);
+  for (int64_t t = blockIdx.x * int64_t(8) + threadIdx.x / 32; t < T; t += int64_t(gridDim.x) * 8)
+    scale_coef(p, t, top, threadIdx.x & 31);
 }
 
 // K > 1: coef[t] = -sum_k w[t, k], and f[t] = 1 or 0: whether any w is not 0. A warp
@@ -326,10 +363,9 @@ __global__ void __launch_bounds__(256) k_logprob_coef(const float* __restrict__ 
   }
 }
 
-// G'[t, ids[t, k]], in the place of what the product wrote there, and f H: 0 for
-// tokens whose w are all 0 (G's row is 0 too, but 0 times an infinity or a NaN of H
-// would not be). The sum of an entry is rounded once; of several equal ids the first
-// writes it. A warp per token.
+// K > 1: G[t, ids[t, k]], in the place of what the product wrote there, and f H. The sum
+// of an entry is rounded once; of several equal ids the first writes it. A warp per
+// token.
 __global__ void __launch_bounds__(256) k_logprob_patch(
     const float* __restrict__ dlogp, const int32_t* __restrict__ ids,
     const float* __restrict__ logp, const float* __restrict__ lse,
@@ -344,66 +380,40 @@ __global__ void __launch_bounds__(256) k_logprob_patch(
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int64_t step = static_cast<int64_t>(gridDim.x) * (blockDim.x / 32);
   for (int64_t t = blockIdx.x * static_cast<int64_t>(blockDim.x / 32) + warp; t < T; t += step) {
-    const float a = __ldg(coef + t), ft = __ldg(f + t);
-    if (K == 1) {
-      const int id = __ldg(ids + t);
-      if (lane == 0 && id >= 0 && id < V) {
-        const float l = __ldg(logp + t);
-        G[t * ldG + id] = a != 0.f ? bf16_bits(a * expm1f(l) *
-                                               head_slope(l + __ldg(lse + t), head))
-                                   : uint16_t(0);
-      }
-    } else {
-      const int K4 = (K + 3) / 4 * 4;
-      for (int k = lane; k < K4; k += 32) {
-        const int id = k < K ? __ldg(ids + t * K + k) : -1;
-        s_id[warp][k] = id < V ? id : -1;
-        s_w[warp][k] = id >= 0 ? __ldg(dlogp + t * K + k) : 0.f;
-      }
-      __syncwarp();
-      for (int k = lane; k < K; k += 32) {
-        const int id = s_id[warp][k];
-        if (id < 0) continue;
-        float w = s_w[warp][k];
-        int equal = 0;
-        for (int j = 0; j < K4; j += 4) {
-          const int4 v = *reinterpret_cast<const int4*>(&s_id[warp][j]);
-          equal += (v.x == id) + (v.y == id) + (v.z == id) + (v.w == id);
-        }
-        if (equal > 1) {  // rare: the sum of them all, written by the first
-          bool first = true;
-          w = 0.f;
-          for (int j = 0; j < K; ++j)
-            if (s_id[warp][j] == id) {
-              first = first && j >= k;
-              w += s_w[warp][j];
-            }
-          if (!first) continue;
-        }
-        const float l = __ldg(logp + t * K + k);
-        const float g = a != 0.f ? fmaf(a, expf(l), w) : w;
-        G[t * ldG + id] =
-            g != 0.f ? bf16_bits(g * head_slope(l + __ldg(lse + t), head)) : uint16_t(0);
-      }
-      __syncwarp();
+    const float a = __ldg(coef + t);
+    const int K4 = (K + 3) / 4 * 4;
+    for (int k = lane; k < K4; k += 32) {
+      const int id = k < K ? __ldg(ids + t * K + k) : -1;
+      s_id[warp][k] = id < V ? id : -1;
+      s_w[warp][k] = id >= 0 ? __ldg(dlogp + t * K + k) : 0.f;
     }
-    const uint4* src = reinterpret_cast<const uint4*>(H + t * D);
-    uint4* dst = reinterpret_cast<uint4*>(Hs + t * D);
-    for (int c = lane; c < D / 8; c += 32) {
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (ft != 0.f) {
-        v = __ldg(src + c);
-        if (ft != 1.f) {
-          uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            x[i] = pack_bf16x2(__uint_as_float(x[i] << 16) * ft,
-                               __uint_as_float(x[i] & 0xffff0000u) * ft);
-          v = make_uint4(x[0], x[1], x[2], x[3]);
-        }
+    __syncwarp();
+    for (int k = lane; k < K; k += 32) {
+      const int id = s_id[warp][k];
+      if (id < 0) continue;
+      float w = s_w[warp][k];
+      int equal = 0;
+      for (int j = 0; j < K4; j += 4) {
+        const int4 v = *reinterpret_cast<const int4*>(&s_id[warp][j]);
+        equal += (v.x == id) + (v.y == id) + (v.z == id) + (v.w == id);
       }
-      dst[c] = v;
+      if (equal > 1) {  // rare: the sum of them all, written by the first
+        bool first = true;
+        w = 0.f;
+        for (int j = 0; j < K; ++j)
+          if (s_id[warp][j] == id) {
+            first = first && j >= k;
+            w += s_w[warp][j];
+          }
+        if (!first) continue;
+      }
+      const float l = __ldg(logp + t * K + k);
+      const float g = a != 0.f ? fmaf(a, expf(l), w) : w;
+      G[t * ldG + id] =
+          g != 0.f ? bf16_bits(g * head_slope(l + __ldg(lse + t), head)) : uint16_t(0);
     }
+    __syncwarp();
+    scale_row(H, Hs, t, D, __ldg(f + t), lane);
   }
 }
 
@@ -512,7 +522,8 @@ ss_status ss_logprob_backward(const float* dlogp, const uint16_t* H, const uint1
   p.status = reinterpret_cast<int*>(ws);
   float* coef = reinterpret_cast<float*>(ws + L.coef);
   float* rowfac = reinterpret_cast<float*>(ws + L.rowfac);
-  float* f = reinterpret_cast<float*>(ws + L.f);
+  float* f = reinterpret_cast<float*>(ws + L.f);            // K > 1
+  uint32_t* entry = reinterpret_cast<uint32_t*>(ws + L.f);  // K = 1
   float* scale = reinterpret_cast<float*>(ws + kHdrScale);
   uint16_t* Hs = reinterpret_cast<uint16_t*>(ws + L.hs);
   uint16_t* G = reinterpret_cast<uint16_t*>(ws + L.g);
@@ -523,31 +534,31 @@ ss_status ss_logprob_backward(const float* dlogp, const uint16_t* H, const uint1
   cudaError_t e;
   {
     StageTrace trace(s, "logprob_coef");
-    const CoefArgs c{dlogp, ids, logp, lse, p.head, coef, f, rowfac};
-    const dim3 blocks(static_cast<unsigned>(std::min((T + 255) / 256, int64_t(p.num_sms) * 4)));
+    const CoefArgs c{dlogp, ids, logp, lse, p.head, coef, entry, rowfac, H, Hs, p.D};
     if (iK > 1) {
       e = launch_pdl(k_logprob_coef, dim3(grid), dim3(256), 0, s, dlogp, ids, iK, p.T, p.V, coef,
                      f, p.status);
-    } else if (T <= kOneBlockTokens) {
-      e = launch_pdl(k_logprob_coef_one, dim3(1), dim3(kCoefThreads), 0, s, c, p.T, p.V, scale,
+    } else if (T <= kOneKernelTokens) {
+      e = launch_pdl(k_logprob_coef_one, dim3(grid), dim3(kCoefThreads), 0, s, c, p.T, p.V, scale,
                      p.status);
     } else {
+      const dim3 blocks(static_cast<unsigned>(std::min((T + 255) / 256, int64_t(p.num_sms) * 4)));
       e = cudaMemsetAsync(scale, 0, sizeof *scale, s);
       if (e == cudaSuccess)
         e = launch_pdl(k_logprob_top, blocks, dim3(256), 0, s, c, p.T, p.V,
                        reinterpret_cast<uint32_t*>(scale), p.status);
       if (e == cudaSuccess)
-        e = launch_pdl(k_logprob_scale, blocks, dim3(256), 0, s, c, p.T,
+        e = launch_pdl(k_logprob_scale, dim3(grid), dim3(256), 0, s, c, p.T,
                        static_cast<const float*>(scale), p.status);
     }
   }
   if (e != cudaSuccess) return record_failure("launch k_logprob_coef", e);
   {
     StageTrace trace(s, "gemm_softmax_grad");
-    e = launch_logprob_g(p, coef, lse, G, L.ldG, s);
+    e = launch_logprob_g(p, coef, lse, iK == 1 ? ids : nullptr, entry, G, L.ldG, s);
   }
   if (e != cudaSuccess) return record_failure("launch gemm_softmax_grad", e);
-  {
+  if (iK > 1) {
     StageTrace trace(s, "logprob_patch");
     e = launch_pdl(k_logprob_patch, dim3(grid), dim3(256), 0, s, dlogp, ids, logp, lse, coef, f,
                    iK, p.T, p.V, p.D, p.head, H, Hs, G, L.ldG, p.status);
@@ -556,9 +567,8 @@ ss_status ss_logprob_backward(const float* dlogp, const uint16_t* H, const uint1
   {
     StageTrace trace(s, "gemm_grads");
     e = launch_logprob_grads(p, G, L.ldG, Hs, iK == 1 ? rowfac : nullptr,
-                             iK == 1 ? scale : nullptr,
-                             part, dH, dW,
-                             dw_dtype == SS_FP32, accumulate, s);
+                             iK == 1 ? scale : nullptr, part, dH, dW, dw_dtype == SS_FP32,
+                             accumulate, s);
   }
   return e == cudaSuccess ? SS_OK : record_failure("launch gemm_grads", e);
 }

@@ -9,9 +9,14 @@ namespace ss {
 
 namespace {
 
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(static_cast<uint16_t>(v)) : "memory");
+}
+
 // The logits of a tile become the rows a[t] exp(z - lse) dz/ds of G, a
 // coefficient of either sign for each row: exp(z - (lse - log|a|)) with the
-// sign put in afterwards. A row of coefficient 0 is 0 whatever its logits are.
+// sign put in afterwards. A row of coefficient 0 is 0 whatever its logits are. With one
+// id per token its entry, which is more than that, goes over it on the way out.
 // Two column groups of four warps, each with a 16 KB staging buffer that holds
 // a 64-column quarter in the swizzled layout of G's tensor map.
 template <bool CAP>
@@ -24,6 +29,8 @@ struct EpiCoef {
     int T, V;
     const float* coef;
     const float* lse;
+    const int32_t* ids;     // null: no entries of their own
+    const uint32_t* entry;  // bf16 at column ids[t]
     HeadCap head;
   };
   __device__ static void begin(const Params&, EpiState&) {}
@@ -44,6 +51,8 @@ struct EpiCoef {
     const uint32_t sgn = a < 0.f ? 0x80008000u : 0u;
     const float off2 = keep ? fmaf(__ldg(p.lse + t), kLog2e, -log2f(fabsf(a))) : 0.f;
     const int j0 = nt * BN;
+    const int own = valid && p.ids ? __ldg(p.ids + t) - j0 : -1;  // its column of the tile
+    const uint32_t entry = own >= 0 && own < BN ? __ldg(p.entry + t) : 0u;
     const int ncols = min(BN, p.V - j0);
     const uint32_t r7 = static_cast<uint32_t>(row & 7);
     const uint32_t buf = es.stage + static_cast<uint32_t>(cg) * 16384u;
@@ -87,6 +96,10 @@ struct EpiCoef {
         st_shared_v4(rowbase + ((ci ^ r7) << 4), pk[4 * w], pk[4 * w + 1], pk[4 * w + 2],
                      pk[4 * w + 3]);
       }
+      if (own >= jc && own < jc + 32) {
+        const uint32_t c = static_cast<uint32_t>(h * 32 + own - jc);
+        st_shared_u16(rowbase + (((c >> 3) ^ r7) << 4) + (c & 7u) * 2u, entry);
+      }
       if (h == 1 || jc + 32 >= ncols) {  // the quarter is complete: store it
         fence_proxy_async_smem();
         named_bar_sync(bar, 128);
@@ -106,8 +119,9 @@ struct EpiCoef {
 constexpr int kGroupRows = 8192;
 
 template <bool CAP>
-cudaError_t coef_gemm(const LogprobArgs& p, const float* coef, const float* lse, uint16_t* G,
-                      int64_t ldG, cudaStream_t s) {
+cudaError_t coef_gemm(const LogprobArgs& p, const float* coef, const float* lse,
+                      const int32_t* ids, const uint32_t* entry, uint16_t* G, int64_t ldG,
+                      cudaStream_t s) {
   CUtensorMap tH, tW;
   typename EpiCoef<CAP>::Params ep;
   const uint64_t row = static_cast<uint64_t>(p.D) * 2;
@@ -121,6 +135,8 @@ cudaError_t coef_gemm(const LogprobArgs& p, const float* coef, const float* lse,
   ep.V = p.V;
   ep.coef = coef;
   ep.lse = lse;
+  ep.ids = ids;
+  ep.entry = entry;
   ep.head = p.head;
   if (pairs) {
     GemmShape shp{(p.T + 2 * BM - 1) / (2 * BM), n_tiles, p.D / BK, 0, 0, nullptr,
@@ -136,9 +152,10 @@ cudaError_t coef_gemm(const LogprobArgs& p, const float* coef, const float* lse,
 }  // namespace
 
 cudaError_t launch_logprob_g(const LogprobArgs& p, const float* coef, const float* lse,
-                             uint16_t* G, int64_t ldG, cudaStream_t s) {
-  return p.cap > 0.f ? coef_gemm<true>(p, coef, lse, G, ldG, s)
-                     : coef_gemm<false>(p, coef, lse, G, ldG, s);
+                             const int32_t* ids, const uint32_t* entry, uint16_t* G, int64_t ldG,
+                             cudaStream_t s) {
+  return p.cap > 0.f ? coef_gemm<true>(p, coef, lse, ids, entry, G, ldG, s)
+                     : coef_gemm<false>(p, coef, lse, ids, entry, G, ldG, s);
 }
 
 }  // namespace ss
