@@ -526,6 +526,7 @@ __device__ __forceinline__ void rows_dot(const FewArgs& p, const uint4* h, const
 
 // (m, s) and the logit z
 __device__ __forceinline__ void take_logit(float z, float& m, float& s) {
+  if (z == -INFINITY) return;  // adds nothing, and leaves no number to subtract if it is first
   const float top = fmaxf(m, z);
   // (the first logit: exp(-inf) = 0; a NaN stays in the sum)
   s = top > -INFINITY ? s * expf(m - top) + expf(z - top) : s + z;
