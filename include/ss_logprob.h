@@ -56,7 +56,10 @@ size_t ss_logprob_workspace_size(int64_t T, int64_t V, int64_t D, int backward);
  *   (SS_ERR_UNSUPPORTED).
  *   logp [T, K], lse [T] fp32 out.
  * A row of H that is not finite touches that token's lse and logp only: a NaN in it
- * makes them NaN, an infinity what the formulas give. T = 0: nothing is enqueued.
+ * makes them NaN, an infinity what the formulas give. A logit of -infinity adds nothing
+ * (its logp is -infinity); one of +infinity makes lse +infinity, the finite logits' logp
+ * -infinity and its own NaN, and a NaN among the logits makes them all NaN. T = 0: nothing
+ * is enqueued.
  */
 ss_status ss_logprob_forward(const uint16_t* H, const uint16_t* W, const int32_t* ids, int64_t K,
                              int64_t T, int64_t V, int64_t D, const ss_head* head, float* logp,

@@ -28,6 +28,7 @@
 // accumulators alternate between runs instead of tiles. A tile's exponentials run
 // beside the next tile's first runs, as its sums are in registers by then.
 #include <algorithm>
+#include <limits>
 
 #include "ss_gemm.cuh"
 #include "ss_gemm2.cuh"
@@ -49,6 +50,8 @@ constexpr int kHalf = kBN / 2;  // columns of a row per epilogue thread
 static_assert(kHalf == 128, "seven bits of a sorted id");
 constexpr int kMostBins = SS_MAX_V / kHalf;
 constexpr double kLog2eExact = 1.4426950408889634074;
+// the exponent of a sum that is infinite: a number, so that differences of it are too
+constexpr float kMostExponent = std::numeric_limits<float>::max();
 using L = Gemm2Smem<kBN, kStages, 0>;
 
 struct FwdArgs {
@@ -420,8 +423,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           m = rintf(fmaxf(m0, m1) * kLog2e);
         }
-        // a row of -infinity alone (or a NaN) has no number to subtract
-        const float r2 = m > -INFINITY ? m : 0.f;
+        // a row of -infinity alone, or of NaN, and one with an infinity have no number to
+        // subtract; the sum of the latter is infinite, or a NaN
+        const float r2 = fabsf(m) < INFINITY ? m : 0.f;
         const uint64_t k2 = f32x2(kLog2e, kLog2e), nr2 = f32x2(-r2, -r2);
         uint64_t s0 = f32x2(0.f, 0.f), s1 = s0;
 #pragma unroll
@@ -448,7 +452,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const float mean = fmaxf(r2 + __log2f(s) - 3.6f, -1e6f);  // (s can be 0)
         s = fmaf(s, fmaf(-kOver, mean, 5.0e-8f), s);
       }
-      if (t < p.T) p.part[static_cast<size_t>(nt * 2 + cg) * p.T + t] = make_float2(m, s);
+      if (t < p.T)
+        p.part[static_cast<size_t>(nt * 2 + cg) * p.T + t] = make_float2(fminf(m, kMostExponent), s);
     }
   }
   __syncthreads();
@@ -528,14 +533,14 @@ __device__ __forceinline__ void rows_dot(const FewArgs& p, const uint4* h, const
 __device__ __forceinline__ void take_logit(float z, float& m, float& s) {
   if (z == -INFINITY) return;  // adds nothing, and leaves no number to subtract if it is first
   const float top = fmaxf(m, z);
-  // (the first logit: exp(-inf) = 0; a NaN stays in the sum)
-  s = top > -INFINITY ? s * expf(m - top) + expf(z - top) : s + z;
+  // (the first logit: exp(-inf) = 0; a NaN stays in the sum; an infinity makes it infinite)
+  s = fabsf(top) < INFINITY ? s * expf(m - top) + expf(z - top) : s + z;
   m = top;
 }
 __device__ __forceinline__ void take_partial(float om, float os, float& m, float& s) {
   if (om == -INFINITY && os == 0.f) return;
   const float top = fmaxf(m, om);
-  s = s * expf(m - top) + os * expf(om - top);
+  s = top < INFINITY ? s * expf(m - top) + os * expf(om - top) : s + os;
   m = top;
 }
 
@@ -594,8 +599,8 @@ __global__ void __launch_bounds__(kFewThreads) k_logprob_few(const FewArgs p) {
       take_partial(s_part[k][threadIdx.x].x, s_part[k][threadIdx.x].y, m, s);
     // 2^n s, log2(e) in two parts
     constexpr float kLog2eLo = static_cast<float>(kLog2eExact - double(kLog2e));
-    const float n = rintf(m * kLog2e);
-    if (m > -INFINITY) s *= exp2f(fmaf(m, kLog2eLo, fmaf(m, kLog2e, -n)));
+    const float n = fminf(rintf(m * kLog2e), kMostExponent);
+    if (fabsf(m) < INFINITY) s *= exp2f(fmaf(m, kLog2eLo, fmaf(m, kLog2e, -n)));
     p.part[static_cast<int64_t>(blockIdx.x) * p.T + threadIdx.x] = make_float2(n, s);
   }
 }
