@@ -59,7 +59,7 @@ size_t ss_logprob_workspace_size(int64_t T, int64_t V, int64_t D, int backward);
  * makes them NaN, an infinity what the formulas give. A logit of -infinity adds nothing
  * (its logp is -infinity); one of +infinity makes lse +infinity, the finite logits' logp
  * -infinity and its own NaN, and a NaN among the logits makes them all NaN. T = 0: nothing
- * is enqueued.
+ * is enqueued. Logits up to 2^127 in magnitude have their lse, to fp32's digits of them.
  */
 ss_status ss_logprob_forward(const uint16_t* H, const uint16_t* W, const int32_t* ids, int64_t K,
                              int64_t T, int64_t V, int64_t D, const ss_head* head, float* logp,

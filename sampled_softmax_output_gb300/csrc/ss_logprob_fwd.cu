@@ -52,6 +52,9 @@ constexpr int kMostBins = SS_MAX_V / kHalf;
 constexpr double kLog2eExact = 1.4426950408889634074;
 // the exponent of a sum that is infinite: a number, so that differences of it are too
 constexpr float kMostExponent = std::numeric_limits<float>::max();
+// From this exponent on, what rounding it leaves of the largest logit is no less than what
+// fp32 leaves of the log-sum-exp, and can be hundreds: the logit itself is subtracted.
+constexpr float kFar = 0x1p24f;
 using L = Gemm2Smem<kBN, kStages, 0>;
 
 struct FwdArgs {
@@ -409,6 +412,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           if (lane < n) p.z[static_cast<int64_t>(t0) * p.K + i + lane] = kept;
         }
+        bool far = false;
         if (CAP && p.head.cap <= kStoredCapMax) {
           // no logit is above it, and exp(-cap) is a normal number
           m = rintf(p.head.cap * kLog2e);
@@ -421,11 +425,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             m0 = fmaxf(m0, x);
             m1 = fmaxf(m1, y);
           }
-          m = rintf(fmaxf(m0, m1) * kLog2e);
+          const float top = fmaxf(m0, m1);
+          m = rintf(top * kLog2e);
+          far = fabsf(m) >= kFar && fabsf(top) < INFINITY;
+          if (__any_sync(0xffffffffu, far)) {
+            const uint64_t off = far ? f32x2(-top, -top) : f32x2(0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kHalf / 2; ++k) acc[k] = add_f32x2(acc[k], off);
+          }
         }
         // a row of -infinity alone, or of NaN, and one with an infinity have no number to
         // subtract; the sum of the latter is infinite, or a NaN
-        const float r2 = fabsf(m) < INFINITY ? m : 0.f;
+        const float r2 = fabsf(m) < INFINITY && !far ? m : 0.f;
         const uint64_t k2 = f32x2(kLog2e, kLog2e), nr2 = f32x2(-r2, -r2);
         uint64_t s0 = f32x2(0.f, 0.f), s1 = s0;
 #pragma unroll
@@ -600,7 +611,7 @@ __global__ void __launch_bounds__(kFewThreads) k_logprob_few(const FewArgs p) {
     // 2^n s, log2(e) in two parts
     constexpr float kLog2eLo = static_cast<float>(kLog2eExact - double(kLog2e));
     const float n = fminf(rintf(m * kLog2e), kMostExponent);
-    if (fabsf(m) < INFINITY) s *= exp2f(fmaf(m, kLog2eLo, fmaf(m, kLog2e, -n)));
+    if (fabsf(n) < kFar) s *= exp2f(fmaf(m, kLog2eLo, fmaf(m, kLog2e, -n)));
     p.part[static_cast<int64_t>(blockIdx.x) * p.T + threadIdx.x] = make_float2(n, s);
   }
 }

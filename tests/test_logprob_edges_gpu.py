@@ -110,3 +110,15 @@ def test_a_row_with_an_infinity_under_a_cap(T, cap):
     assert ((logp[T - 1].to(F64) - (z[ids[T - 1].long()] - want)).abs()
             <= 2 * tol + 2 * F32 * cap).all()
 
+
+@pytest.mark.parametrize("T", [1, 2, 3, 130])
+@pytest.mark.parametrize("log_size", [20, 27, 32, 33, 34, 90, 120])
+def test_large_finite_logits(T, log_size):
+    """However large the logits are, a finite sum of them is a finite number: the largest
+    logit, to fp32's digits of it."""
+    H, W, ids = _inputs(T, 300, seed=4)
+    W = (W.float() * 2.0 ** log_size).to(BF16)
+    logp, lse = ss.logprobs(H, W, ids, ss.logprob_workspace(T, 300, 128))
+    ref = logprobs64(H, W, ids)
+    assert_within(lse, ref["lse"], "lse")
+    assert_within(logp, ref["logp"], "logp")
