@@ -498,12 +498,13 @@ __global__ void __launch_bounds__(256, 5) k_distill_loss(const DistillArgs p) {
 #pragma unroll
       for (int o = 1; o < LANES; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       // sum of exp(x - top); and, with log p = x - top - log(sum), of exp(x - top)
-      // times (x - top - l), from which the loss is made
+      // times (x - top - l), from which the loss is made. Where no value is a number above
+      // -infinity, top is -infinity: -infinity counts as 0 there too, a NaN stays one
       float sum = 0.f, part = 0.f, pr[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float d = x[i] - top;
-        pr[i] = here[i] && top > -INFINITY ? expf(d) : 0.f;
+        pr[i] = here[i] && x[i] != -INFINITY ? expf(d) : 0.f;
         sum += pr[i];
         if (pr[i] > 0.f) part += pr[i] * (d - l[i]);
       }

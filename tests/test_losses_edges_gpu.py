@@ -1,0 +1,47 @@
+"""The losses of log-probabilities where a term has no weight or a value is no number,
+infinite or near its limit."""
+import pytest
+import torch
+
+import sampled_softmax_output_gb300 as ss
+
+pytestmark = pytest.mark.gpu
+I32 = torch.int32
+NAN, INF = float("nan"), float("inf")
+
+
+def _gen(seed):
+    return torch.Generator("cuda").manual_seed(seed)
+
+
+def _policy_inputs(n, seed=0):
+    g = _gen(seed)
+    logp = -torch.randn(n, generator=g, device="cuda").exp()
+    old = logp - 0.1 * torch.randn(n, generator=g, device="cuda")
+    return logp, old, torch.randn(n, generator=g, device="cuda")
+
+
+# ------------------------------------------------------------ distillation
+
+@pytest.mark.parametrize("K", [1, 2, 7, 33, 128])
+@pytest.mark.parametrize("rest", ["nothing", "-infinity", "absent"])
+def test_distill_row_without_any_number(K, rest):
+    """The teacher's values that count are NaN and nothing else, or -infinity beside it:
+    a NaN, not a loss of 0; of that row alone."""
+    g = _gen(K)
+    s, t = (torch.log_softmax(torch.randn(9, K + 1, generator=g, device="cuda"), 1)[:, :K]
+            .contiguous() for _ in range(2))
+    ids = torch.arange(K, device="cuda", dtype=I32).repeat(9, 1)
+    want = ss.distill_loss(s, t, ids)
+    t[4] = NAN
+    if rest == "-infinity":
+        t[4, 1:] = -INF
+    elif rest == "absent":
+        ids[4, 1:] = -1
+    got = ss.distill_loss(s, t, ids)
+    assert got["loss"][4].isnan()
+    here = ids[4] >= 0
+    assert got["dlogp"][4][here].isnan().all() and (got["dlogp"][4][~here] == 0).all()
+    others = torch.arange(9, device="cuda") != 4
+    for k in ("loss", "dlogp"):
+        assert torch.equal(got[k][others], want[k][others])
