@@ -92,7 +92,7 @@ ss_status ss_logprob_backward(const float* dlogp, const uint16_t* H, const uint1
 /*
  * The clipped policy loss of n tokens with a KL term to a reference policy. With
  * r = exp(logp - old_logp), A the advantage, d = ref_logp - logp, m the weight:
- *   kl   = exp(d) - d - 1
+ *   kl   = exp(d) - d - 1  (infinity where d is +infinity: a token the policy rules out)
  *   loss = m (-min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl_coef kl)
  *   dlogp = scale d loss / d logp
  * (the gradient of the first term is -r A where r A is the smaller or both are

@@ -68,7 +68,7 @@ __device__ __forceinline__ PolicyOut policy_token(const PolicyArgs& p, float log
   float loss = -gain, d_loss = -slope;
   if (has_ref) {
     const float d = ref - logp, e = expm1f(d);
-    o.kl = e - d;
+    o.kl = e < INFINITY ? e - d : e;  // (not inf - inf)
     loss = fmaf(p.kl_coef, o.kl, loss);
     d_loss = fmaf(-p.kl_coef, e, d_loss);
   }

@@ -45,3 +45,16 @@ def test_distill_row_without_any_number(K, rest):
     others = torch.arange(9, device="cuda") != 4
     for k in ("loss", "dlogp"):
         assert torch.equal(got[k][others], want[k][others])
+
+
+# ------------------------------------------------------------------ policy
+
+def test_policy_kl_of_an_impossible_token():
+    """A token that the policy gives no probability at all and the reference some: its KL
+    is infinite, not a NaN."""
+    logp = torch.tensor([-INF, -1.0, -INF], device="cuda")
+    ref = torch.tensor([-2.0, -2.0, 1e30], device="cuda")
+    A = torch.zeros(3, device="cuda")
+    out = ss.policy_loss(logp, torch.full_like(logp, -1.0), A, ref_logp=ref, kl=0.1)
+    assert out["kl"][0] == INF and out["kl"][2] == INF and out["kl"][1].isfinite()
+    assert out["loss"][0] == INF and out["dlogp"][0] == -INF
