@@ -97,7 +97,8 @@ ss_status ss_logprob_backward(const float* dlogp, const uint16_t* H, const uint1
  *   dlogp = scale d loss / d logp
  * (the gradient of the first term is -r A where r A is the smaller or both are
  * equal, else 0). Where m = 0 the outputs are 0, and where A = 0 the first term
- * is, whatever the other inputs hold there.
+ * is, whatever the other inputs hold there; with kl_coef = 0 the loss and dlogp are
+ * the same as without ref_logp, whatever that holds.
  *   logp, old_logp, advantage [n] fp32; ref_logp [n] or NULL (no KL term; then
  *   kl_coef must be 0); weight [n] or NULL (1 everywhere).
  *   clip_low in [0, 1], clip_high >= 0 (infinity: no clipping on that side);

@@ -69,8 +69,10 @@ __device__ __forceinline__ PolicyOut policy_token(const PolicyArgs& p, float log
   if (has_ref) {
     const float d = ref - logp, e = expm1f(d);
     o.kl = e < INFINITY ? e - d : e;  // (not inf - inf)
-    loss = fmaf(p.kl_coef, o.kl, loss);
-    d_loss = fmaf(-p.kl_coef, e, d_loss);
+    if (p.kl_coef != 0.f) {  // (0 times an infinite term is none)
+      loss = fmaf(p.kl_coef, o.kl, loss);
+      d_loss = fmaf(-p.kl_coef, e, d_loss);
+    }
   }
   o.loss = m * loss;
   o.dlogp = p.scale * (m * d_loss);

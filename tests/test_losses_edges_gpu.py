@@ -1,5 +1,7 @@
 """The losses of log-probabilities where a term has no weight or a value is no number,
 infinite or near its limit."""
+import math
+
 import pytest
 import torch
 
@@ -58,3 +60,17 @@ def test_policy_kl_of_an_impossible_token():
     out = ss.policy_loss(logp, torch.full_like(logp, -1.0), A, ref_logp=ref, kl=0.1)
     assert out["kl"][0] == INF and out["kl"][2] == INF and out["kl"][1].isfinite()
     assert out["loss"][0] == INF and out["dlogp"][0] == -INF
+
+
+@pytest.mark.parametrize("ref", [-INF, INF, NAN, 100.0, -5000.0])
+def test_policy_reference_of_no_weight(ref):
+    """kl = 0 with a reference: its KL is written, and touches neither loss nor gradient,
+    whatever it is."""
+    logp, old, A = _policy_inputs(103)
+    plain = ss.policy_loss(logp, old, A)
+    far = logp + ref
+    out = ss.policy_loss(logp, old, A, ref_logp=far, kl=0.0)
+    assert torch.equal(out["loss"], plain["loss"])
+    assert torch.equal(out["dlogp"], plain["dlogp"])
+    if not math.isnan(ref):
+        assert (out["kl"] > 90).all()
