@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import sampled_softmax_output_gb300 as ss
+from logprob_util import F32, F64, assert_within
 
 pytestmark = pytest.mark.gpu
 I32 = torch.int32
@@ -74,3 +75,28 @@ def test_policy_reference_of_no_weight(ref):
     assert torch.equal(out["dlogp"], plain["dlogp"])
     if not math.isnan(ref):
         assert (out["kl"] > 90).all()
+
+
+def test_policy_kl_of_a_near_reference():
+    """exp(d) - d - 1 is d^2 / 2 near 0: all its digits are there, and it is never negative.
+    The difference d of the two is exact here; 12 half steps of the KL: below |d| = 1/2
+    some 8 roundings of its series, above 1 step of expm1 (2 |expm1(d)| / kl <= 8.8 half
+    steps) and the subtraction's."""
+    g = _gen(5)
+    n = 20001
+    size = torch.logspace(-7, 1, n, device="cuda")
+    sign = (torch.rand(n, generator=g, device="cuda") < 0.5).float() * 2 - 1
+    logp = torch.full((n,), -1.0, device="cuda")
+    # (both on one grid of 2^-23, so that their difference is exact up to 2)
+    d = torch.where(size < 2, torch.round(sign * size * 2.0 ** 23) * 2.0 ** -23, 0.0)
+    ref = torch.where(size < 2, logp + d, logp + torch.round(sign * size))
+    old, A = logp.clone(), torch.zeros(n, device="cuda")
+    out = ss.policy_loss(logp, old, A, ref_logp=ref, kl=0.5)
+    x = ref.to(F64) - logp.to(F64)
+    # (64 bits lose 2e-16 / |d| of it themselves: 2e-9 at 1e-7)
+    want = torch.expm1(x) - x
+    assert (out["kl"] >= 0).all() and (out["kl"][x != 0] > 0).all()
+    assert_within(out["kl"], (want, 12 * F32 * want), "kl")
+    assert_within(out["loss"], (0.5 * want, 13 * F32 * 0.5 * want), "loss")
+    same = ss.policy_loss(logp, old, A, ref_logp=logp, kl=0.5)
+    assert (same["kl"] == 0).all() and (same["dlogp"] == 0).all()
