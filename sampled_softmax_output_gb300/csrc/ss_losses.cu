@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kPrefThreads, 6) k_preference_loss(const Prefe
       } else if (p.kind == SS_PREF_HINGE) {
         loss = fmaxf(0.f, 1.f - h);
         slope = h < 1.f ? -p.beta : 0.f;
-        if (isnan(h)) loss = h;
+        if (isnan(h)) loss = slope = h;
       } else {
         const Pair d = pair_add(x, Pair{-0.5f / p.beta, 0.f});
         const float df = d.hi + d.lo;

@@ -100,3 +100,19 @@ def test_policy_kl_of_a_near_reference():
     assert_within(out["loss"], (0.5 * want, 13 * F32 * 0.5 * want), "loss")
     same = ss.policy_loss(logp, old, A, ref_logp=logp, kl=0.5)
     assert (same["kl"] == 0).all() and (same["dlogp"] == 0).all()
+
+
+# -------------------------------------------------------------- preference
+
+@pytest.mark.parametrize("kind", ["sigmoid", "hinge", "ipo"])
+def test_preference_gradient_of_no_number(kind):
+    """A NaN that counts is in its pair's loss and gradient, and in no other's."""
+    logp = -torch.rand(40, generator=_gen(6), device="cuda")
+    at = torch.tensor([0, 9, 20, 27, 40], dtype=I32, device="cuda")
+    ws = ss.logprob_workspace(0, 1, 64)
+    want = ss.preference_loss(logp, at, ws, kind=kind)
+    logp[13] = NAN
+    got = ss.preference_loss(logp, at, ws, kind=kind)
+    assert got["loss"][0].isnan() and got["dlogp"][:20].isnan().all()
+    assert torch.equal(got["loss"][1], want["loss"][1])
+    assert torch.equal(got["dlogp"][20:], want["dlogp"][20:])
