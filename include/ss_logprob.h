@@ -132,8 +132,9 @@ typedef enum ss_preference {
  *   logp [n] fp32; ref_logp [n] or NULL (0 everywhere); weight [n] or NULL (1).
  *   Tokens of weight 0 add nothing, whatever logp and ref_logp hold there.
  *   offsets [2 pairs + 1] int32, not decreasing, in [0, n]; a pair whose offsets
- *   are not sets SS_ERR_INDEX in the workspace's status word, its loss and
- *   rewards are NaN, and dlogp is unspecified.
+ *   are not sets SS_ERR_INDEX in the workspace's status word, and its loss and
+ *   rewards are NaN. The other pairs have theirs, and their tokens' dlogp, if their
+ *   own offsets, taken together, do not decrease; dlogp is unspecified elsewhere.
  *   smoothing (e) in [0, 0.5], 0 but for SS_PREF_SIGMOID; beta > 0.
  *   loss [pairs], reward [2 pairs], dlogp [n] out; dlogp may be logp or ref_logp.
  * Sums are held in pairs of fp32 numbers (48 bits), joined in a fixed order. 0 <= n

@@ -209,9 +209,12 @@ __global__ void __launch_bounds__(kPrefThreads, 6) k_preference_loss(const Prefe
   const int me = rank * kPrefThreads + static_cast<int>(threadIdx.x);
   const int threads = size * kPrefThreads;
   const int clusters = static_cast<int>(gridDim.x) / size;
+  auto in_order = [&](const int (&o)[3]) {
+    return o[0] >= 0 && o[1] >= o[0] && o[2] >= o[1] && o[2] <= p.n;
+  };
   for (int pair = static_cast<int>(blockIdx.x) / size; pair < p.pairs; pair += clusters) {
     const int o[3] = {p.offsets[2 * pair], p.offsets[2 * pair + 1], p.offsets[2 * pair + 2]};
-    if (o[0] < 0 || o[1] < o[0] || o[2] < o[1] || o[2] > p.n) {  // the same for all CTAs
+    if (!in_order(o)) {  // the same for all CTAs
       if (threadIdx.x == 0 && rank == 0) {
         set_status(p.status, SS_ERR_INDEX);
         p.loss[pair] = p.reward[2 * pair] = p.reward[2 * pair + 1] = NAN;
@@ -323,10 +326,17 @@ __global__ void __launch_bounds__(kPrefThreads, 6) k_preference_loss(const Prefe
     if (size > 1) cluster_sync_all();
     else __syncthreads();
   }
-  // what lies outside every sequence
-  const int64_t begin = p.pairs > 0 ? min(max(p.offsets[0], 0), p.n) : p.n;
-  const int64_t end = p.pairs > 0 ? min(max(p.offsets[2 * p.pairs], static_cast<int>(begin)), p.n)
-                                  : p.n;
+  // What lies outside every sequence. The first or last offset of a pair that is bad says
+  // nothing of where that is: other pairs' tokens may lie beyond it.
+  int64_t begin = p.n, end = p.n;
+  if (p.pairs > 0) {
+    const int32_t* last = p.offsets + 2 * (static_cast<int64_t>(p.pairs) - 1);
+    const int a[3] = {p.offsets[0], p.offsets[1], p.offsets[2]};
+    const int b[3] = {last[0], last[1], last[2]};
+    begin = in_order(a) ? a[0] : 0;
+    end = in_order(b) ? b[2] : p.n;
+    if (begin > end) begin = 0, end = p.n;
+  }
   const int64_t outside = begin + (p.n - end);
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPrefThreads + threadIdx.x; i < outside;
        i += static_cast<int64_t>(gridDim.x) * kPrefThreads)

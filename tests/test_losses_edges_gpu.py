@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import sampled_softmax_output_gb300 as ss
-from logprob_util import F32, F64, assert_within
+from logprob_util import F32, F64, assert_within, preference64
 
 pytestmark = pytest.mark.gpu
 I32 = torch.int32
@@ -116,3 +116,56 @@ def test_preference_gradient_of_no_number(kind):
     assert got["loss"][0].isnan() and got["dlogp"][:20].isnan().all()
     assert torch.equal(got["loss"][1], want["loss"][1])
     assert torch.equal(got["dlogp"][20:], want["dlogp"][20:])
+
+
+def _preference_call(logp, at, dlogp, ws):
+    """The C entry, so that dlogp may be any buffer."""
+    pairs = at.numel() // 2
+    loss, reward = torch.zeros(pairs, device="cuda"), torch.zeros(pairs, 2, device="cuda")
+    s = torch.cuda.current_stream().cuda_stream
+    status = ss.lib().ss_preference_loss(
+        logp.data_ptr(), None, None, at.data_ptr(), pairs, logp.numel(), 0, 0.1, 0.0, 0, 1.0,
+        loss.data_ptr(), reward.data_ptr(), dlogp.data_ptr(), ws.data_ptr(), ws.numel(), s)
+    assert status == 0
+    torch.cuda.synchronize()
+    return loss, reward
+
+
+# offsets in, the pairs that are bad and those that are good
+BAD = {"before all": ([40000, 4, 900, 20000, 39000], [0], [1]),
+       "above": ([0, 40001, 900, 20000, 39000], [0], [1]),
+       "negative": ([-5, 900, 1000, 20000, 39000], [0], [1]),
+       "falling": ([900, 1000, 800, 20000, 39000], [0], [1]),
+       "last below": ([0, 900, 30000, 39000, 3], [1], [0]),
+       "last negative": ([0, 900, 30000, 39000, -3], [1], [0]),
+       "last above": ([0, 900, 30000, 39000, 2 ** 31 - 1], [1], [0]),
+       "between": ([0, 900, 9000, 8000, 9500, 20000, 39000], [1], [0, 2])}
+
+
+@pytest.mark.parametrize("offsets,bad,good", BAD.values(), ids=BAD.keys())
+@pytest.mark.parametrize("in_place", [False, True])
+def test_preference_other_pairs_beside_a_bad_one(offsets, bad, good, in_place):
+    """The good pairs' losses, rewards and gradients are there, with the gradient in the
+    place of the log-probabilities too, and nothing is written around it."""
+    n, guard = 40000, 64
+    logp = -torch.rand(n, generator=_gen(7), device="cuda")
+    at = torch.tensor(offsets, dtype=I32, device="cuda")
+    own = logp.clone()
+    for _ in range(10):
+        buffer = torch.full((n + 2 * guard,), 7.0, device="cuda")
+        dlogp = buffer[guard:guard + n]
+        dlogp.copy_(logp)
+        ws = ss.logprob_workspace(0, 1, 64)
+        loss, reward = _preference_call(dlogp if in_place else logp, at, dlogp, ws)
+        assert ss.read_status(ws)[0] == 8
+        assert (buffer[:guard] == 7).all() and (buffer[guard + n:] == 7).all()
+        assert torch.equal(logp, own)
+        for i in bad:
+            assert loss[i].isnan() and reward[i].isnan().all()
+        for i in good:
+            part = at[2 * i:2 * i + 3]
+            want = preference64(logp, part, beta=torch.tensor(0.1).item())
+            assert_within(loss[i:i + 1], want["loss"], "loss")
+            assert_within(reward[i:i + 1], want["reward"], "reward")
+            a, b = offsets[2 * i], offsets[2 * i + 2]
+            assert_within(dlogp[a:b], tuple(t[a:b] for t in want["dlogp"]), "dlogp")
