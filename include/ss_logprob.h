@@ -33,7 +33,9 @@ extern "C" {
  * 16-byte aligned, the first 1024 bytes (the header of ss.h, with the status
  * word) zero when new. Limits: 0 <= T < 2^31; 1 <= V <= SS_MAX_V; D % 64 == 0,
  * 64 <= D <= SS_MAX_D (SS_ERR_UNSUPPORTED, or SS_ERR_INVALID for values that can
- * never be valid).
+ * never be valid). With backward it holds the T x V matrix G in bf16, 2 T V bytes (1.65 GB
+ * at T 16384, V 50304), which is most of it; accumulate takes a longer batch in parts.
+ * Without, 8 bytes a token and 128 rows of the vocabulary, and 1 KB a token for its ids.
  * Nothing in it outlives a call but the status word, so one workspace serves
  * any number of batches in any order; calls that may run at the same time need
  * one each (two captured graphs that are replayed at the same time too). Errors
@@ -49,7 +51,10 @@ size_t ss_logprob_workspace_size(int64_t T, int64_t V, int64_t D, int backward);
  *   z = H W^T (with head->cap > 0: z = cap / (1 + exp(-H W^T / tau)))
  *   lse[t] = log sum_j exp(z[t, j])
  *   logp[t, k] = z[t, ids[t, k]] - lse[t]; 0 where ids[t, k] is -1 (absent)
- * The T x V logits never reach device memory.
+ * The T x V logits never reach device memory. From three tokens on their sums are a
+ * tensor core's, which truncates: with logits of standard deviation 3 every lse is some
+ * 3e-6 too small, and so logp as much too large for ids that are not drawn from the model
+ * (for those that are, their own logit's truncation cancels it).
  *   H [T, D], W [V, D] bf16; ids [T, K] int32, 1 <= K <= SS_MAX_IDS, each in
  *   [-1, V); an id may come more than once in a row.
  *   head: NULL (plain) or cap and tau as for ss_forward_head; no FP8
@@ -72,7 +77,10 @@ ss_status ss_logprob_forward(const uint16_t* H, const uint16_t* W, const int32_t
  *   G[t, j] = (a[t] exp(z[t, j] - lse[t]) + sum_k w[t, k] [ids[t, k] = j]) dz/ds
  *   dH = G W      dW = G^T H
  * The logits are computed again from H, W and lse; G is rounded once to bf16
- * for the two products, whose sums are held in fp32.
+ * for the two products, whose sums are held in fp32. With K = 1 a factor of each row
+ * of G goes to H's row for dW instead, which is then rounded to bf16 once more where
+ * that factor is no power of two. (dH and dW, as bf16: 1.8e-3 to 2.4e-3 of their norm
+ * off, of which their own rounding is 1.7e-3.)
  *   dlogp [T, K] fp32; H, W, ids, logp, lse, head: as in the forward, but for a
  *   cap below 2^-6 (SS_ERR_UNSUPPORTED): the ids' z, from which their dz/ds is made,
  *   is logp + lse here and has no digits left beside so small a cap.

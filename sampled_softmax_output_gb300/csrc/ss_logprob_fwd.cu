@@ -13,9 +13,11 @@
 // nearest, 128 columns of a row per thread: 2.9e-6 too small, whatever D.
 //
 // The chosen ids' logits are taken from those registers too: what truncation is
-// left then falls on both terms of the difference alike (log-probabilities of tokens
-// drawn from the model are 1.3e-6 off either way, with no shift), and no row of W is
-// read again (16384 tokens of 64 ids: gathered rows took 228 us). k_bin_ids sorts the
+// left then falls on both terms of the difference alike for tokens drawn from the model
+// (1.3e-6 off either way, with no shift); for ids that are not, whose logits are smaller,
+// the log-sum-exp's shift stays (ids drawn uniformly: logp 2.7e-6 too large at V 50257,
+// D 1088, where plain fp32 products are 1.1e-6 off either way). And no row of W is read
+// again (16384 tokens of 64 ids: gathered rows took 228 us). k_bin_ids sorts the
 // ids of each 32 tokens by the 128 columns they fall into; a warp, which holds those
 // columns of those tokens, looks up the few that are its own.
 //
@@ -452,16 +454,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         f32x2_split(s1, a2, a3);
         s = (a0 + a1) + (a2 + a3);
         // What shifts every token's sum the same way, and so adds up over a sequence:
-        // kLog2e is 1.93e-8 above log2(e), so that exp(z) came out as exp(z (1 + 1.3e-8))
-        // (1.2e-7 of it where z is 9), which is taken off at the mean of z log2(e), some
-        // 3.6 below the logarithm of the sum; and the hardware's exponential is 5.0e-8 too
+        // kLog2e is 1.93e-8 below log2(e), so that exp(z) came out as exp(z (1 - 1.3e-8))
+        // (1.2e-7 less where z is 9), which is put back at the mean of z log2(e). That mean
+        // is the logarithm of the sum less the entropy of the 128 columns in bits, which is
+        // taken as 3.6, what logits of standard deviation 3 have; it is 0 to 7, and the
+        // difference worth 3.4e-8 at most. And the hardware's exponential is 5.0e-8 too
         // small on average (a million points). Log-probabilities of tokens drawn from the
         // model are then off by 1e-8 on average, 9e-7 with neither this nor integers as
         // the exponents (a cap of 30).
-        constexpr float kOver = static_cast<float>((double(kLog2e) - kLog2eExact) /
-                                                   (kLog2eExact * kLog2eExact));
+        constexpr float kUnder = static_cast<float>((kLog2eExact - double(kLog2e)) /
+                                                    (kLog2eExact * kLog2eExact));
         const float mean = fmaxf(r2 + __log2f(s) - 3.6f, -1e6f);  // (s can be 0)
-        s = fmaf(s, fmaf(-kOver, mean, 5.0e-8f), s);
+        s = fmaf(s, fmaf(kUnder, mean, 5.0e-8f), s);
       }
       if (t < p.T)
         p.part[static_cast<size_t>(nt * 2 + cg) * p.T + t] = make_float2(fminf(m, kMostExponent), s);

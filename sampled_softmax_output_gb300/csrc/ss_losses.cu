@@ -99,7 +99,7 @@ __device__ __forceinline__ PolicyOut policy_token(const PolicyArgs& p, float log
 
 // Memory-bound: 20 bytes read and 12 written a token (with a reference and weights);
 // four tokens a thread, 16 bytes an access, where the pointers allow, else one. 2^24
-// tokens in 91 us, 5.9 TB/s of the copy's 6.8; two groups a thread, or fewer blocks that
+// tokens in 92 us, 5.9 TB/s of the copy's 6.8; two groups a thread, or fewer blocks that
 // walk the data, take 93 to 96.
 template <bool VEC>
 __global__ void __launch_bounds__(256) k_policy_loss(const PolicyArgs p) {
@@ -467,7 +467,7 @@ struct Entries {
 };
 
 // A token's K entries over LANES lanes, four a lane. The instructions bound it, not the
-// 14 bytes an entry: 65536 tokens of K 128 in 29 us, 40 with a tail (3.4 of 4 possible
+// 14 bytes an entry: 65536 tokens of K 128 in 26 us, 40 with a tail (3.4 of 4 possible
 // instructions a cycle, most of them the exponentials'), where a copy of as many bytes
 // takes 17. Two or four times as many entries a lane, which halve the steps of each
 // sum over lanes, take registers that cost more (36 and 39 us without a tail); the
